@@ -75,6 +75,7 @@ STATIC_SCRATCH_BYTES = 16777216
 ROUTE_AUTO, ROUTE_BY_COLUMN, ROUTE_BY_EXPERT = 0, 1, 2
 
 _i64, _vp, _int, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_f32 = ctypes.c_float
 _szp = ctypes.POINTER(_sz)
 _SIGS = {
     "q4_0_blocks_bytes": (_sz, [_i64, _i64]),
@@ -105,6 +106,14 @@ _SIGS = {
                                      _int, _vp, _sz, _vp]),
     "q4_0_select_route": (_int, [_i64, _i64, _i64, _i64, _i64]),
     "q4_0_routed_workspace_size": (_int, [_i64, _i64, _i64, _i64, _i64, _int, _szp]),
+    "q4_0_kv_append": (_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _int, _i64,
+                              _vp, _vp, _i64, _vp]),
+    "q4_0_attention": (_int, [_vp, _vp, _i64, _int, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
+                              _i64, _i64, _f32, _vp, _sz, _vp]),
+    "q4_0_attention_workspace_size": (_int, [_vp, _i64, _int, _i64, _i64, _i64, _i64, _i64,
+                                             _szp]),
+    "q4_0_residual_norm": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _i64,
+                                  _vp, _f32, _f32, _vp, _int, _i64, _i64, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -331,6 +340,60 @@ def q4_0_stream_read(src, nbytes: int, sink, workgroups: int, stream=None) -> No
                                  _stream(stream, sink)), "q4_0_stream_read")
 
 
+class q4_0_kv_cache(ctypes.Structure):
+    """A paged cache's descriptor (struct q4_0_kv_cache of include/q4_0.h)."""
+    _fields_ = [("k", _vp), ("v", _vp), ("pages", _i64), ("heads", _i64), ("page_size", _i64),
+                ("dim", _i64)]
+
+
+class q4_0_rotary(ctypes.Structure):
+    """Position rotation and per-head norms (struct q4_0_rotary of include/q4_0.h)."""
+    _fields_ = [("inv_freq", _vp), ("rot_dim", _i64), ("interleaved", _int),
+                ("amplitude", _f32), ("q_norm", _vp), ("k_norm", _vp), ("eps", _f32),
+                ("weight_offset", _f32)]
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def q4_0_kv_append(cache, rot, q, q_stride: int, k, k_stride: int, v, v_stride: int,
+                   x_dtype: int, q_out, q_dtype: int, q_heads: int, positions, slots, n: int,
+                   stream=None) -> None:
+    """cache: q4_0_kv_cache; rot: q4_0_rotary or None."""
+    _check(_lib.q4_0_kv_append(_ref(cache), _ref(rot), _ptr(q), q_stride, _ptr(k), k_stride,
+                               _ptr(v), v_stride, x_dtype, _ptr(q_out), q_dtype, q_heads,
+                               _ptr(positions), _ptr(slots), n, _stream(stream, k, v)),
+           "q4_0_kv_append")
+
+
+def q4_0_attention(cache, q, q_stride: int, x_dtype: int, q_heads: int, y, n: int, q_start,
+                   kv_len, table, table_stride: int, batch: int, window: int, sinks: int,
+                   scale: float, workspace=None, workspace_bytes=None, stream=None) -> None:
+    """cache: q4_0_kv_cache."""
+    _check(_lib.q4_0_attention(_ref(cache), _ptr(q), q_stride, x_dtype, q_heads, _ptr(y), n,
+                               _ptr(q_start), _ptr(kv_len), _ptr(table), table_stride, batch,
+                               window, sinks, scale, _ptr(workspace),
+                               _nbytes(workspace, workspace_bytes), _stream(stream, q, y)),
+           "q4_0_attention")
+
+
+def q4_0_attention_workspace_size(cache, q_heads: int, x_dtype: int, n: int, table_stride: int,
+                                  batch: int, window: int = 0, sinks: int = 0) -> int:
+    return _size(_lib.q4_0_attention_workspace_size, "q4_0_attention_workspace_size",
+                 _ref(cache), q_heads, x_dtype, n, table_stride, batch, window, sinks)
+
+
+def q4_0_residual_norm(b, b_dtype: int, b_stride: int, post, gate, gate_row: int, gate_col: int,
+                       alpha: float, h, h_out, h_stride: int, pre, weight_offset: float,
+                       eps: float, y, y_dtype: int, y_stride: int, n: int, dim: int,
+                       stream=None) -> None:
+    _check(_lib.q4_0_residual_norm(_ptr(b), b_dtype, b_stride, _ptr(post), _ptr(gate), gate_row,
+                                   gate_col, alpha, _ptr(h), _ptr(h_out), h_stride, _ptr(pre),
+                                   weight_offset, eps, _ptr(y), y_dtype, y_stride, n, dim,
+                                   _stream(stream, h, y)), "q4_0_residual_norm")
+
+
 # ---- torch conveniences (allocation through torch, then the C calls above) --
 def dtype_code(x) -> int:
     """Q4_0_F32 or Q4_0_F16 for a torch tensor's dtype."""
@@ -431,3 +494,160 @@ def matmul_routed(experts, n_experts: int, x, route, out: int, y=None, stream=No
     q4_0_matmul_routed_ex(experts, n_experts, x, dtype_code(x), route, k, y, n, out, in_,
                           route_kernel, ws, None, stream)
     return y
+
+
+def _typed(t, name: str, dtype, *shape):
+    """t's checks before its address goes to the library: type, shape (None:
+    any size) and dense rows."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if len(t.shape) != len(shape) or any(s is not None and s != g
+                                         for s, g in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name: str, n: int, width=None):
+    """(row width, row stride) of [n, ...] rows: dense within a row, any
+    distance between rows."""
+    if t.dim() == 3:
+        heads, dim = t.shape[1:]
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+            raise ValueError(f"{name}'s rows must be dense")
+        w = heads * dim
+    elif t.dim() == 2:
+        w = t.shape[1]
+        if w > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}'s rows must be dense")
+    else:
+        raise ValueError(f"{name} must have two or three dimensions")
+    if t.shape[0] != n or (width is not None and w != width):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not fit the call")
+    return w, t.stride(0) if n > 1 else w
+
+
+def kv_cache(k, v):
+    """Descriptor of a paged cache: k and v float16 [pages, heads, page_size,
+    dim] CUDA tensors.  It holds their addresses: keep the tensors alive."""
+    import torch
+    _typed(k, "k", torch.float16, None, None, None, None)
+    _typed(v, "v", torch.float16, *k.shape)
+    pages, heads, page_size, dim = k.shape
+    return q4_0_kv_cache(k.data_ptr(), v.data_ptr(), pages, heads, page_size, dim)
+
+
+def rotary(inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q_norm=None,
+           k_norm=None, eps: float = 1e-6, weight_offset: float = 0.0):
+    """Descriptor of a rotation (inv_freq: float32 [rot_dim / 2], or None) and of
+    per-head norms (float32 [dim] weights, or None).  It holds the tensors'
+    addresses: keep them alive."""
+    import torch
+    for t, name in ((inv_freq, "inv_freq"), (q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _typed(t, name, torch.float32, None)
+    return q4_0_rotary(_ptr(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(),
+                       int(interleaved), amplitude, _ptr(q_norm), _ptr(k_norm), eps,
+                       weight_offset)
+
+
+def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
+    """Append k and v to `cache` and rotate q: q [n, q_heads * dim] (or None), k
+    and v [n, heads * dim], or the same with the heads as a dimension; rows may
+    be slices of wider ones.  positions int32 [n], slots int64 [n].  Returns the
+    rotated q [n, q_heads, dim]: q_out, or a new tensor of q's type."""
+    import torch
+    n, dim = k.shape[0], cache.dim
+    kw, ks = _rows(k, "k", n, cache.heads * dim)
+    _, vs = _rows(v, "v", n, kw)
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must have one type")
+    _typed(slots, "slots", torch.int64, n)
+    if positions is not None:
+        _typed(positions, "positions", torch.int32, n)
+    code, qs, heads, qcode = dtype_code(k), 0, 0, 0
+    if q is not None:
+        qw, qs = _rows(q, "q", n)
+        heads = qw // dim
+        if qw % dim:
+            raise ValueError(f"q's rows of {qw} are no whole heads of {dim}")
+        if q_out is None:
+            q_out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
+        qcode = dtype_code(q_out)
+        _typed(q_out, "q_out", q_out.dtype, n, heads, dim)
+    q4_0_kv_append(cache, rot, q, qs, k, ks, v, vs, code, q_out, qcode, heads, positions, slots,
+                   n, stream)
+    return q_out
+
+
+def attention(cache, q, q_start, kv_len, table, window: int = 0, sinks: int = 0, scale=None,
+              y=None, stream=None, ws=None):
+    """Attention of q [n, q_heads, dim] over `cache` (q4_0_attention): q_start
+    int32 [batch + 1], kv_len int32 [batch], table int32 [batch, pages of the
+    longest].  scale: dim ** -0.5 unless given.  Returns y, like q."""
+    import torch
+    n, heads, dim = q.shape
+    if dim != cache.dim:
+        raise ValueError(f"q's heads of {dim} do not fit the cache's {cache.dim}")
+    code = dtype_code(q)
+    _, qs = _rows(q, "q", n)
+    batch = kv_len.shape[0]
+    _typed(kv_len, "kv_len", torch.int32, batch)
+    _typed(q_start, "q_start", torch.int32, batch + 1)
+    _typed(table, "table", torch.int32, batch, None)
+    if y is None:
+        y = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
+    else:
+        _typed(y, "y", q.dtype, n, heads, dim)
+    width = table.shape[1]
+    if ws is None:
+        ws = workspace(q4_0_attention_workspace_size(cache, heads, code, n, width, batch, window,
+                                                     sinks), q.device)
+    q4_0_attention(cache, q, qs, code, heads, y, n, q_start, kv_len, table, width, batch, window,
+                   sinks, dim ** -0.5 if scale is None else scale, ws, None, stream)
+    return y
+
+
+def residual_norm(h, b=None, pre=None, post=None, gate=None, alpha: float = 1.0,
+                  eps: float = 1e-6, weight_offset: float = 0.0, h_out=None, y=None,
+                  y_dtype=None, stream=None):
+    """h_out = h + alpha * gate * N(b; post) and y = N(h_out; pre)
+    (q4_0_residual_norm) for h float32 [n, dim] and b [n, dim] float32 or
+    float16.  gate float32 [n, dim], [n, 1] or [1, dim]; post, pre float32
+    [dim] or None (no norm).  Without b, y = N(h; pre).  Returns (h_out, y):
+    as given, or new tensors (y of y_dtype, float32 unless given; None without
+    pre).  h_out may be h."""
+    import torch
+    n, dim = h.shape
+    if h.dtype != torch.float32:
+        raise TypeError(f"h must be float32, not {h.dtype}")
+    _, hs = _rows(h, "h", n)
+    bs = bcode = ys = ycode = grow = gcol = 0
+    if b is not None:
+        _, bs = _rows(b, "b", n, dim)
+        bcode = dtype_code(b)
+        if h_out is None:
+            h_out = torch.empty_strided((n, dim), (hs, 1), dtype=torch.float32, device=h.device)
+        elif h_out.dtype != torch.float32 or _rows(h_out, "h_out", n, dim)[1] != hs:
+            raise ValueError("h_out must be float32 with h's row stride")
+        if gate is not None:
+            if gate.dtype != torch.float32 or gate.dim() != 2 \
+                    or gate.shape[0] not in (1, n) or gate.shape[1] not in (1, dim):
+                raise ValueError("gate must be float32 [n, dim], [n, 1] or [1, dim]")
+            grow = gate.stride(0) if gate.shape[0] > 1 else 0
+            gcol = gate.stride(1) if gate.shape[1] > 1 else 0
+    else:
+        h_out = h
+    if pre is not None:
+        _typed(pre, "pre", torch.float32, dim)
+        if y is None:
+            y = torch.empty((n, dim), dtype=y_dtype or torch.float32, device=h.device)
+        _, ys = _rows(y, "y", n, dim)
+        ycode = dtype_code(y)
+    else:
+        y = None
+    if post is not None:
+        _typed(post, "post", torch.float32, dim)
+    q4_0_residual_norm(b, bcode, bs, post, gate, grow, gcol, alpha, h, h_out, hs, pre,
+                       weight_offset, eps, y, ycode, ys, n, dim, stream)
+    return h_out, y

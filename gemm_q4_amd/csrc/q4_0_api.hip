@@ -2,6 +2,8 @@
 // choice, workspace sizes, launches.  Every check runs on the host before any
 // HIP call, so an invalid call enqueues nothing and is testable without a
 // GPU.  The library owns no device memory: scratch comes from the caller.
+#include <math.h>
+
 #include <mutex>
 
 #include "q4_0.h"
@@ -278,6 +280,86 @@ size_t routed_workspace(int form, int64_t n, int64_t k, int64_t n_experts, int64
     return form == Q4_0_ROUTE_BY_COLUMN
                ? q4::gemv_mfma_routed_workspace_bytes(n * k, out, in)
                : q4::gemv_mfma_by_expert_workspace_bytes(n, k, n_experts, out, in);
+}
+
+// Checks of a cache descriptor (host) and the kernels' view of it.
+int check_cache(const q4_0_kv_cache *c, bool pointers) {
+    if (!c) return Q4_0_ENULL;
+    if (c->pages < 1 || c->pages > INT32_MAX || c->heads < 1 || c->heads > 1024)
+        return Q4_0_ESHAPE;
+    if (c->dim < 8 || c->dim > 512 || c->dim % 8 != 0) return Q4_0_ESHAPE;
+    if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0)
+        return Q4_0_ESHAPE;
+    // at most 2^10 heads x 2^16 x 2^9 x 2 bytes a page, so the product below
+    // cannot overflow once pages is checked against it
+    const int64_t page = c->heads * c->page_size * c->dim * 2;
+    if (c->pages > (INT64_C(1) << 62) / page) return Q4_0_ESHAPE;
+    if (!pointers) return Q4_0_OK;
+    if (!c->k || !c->v) return Q4_0_ENULL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return Q4_0_EALIGN;
+    const size_t bytes = (size_t)c->pages * (size_t)page;
+    if (overlaps(c->k, bytes, c->v, bytes)) return Q4_0_EALIAS;
+    return Q4_0_OK;
+}
+
+size_t cache_bytes(const q4_0_kv_cache *c) {
+    return (size_t)c->pages * (size_t)(c->heads * c->page_size * c->dim * 2);
+}
+
+q4::KvCache cache_view(const q4_0_kv_cache *c) {
+    int shift = 0;
+    while ((INT64_C(1) << shift) < c->page_size) ++shift;
+    return {(_Float16 *)c->k, (_Float16 *)c->v, c->pages, (int)c->heads, shift, (int)c->dim};
+}
+
+// Largest row stride (elements) accepted: rows, strides and sizes of a call
+// then stay far below 2^63 bytes.
+constexpr int64_t kMaxStride = INT64_C(1) << 40;
+
+// Bytes from the first element of n rows of `width` elements, `stride`
+// elements apart, to the end of the last.
+size_t rows_bytes(int64_t n, int64_t stride, int64_t width, int64_t el) {
+    return (size_t)((n - 1) * stride + width) * (size_t)el;
+}
+
+// Whether an output overlaps any of the call's inputs or a later output.
+bool outputs_clash(const Span *outs, int nouts, const Span *ins, int nins) {
+    for (int i = 0; i < nouts; ++i) {
+        for (int j = 0; j < nins; ++j)
+            if (overlaps(outs[i].p, outs[i].len, ins[j].p, ins[j].len)) return true;
+        for (int j = i + 1; j < nouts; ++j)
+            if (overlaps(outs[i].p, outs[i].len, outs[j].p, outs[j].len)) return true;
+    }
+    return false;
+}
+
+// Shape checks shared by q4_0_attention and its workspace query.
+int check_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, int64_t n,
+                    int64_t table_stride, int64_t batch, int64_t window, int64_t sinks,
+                    bool pointers) {
+    const int st = check_cache(cache, pointers);
+    if (st != Q4_0_OK) return st;
+    if (n < 1 || n > Q4_0_MAX_N || batch < 1 || batch > Q4_0_MAX_N) return Q4_0_ESHAPE;
+    if (q_heads < 1 || q_heads > 1024 || q_heads % cache->heads != 0) return Q4_0_ESHAPE;
+    if (table_stride < 1 || table_stride > INT32_MAX / cache->page_size) return Q4_0_ESHAPE;
+    if (window < 0 || window > INT32_MAX || sinks < 0 || sinks > INT32_MAX) return Q4_0_EINVAL;
+    if (!valid_dtype(x_dtype)) return Q4_0_EINVAL;
+    if (!q4::attention_supports((int)cache->dim)) return Q4_0_EUNSUPPORTED;
+    return Q4_0_OK;
+}
+
+q4::AttentionArgs attention_args(const q4_0_kv_cache *cache, int64_t q_heads, int64_t n,
+                                 int64_t table_stride, int64_t batch, int64_t window,
+                                 int64_t sinks) {
+    q4::AttentionArgs a = {};
+    a.cache = cache_view(cache);
+    a.q_heads = (int)q_heads;
+    a.n = (int)n;
+    a.batch = (int)batch;
+    a.table_stride = (int)table_stride;
+    a.window = (int)window;
+    a.sinks = window ? (int)sinks : 0;
+    return a;
 }
 
 }  // namespace
@@ -590,6 +672,155 @@ int q4_0_matmul_grouped(const q4_0_linear *linears, int count, int x_dtype, int6
         if (st != Q4_0_OK) return st;
     }
     return Q4_0_OK;
+}
+
+int q4_0_kv_append(const q4_0_kv_cache *cache, const q4_0_rotary *rot, const void *q,
+                   int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, int x_dtype, void *q_out, int q_dtype, int64_t q_heads,
+                   const int32_t *positions, const int64_t *slots, int64_t n, void *stream) {
+    const int st = check_cache(cache, true);
+    if (st != Q4_0_OK) return st;
+    const int64_t dim = cache->dim;
+    if (n < 1 || n > Q4_0_MAX_N) return Q4_0_ESHAPE;
+    if (!valid_dtype(x_dtype)) return Q4_0_EINVAL;
+    if (q && (q_heads < 1 || q_heads > 1024)) return Q4_0_ESHAPE;
+    if (q && !valid_dtype(q_dtype)) return Q4_0_EINVAL;
+    if (rot && (rot->rot_dim < 0 || rot->rot_dim > dim || rot->rot_dim % 8 != 0))
+        return Q4_0_ESHAPE;
+    const int64_t kw = cache->heads * dim, qw = q ? q_heads * dim : 0;
+    if (k_stride < kw || v_stride < kw || k_stride > kMaxStride || v_stride > kMaxStride ||
+        (q && (q_stride < qw || q_stride > kMaxStride)))
+        return Q4_0_ESHAPE;
+    if (!k || !v || !slots || (q && !q_out)) return Q4_0_ENULL;
+    const bool rotates = rot && rot->rot_dim > 0;
+    if (rotates && (!rot->inv_freq || !positions)) return Q4_0_ENULL;
+    const int64_t el = elem_bytes(x_dtype);
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride * el % 16 || v_stride * el % 16 ||
+        !aligned(slots, 8) || !aligned(positions, 4))
+        return Q4_0_EALIGN;
+    if (q && (!aligned(q, 16) || q_stride * el % 16 || !aligned(q_out, 16))) return Q4_0_EALIGN;
+    if (rot && (!aligned(rot->inv_freq, 4) || !aligned(rot->q_norm, 16) ||
+                !aligned(rot->k_norm, 16)))
+        return Q4_0_EALIGN;
+    const size_t norm_bytes = (size_t)dim * 4u;
+    const Span ins[8] = {
+        {k, rows_bytes(n, k_stride, kw, el)},
+        {v, rows_bytes(n, v_stride, kw, el)},
+        {q, q ? rows_bytes(n, q_stride, qw, el) : 0},
+        {rotates ? positions : nullptr, (size_t)n * 4u},
+        {slots, (size_t)n * 8u},
+        {rotates ? rot->inv_freq : nullptr, rotates ? (size_t)rot->rot_dim * 2u : 0},
+        {rot ? rot->q_norm : nullptr, norm_bytes},
+        {rot ? rot->k_norm : nullptr, norm_bytes}};
+    const Span outs[3] = {{cache->k, cache_bytes(cache)},
+                          {cache->v, cache_bytes(cache)},
+                          {q ? q_out : nullptr,
+                           q ? (size_t)(n * qw) * (size_t)elem_bytes(q_dtype) : 0}};
+    if (outputs_clash(outs, 3, ins, 8)) return Q4_0_EALIAS;
+    q4::AppendArgs a = {};
+    a.cache = cache_view(cache);
+    a.q = q, a.k = k, a.v = v;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.q_out = q_out;
+    a.q_heads = q ? (int)q_heads : 0;
+    a.positions = positions, a.slots = slots, a.n = n;
+    if (rot) {
+        a.inv_freq = rot->inv_freq, a.q_norm = rot->q_norm, a.k_norm = rot->k_norm;
+        a.rot_dim = (int)rot->rot_dim, a.interleaved = rot->interleaved != 0;
+        a.amplitude = rot->amplitude, a.eps = rot->eps, a.weight_offset = rot->weight_offset;
+    }
+    return map_hip(q4::launch_kv_append(a, x_dtype == Q4_0_F16, q && q_dtype == Q4_0_F16,
+                                        (hipStream_t)stream));
+}
+
+int q4_0_attention_workspace_size(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype,
+                                  int64_t n, int64_t table_stride, int64_t batch,
+                                  int64_t window, int64_t sinks, size_t *bytes) {
+    if (!bytes) return Q4_0_ENULL;
+    const int st =
+        check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks, false);
+    if (st != Q4_0_OK) return st;
+    *bytes = q4::attention_workspace_bytes(
+        attention_args(cache, q_heads, n, table_stride, batch, window, sinks),
+        x_dtype == Q4_0_F16);
+    return Q4_0_OK;
+}
+
+int q4_0_attention(const q4_0_kv_cache *cache, const void *q, int64_t q_stride, int x_dtype,
+                   int64_t q_heads, void *y, int64_t n, const int32_t *q_start,
+                   const int32_t *kv_len, const int32_t *table, int64_t table_stride,
+                   int64_t batch, int64_t window, int64_t sinks, float scale, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    const int st =
+        check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks, true);
+    if (st != Q4_0_OK) return st;
+    if (!(scale > 0.0f) || !isfinite(scale)) return Q4_0_EINVAL;
+    const int64_t qw = q_heads * cache->dim, el = elem_bytes(x_dtype);
+    if (q_stride < qw || q_stride > kMaxStride) return Q4_0_ESHAPE;
+    if (!q || !y || !q_start || !kv_len || !table) return Q4_0_ENULL;
+    if (!aligned(q, 16) || q_stride * el % 16 || !aligned(y, 16) || !aligned(q_start, 4) ||
+        !aligned(kv_len, 4) || !aligned(table, 4))
+        return Q4_0_EALIGN;
+    const Span spans[7] = {{cache->k, cache_bytes(cache)},
+                           {cache->v, cache_bytes(cache)},
+                           {q, rows_bytes(n, q_stride, qw, el)},
+                           {q_start, (size_t)(batch + 1) * 4u},
+                           {kv_len, (size_t)batch * 4u},
+                           {table, (size_t)(batch * table_stride) * 4u},
+                           {y, (size_t)(n * qw) * (size_t)el}};
+    if (outputs_clash(spans + 6, 1, spans, 6)) return Q4_0_EALIAS;
+    q4::AttentionArgs a = attention_args(cache, q_heads, n, table_stride, batch, window, sinks);
+    a.q = q, a.q_stride = q_stride, a.y = y;
+    a.q_start = q_start, a.kv_len = kv_len, a.table = table;
+    a.scale = scale;
+    const int f16 = x_dtype == Q4_0_F16;
+    const int wst = check_workspace(workspace, workspace_bytes,
+                                    q4::attention_workspace_bytes(a, f16), spans, 7);
+    if (wst != Q4_0_OK) return wst;
+    return map_hip(q4::launch_attention(a, f16, workspace, (hipStream_t)stream));
+}
+
+int q4_0_residual_norm(const void *b, int b_dtype, int64_t b_stride, const float *post,
+                       const float *gate, int64_t gate_row, int64_t gate_col, float alpha,
+                       const float *h, float *h_out, int64_t h_stride, const float *pre,
+                       float weight_offset, float eps, void *y, int y_dtype, int64_t y_stride,
+                       int64_t n, int64_t dim, void *stream) {
+    if (n < 1 || n > Q4_0_MAX_N || dim < 1) return Q4_0_ESHAPE;
+    if (dim > q4::kNormMaxDim) return Q4_0_EUNSUPPORTED;
+    if (!b && !y) return Q4_0_ENULL;
+    if (b && !valid_dtype(b_dtype)) return Q4_0_EINVAL;
+    if (y && !valid_dtype(y_dtype)) return Q4_0_EINVAL;
+    if (b && gate && (gate_col < 0 || gate_col > 1 || gate_row < 0 || gate_row > kMaxStride))
+        return Q4_0_EINVAL;
+    if ((b && (b_stride < dim || b_stride > kMaxStride)) || h_stride < dim ||
+        h_stride > kMaxStride || (y && (y_stride < dim || y_stride > kMaxStride)))
+        return Q4_0_ESHAPE;
+    if (!h || (b && !h_out) || (y && !pre)) return Q4_0_ENULL;
+    const int64_t bel = b ? elem_bytes(b_dtype) : 4, yel = y ? elem_bytes(y_dtype) : 4;
+    if (!aligned(h, 4) || (b && (!aligned(b, bel) || !aligned(h_out, 4) || !aligned(post, 4) ||
+                                 !aligned(gate, 4))) ||
+        (y && (!aligned(y, yel) || !aligned(pre, 4))))
+        return Q4_0_EALIGN;
+    const size_t hbytes = rows_bytes(n, h_stride, dim, 4), wbytes = (size_t)dim * 4u;
+    const bool in_place = b && h_out == h;
+    const Span ins[5] = {
+        {b, b ? rows_bytes(n, b_stride, dim, bel) : 0},
+        {b ? post : nullptr, wbytes},
+        {b ? gate : nullptr,
+         b && gate ? (size_t)((n - 1) * gate_row + (dim - 1) * gate_col + 1) * 4u : 0},
+        {y ? pre : nullptr, wbytes},
+        {in_place ? nullptr : h, hbytes}};
+    const Span outs[2] = {{b ? h_out : nullptr, hbytes},
+                          {y, y ? rows_bytes(n, y_stride, dim, yel) : 0}};
+    if (outputs_clash(outs, 2, ins, 5)) return Q4_0_EALIAS;
+    q4::NormArgs a = {};
+    a.b = b, a.b_stride = b_stride, a.post = post, a.gate = gate;
+    a.gate_row = gate_row, a.gate_col = (int)gate_col, a.alpha = alpha;
+    a.h = h, a.h_out = h_out, a.h_stride = h_stride, a.pre = pre;
+    a.weight_offset = weight_offset, a.eps = eps;
+    a.y = y, a.y_stride = y_stride, a.n = n, a.dim = (int)dim;
+    return map_hip(q4::launch_residual_norm(a, b && b_dtype == Q4_0_F16,
+                                            y && y_dtype == Q4_0_F16, (hipStream_t)stream));
 }
 
 int q4_0_mfma_loop(float *sink, int64_t workgroups, int64_t iters, int64_t *flops,

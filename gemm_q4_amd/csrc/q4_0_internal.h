@@ -114,6 +114,60 @@ size_t gemm_workspace_bytes(int64_t n, int64_t out, int64_t in);
 hipError_t launch_gemm(const void *packed, const void *x, int x_f16, float *y,
                        int64_t n, int64_t out, int64_t in, void *ws, hipStream_t stream);
 
+// Operators between the products (include/q4_0.h documents the formulas).
+struct KvCache {
+    _Float16 *k, *v;
+    int64_t pages;
+    int heads, page_shift, dim;  // page_size == 1 << page_shift
+};
+struct AppendArgs {
+    KvCache cache;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements
+    void *q_out;
+    int q_heads;  // 0: no q
+    const int32_t *positions;
+    const int64_t *slots;
+    int64_t n;
+    const float *inv_freq, *q_norm, *k_norm;
+    int rot_dim, interleaved;
+    float amplitude, eps, weight_offset;
+};
+hipError_t launch_kv_append(const AppendArgs &a, int x_f16, int q_f16, hipStream_t stream);
+
+struct AttentionArgs {
+    KvCache cache;
+    const void *q;
+    int64_t q_stride;  // elements
+    void *y;
+    int q_heads, n, batch;
+    const int32_t *q_start, *kv_len, *table;
+    int table_stride, window, sinks;  // window 0: none
+    float scale;
+};
+bool attention_supports(int dim);
+size_t attention_workspace_bytes(const AttentionArgs &a, int x_f16);
+hipError_t launch_attention(const AttentionArgs &a, int x_f16, void *ws, hipStream_t stream);
+
+struct NormArgs {
+    const void *b;  // null: no block output
+    int64_t b_stride;
+    const float *post, *gate;
+    int64_t gate_row;
+    int gate_col;
+    float alpha;
+    const float *h;
+    float *h_out;
+    int64_t h_stride;
+    const float *pre;
+    float weight_offset, eps;
+    void *y;  // null: no second norm
+    int64_t y_stride, n;
+    int dim;
+};
+constexpr int64_t kNormMaxDim = 32768;
+hipError_t launch_residual_norm(const NormArgs &a, int b_f16, int y_f16, hipStream_t stream);
+
 // Measurement aids: back-to-back v_mfma_f32_32x32x16_f16 on every SIMD; a
 // plain streaming read of `bytes` bytes (an empty launch for 0).
 int64_t mfma_loop_flops(int64_t workgroups, int64_t iters);

@@ -323,6 +323,136 @@ int q4_0_matmul_w4a8(const void *packed, const int8_t *q, const float *d, float 
 /* Workspace bytes of q4_0_matmul_w4a8 into *bytes.  Host only. */
 int q4_0_w4a8_workspace_size(int64_t n, int64_t out, int64_t in, size_t *bytes);
 
+/* ---- between a decoder block's products ---------------------------------
+ * What a served block runs between its linears: the append of a pass's keys
+ * and values to a paged cache, attention over that cache, and the norms around
+ * each half of the block.  golem README "Several conversations, one pass": one
+ * pass carries the new positions of several conversations, each with its own
+ * length, so every call below takes a ragged batch, and what changes from pass
+ * to pass (positions, lengths, page tables) stays on the device: a captured
+ * graph of a decode step can be replayed as the conversations grow. */
+
+/* A paged key/value cache of one layer: K and V, each binary16
+ * [pages][heads][page_size][dim], dense, 16-byte aligned, not overlapping.
+ * The keys of one head on one page are one contiguous run, which is what
+ * attention streams.  A descriptor on the HOST; the caller owns the memory.
+ *   1 <= pages < 2^31, 1 <= heads <= 1024, dim % 8 == 0, 8 <= dim <= 512,
+ *   page_size a power of two, 16 <= page_size <= 65536, less than 2^62 bytes. */
+typedef struct q4_0_kv_cache {
+    void *k;
+    void *v;
+    int64_t pages, heads, page_size, dim;
+} q4_0_kv_cache;
+
+/* Position rotation and per-head norms of q and k (HOST descriptor).
+ *   norm, where the weights (DEVICE float32 [dim]) are given, per head row x:
+ *     x <- x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
+ *   rotation of the first rot_dim elements, pair i < rot_dim / 2:
+ *     angle = position * inv_freq[i]  (formed and reduced in 64 bits, so far
+ *                                      positions keep the accuracy of near ones)
+ *     (a, b) <- amplitude * (a cos - b sin, b cos + a sin)
+ *   where (a, b) = (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) when
+ *   `interleaved` is not 0.  Elements from rot_dim on pass unrotated.
+ *   inv_freq: DEVICE float32 [rot_dim/2]; rot_dim % 8 == 0, 0 <= rot_dim <=
+ *   dim (0: no rotation, inv_freq may be NULL). */
+typedef struct q4_0_rotary {
+    const float *inv_freq;
+    int64_t rot_dim;
+    int interleaved;
+    float amplitude;
+    const float *q_norm;
+    const float *k_norm;
+    float eps, weight_offset;
+} q4_0_rotary;
+
+/* Append n tokens' keys and values to the cache, norms and rotation on the
+ * way; q is rotated in the same launch.
+ *   rot       : HOST descriptor, or NULL (no norm, no rotation).
+ *   q, k, v   : DEVICE rows of q_heads * dim, heads * dim and heads * dim
+ *               elements of x_dtype, *_stride elements apart (so slices of one
+ *               fused product's rows can be passed as they are); bases and row
+ *               strides a multiple of 16 bytes.  q may be NULL (q_out and
+ *               q_heads are then ignored).
+ *   q_out     : DEVICE [n][q_heads][dim] of q_dtype, dense, 16-byte aligned.
+ *   positions : DEVICE int32 [n], the rotation's positions.
+ *   slots     : DEVICE int64 [n]: page * page_size + offset of each token's
+ *               cache row.  A slot outside [0, pages * page_size) writes no
+ *               cache row (a padded token: its q is still written).  Two tokens
+ *               with one slot leave either's row there.
+ * Sums and rotations in float32; K, V and a binary16 q_out are each rounded
+ * once.  1 <= n <= Q4_0_MAX_N, 1 <= q_heads <= 1024.  No output overlaps an
+ * input or another output (Q4_0_EALIAS).  Needs no workspace. */
+int q4_0_kv_append(const q4_0_kv_cache *cache, const q4_0_rotary *rot, const void *q,
+                   int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, int x_dtype, void *q_out, int q_dtype, int64_t q_heads,
+                   const int32_t *positions, const int64_t *slots, int64_t n, void *stream);
+
+/* Attention of a ragged batch over the paged cache:
+ *     y[t][h] = sum_j softmax_j(scale * q[t][h] . K[j]) V[j]
+ * over the cached keys j of token t's conversation that it sees, with K and V
+ * of key/value head h / (q_heads / heads).  Conversation s holds tokens
+ * q_start[s] .. q_start[s+1] - 1, the LAST of its kv_len[s] cached positions (so
+ * append first), and key j of it lives on page table[s][j / page_size], offset
+ * j % page_size.  The token at position p sees
+ *     j <= p                                      when window == 0,
+ *     j <= p and (j > p - window or j < sinks)    otherwise
+ * (a sliding window, and the first `sinks` positions that stay visible).  Pages
+ * no token of the call sees are never read: their table entries may hold
+ * anything.  A decode step is the batch with one token per conversation.
+ *   q       : DEVICE [n] rows of q_heads * dim elements of x_dtype, q_stride
+ *             elements apart; base and row stride a multiple of 16 bytes.
+ *   y       : DEVICE [n][q_heads][dim] of x_dtype, dense, 16-byte aligned.
+ *   q_start : DEVICE int32 [batch + 1], 0 <= q_start[s] <= q_start[s+1] <= n.
+ *             A token that no conversation holds keeps what y has.
+ *   kv_len  : DEVICE int32 [batch].  A token at a negative position (more new
+ *             tokens than kv_len) sees nothing: its y is 0.
+ *   table   : DEVICE int32 [batch][table_stride].  A row that sees a key on a
+ *             page outside [0, pages), or past the table's end, is NaN.
+ *   workspace, workspace_bytes : q4_0_attention_workspace_size gives the need
+ *             (partial results of a key axis split across workgroups).
+ * Binary16 x: products of binary16 values, each weight rounded to binary16
+ * before its product with V.  Float32 x: q and the weights as binary16 high
+ * and low parts (22 bits).  Scores, maxima and sums are float32 in both.
+ * K or V that a row does not see never change it, infinities and NaN included.
+ * dim 64, 128 or 256 (Q4_0_EUNSUPPORTED otherwise); q_heads a multiple of the
+ * cache's heads, at most 1024; 1 <= n <= Q4_0_MAX_N, 1 <= batch <= Q4_0_MAX_N;
+ * table_stride >= 1, table_stride * page_size < 2^31; window, sinks in
+ * [0, 2^31); scale positive and finite (Q4_0_EINVAL). */
+int q4_0_attention(const q4_0_kv_cache *cache, const void *q, int64_t q_stride, int x_dtype,
+                   int64_t q_heads, void *y, int64_t n, const int32_t *q_start,
+                   const int32_t *kv_len, const int32_t *table, int64_t table_stride,
+                   int64_t batch, int64_t window, int64_t sinks, float scale, void *workspace,
+                   size_t workspace_bytes, void *stream);
+/* Workspace bytes of q4_0_attention with these sizes into *bytes (only the
+ * cache's sizes are read).  Host only. */
+int q4_0_attention_workspace_size(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype,
+                                  int64_t n, int64_t table_stride, int64_t batch,
+                                  int64_t window, int64_t sinks, size_t *bytes);
+
+/* The residual step between two half blocks, with the norm after the one and
+ * the norm before the next:
+ *     h_out[t] = h[t] + alpha * g[t] * N(b[t]; post),   y[t] = N(h_out[t]; pre)
+ *     N(x; w)[i] = x[i] / sqrt(mean(x^2) + eps) * (w[i] + weight_offset)
+ *   b    : DEVICE [n] rows of dim elements of b_dtype, b_stride apart (a half
+ *          block's output), or NULL: y = N(h; pre) alone, h_out not written
+ *          and ignored.
+ *   post : DEVICE float32 [dim], or NULL: b enters without a norm.
+ *   gate : DEVICE float32, g[t][i] = gate[t * gate_row + i * gate_col], or NULL
+ *          (1).  gate_col 0 or 1; gate_row >= 0 (0: one row for all tokens).
+ *   h, h_out : DEVICE float32 rows, h_stride elements apart; h_out may be h
+ *          itself (in place), and overlaps nothing else.
+ *   y    : DEVICE rows of dim elements of y_dtype, y_stride apart, with
+ *          pre (DEVICE float32 [dim]); or NULL: no second norm, pre ignored.
+ * The residual stream and all sums are float32; a binary16 y is rounded once.
+ * Rows whose sizes, bases or strides are no multiple of 16 bytes are taken
+ * element by element.  1 <= n <= Q4_0_MAX_N, 1 <= dim <= 32768
+ * (Q4_0_EUNSUPPORTED above); at least one of b and y.  Needs no workspace. */
+int q4_0_residual_norm(const void *b, int b_dtype, int64_t b_stride, const float *post,
+                       const float *gate, int64_t gate_row, int64_t gate_col, float alpha,
+                       const float *h, float *h_out, int64_t h_stride, const float *pre,
+                       float weight_offset, float eps, void *y, int y_dtype, int64_t y_stride,
+                       int64_t n, int64_t dim, void *stream);
+
 /* The kernel q4_0_matmul would run for this call shape (a Q4_0_KERNEL_*
  * value), or a negative status for an invalid shape.  Host only. */
 int q4_0_select_kernel(int64_t n, int64_t out, int64_t in, int x_dtype);
