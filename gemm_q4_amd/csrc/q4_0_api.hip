@@ -341,7 +341,7 @@ int check_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, in
     if (st != Q4_0_OK) return st;
     if (n < 1 || n > Q4_0_MAX_N || batch < 1 || batch > Q4_0_MAX_N) return Q4_0_ESHAPE;
     if (q_heads < 1 || q_heads > 1024 || q_heads % cache->heads != 0) return Q4_0_ESHAPE;
-    if (table_stride < 1 || table_stride > INT32_MAX / cache->page_size) return Q4_0_ESHAPE;
+    if (table_stride < 1 || table_stride > (INT64_C(1) << 30) / cache->page_size) return Q4_0_ESHAPE;
     if (window < 0 || window > INT32_MAX || sinks < 0 || sinks > INT32_MAX) return Q4_0_EINVAL;
     if (!valid_dtype(x_dtype)) return Q4_0_EINVAL;
     if (!q4::attention_supports((int)cache->dim)) return Q4_0_EUNSUPPORTED;

@@ -416,7 +416,7 @@ int q4_0_kv_append(const q4_0_kv_cache *cache, const q4_0_rotary *rot, const voi
  * K or V that a row does not see never change it, infinities and NaN included.
  * dim 64, 128 or 256 (Q4_0_EUNSUPPORTED otherwise); q_heads a multiple of the
  * cache's heads, at most 1024; 1 <= n <= Q4_0_MAX_N, 1 <= batch <= Q4_0_MAX_N;
- * table_stride >= 1, table_stride * page_size < 2^31; window, sinks in
+ * table_stride >= 1, table_stride * page_size <= 2^30; window, sinks in
  * [0, 2^31); scale positive and finite (Q4_0_EINVAL). */
 int q4_0_attention(const q4_0_kv_cache *cache, const void *q, int64_t q_stride, int x_dtype,
                    int64_t q_heads, void *y, int64_t n, const int32_t *q_start,

@@ -95,7 +95,7 @@ def test_attention_refuses_bad_caches(bad, expect):
     (dict(cache=None), q4.ENULL), (dict(n=0), q4.ESHAPE), (dict(batch=0), q4.ESHAPE),
     (dict(n=q4.MAX_N + 1), q4.ESHAPE), (dict(batch=q4.MAX_N + 1), q4.ESHAPE),
     (dict(q_heads=3), q4.ESHAPE), (dict(q_heads=0), q4.ESHAPE), (dict(table_stride=0), q4.ESHAPE),
-    (dict(table_stride=1 << 27), q4.ESHAPE), (dict(window=-1), q4.EINVAL),
+    (dict(table_stride=(1 << 26) + 1), q4.ESHAPE), (dict(window=-1), q4.EINVAL),
     (dict(window=1 << 31), q4.EINVAL), (dict(sinks=-1), q4.EINVAL), (dict(x_dtype=2), q4.EINVAL),
     (dict(cache=cache(dim=96)), q4.EUNSUPPORTED), (dict(cache=cache(dim=512)), q4.EUNSUPPORTED),
     (dict(scale=0.0), q4.EINVAL), (dict(scale=-1.0), q4.EINVAL),

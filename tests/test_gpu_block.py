@@ -289,6 +289,21 @@ def test_attention_bad_pages_and_tables(half):
     near(y[:62], ref[:62], attention_tol(np.nan_to_num(ref[:62]), absolute[:62], score[:62], 120, 64, half))
 
 
+@pytest.mark.parametrize("window", [0, 20])
+def test_attention_impossible_lengths(window):
+    """Lengths far past the table, and negative ones, end as rows of NaN and of
+    zeros; the conversation beside them is untouched."""
+    kc, vc, q, start, lens, table = batch_inputs([(2, 40)] * 3, 4, 2, 64, 16, True, 4)
+    lens[0], lens[2] = 2 ** 31 - 1, -2 ** 31
+    kc, vc = np.nan_to_num(kc), np.nan_to_num(vc)
+    tk, tv = dev(kc), dev(vc)
+    y = q4.attention(q4.kv_cache(tk, tv), dev(q), dev(start), dev(lens), dev(table), window, 1)
+    lens[0] = lens[2] = 0
+    ref, absolute, score = block.attend(kc, vc, q, start, lens, table, window, 1, 0.125)
+    assert torch.isnan(y[:2]).all() and (y[4:] == 0).all()
+    near(y[2:4], ref[2:4], attention_tol(ref[2:4], absolute[2:4], score[2:4], 40, 64, True))
+
+
 def test_attention_offsets_past_32_bits():
     """Pages whose elements lie past 2^32: the same keys on the cache's first and
     last pages give the same result."""
