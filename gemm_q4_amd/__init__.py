@@ -26,7 +26,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch  # noqa: F401  (must precede the CDLL below)
+import torch  # must precede the CDLL below
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # Q4_0_LIBRARY names another build of the same library (a tuning variant)
@@ -146,12 +146,17 @@ def _nbytes(ws, workspace_bytes):
     return ws.numel() * ws.element_size()
 
 
+# torch's current stream as a bare handle where torch offers that (0.1 us
+# against 2 us through a Stream object, as much as a small call's marshalling)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream, *tensors):
     if stream is None:
         for t in tensors:
-            if hasattr(t, "is_cuda") and t.is_cuda:
-                import torch
-                return torch.cuda.current_stream(t.device).cuda_stream
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                return _raw_stream(t.get_device())
         return None
     if isinstance(stream, int):
         return stream
@@ -351,6 +356,7 @@ class q4_0_rotary(ctypes.Structure):
     _fields_ = [("inv_freq", _vp), ("rot_dim", _i64), ("interleaved", _int),
                 ("amplitude", _f32), ("q_norm", _vp), ("k_norm", _vp), ("eps", _f32),
                 ("weight_offset", _f32)]
+    norm_dims = frozenset()      # lengths of the weights, where they are known
 
 
 def _ref(struct):
@@ -395,13 +401,14 @@ def q4_0_residual_norm(b, b_dtype: int, b_stride: int, post, gate, gate_row: int
 
 
 # ---- torch conveniences (allocation through torch, then the C calls above) --
+_DTYPE_CODES = {torch.float32: F32, torch.float16: F16}
+
+
 def dtype_code(x) -> int:
     """Q4_0_F32 or Q4_0_F16 for a torch tensor's dtype."""
-    import torch
-    if x.dtype == torch.float32:
-        return F32
-    if x.dtype == torch.float16:
-        return F16
+    code = _DTYPE_CODES.get(x.dtype)
+    if code is not None:
+        return code
     raise TypeError(f"x must be float32 or float16, not {x.dtype}")
 
 
@@ -496,9 +503,14 @@ def matmul_routed(experts, n_experts: int, x, route, out: int, y=None, stream=No
     return y
 
 
+# The checks below cost as much as a small kernel if they are spelled out each
+# time: what fits is recognised in one expression, and only what does not is
+# looked at for its reason.
 def _typed(t, name: str, dtype, *shape):
     """t's checks before its address goes to the library: type, shape (None:
-    any size) and dense rows."""
+    any size) and dense rows.  Returns the address."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if len(t.shape) != len(shape) or any(s is not None and s != g
@@ -506,35 +518,36 @@ def _typed(t, name: str, dtype, *shape):
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _rows(t, name: str, n: int, width=None):
-    """(row width, row stride) of [n, ...] rows: dense within a row, any
+def _rows(t, name: str, n: int, width: int):
+    """Row stride of [n, width] or [n, heads, dim] rows: dense within a row, any
     distance between rows."""
-    if t.dim() == 3:
-        heads, dim = t.shape[1:]
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-            raise ValueError(f"{name}'s rows must be dense")
-        w = heads * dim
-    elif t.dim() == 2:
-        w = t.shape[1]
-        if w > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}'s rows must be dense")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        w = shape[1]
+        dense = stride[1] == 1 or w == 1
+    elif len(shape) == 3:
+        w = shape[1] * shape[2]
+        dense = (stride[2] == 1 or shape[2] == 1) and (stride[1] == shape[2] or shape[1] == 1)
     else:
         raise ValueError(f"{name} must have two or three dimensions")
-    if t.shape[0] != n or (width is not None and w != width):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not fit the call")
-    return w, t.stride(0) if n > 1 else w
+    if not dense:
+        raise ValueError(f"{name}'s rows must be dense")
+    if shape[0] != n or w != width:
+        raise ValueError(f"{name} has shape {tuple(shape)}, which does not fit the call")
+    return stride[0] if n > 1 else w
 
 
 def kv_cache(k, v):
     """Descriptor of a paged cache: k and v float16 [pages, heads, page_size,
     dim] CUDA tensors.  It holds their addresses: keep the tensors alive."""
-    import torch
-    _typed(k, "k", torch.float16, None, None, None, None)
-    _typed(v, "v", torch.float16, *k.shape)
-    pages, heads, page_size, dim = k.shape
-    return q4_0_kv_cache(k.data_ptr(), v.data_ptr(), pages, heads, page_size, dim)
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"k must be [pages, heads, page_size, dim], not {tuple(shape)}")
+    return q4_0_kv_cache(_typed(k, "k", torch.float16, *shape),
+                         _typed(v, "v", torch.float16, *shape), *shape)
 
 
 def rotary(inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q_norm=None,
@@ -542,13 +555,16 @@ def rotary(inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q_n
     """Descriptor of a rotation (inv_freq: float32 [rot_dim / 2], or None) and of
     per-head norms (float32 [dim] weights, or None).  It holds the tensors'
     addresses: keep them alive."""
-    import torch
-    for t, name in ((inv_freq, "inv_freq"), (q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None:
-            _typed(t, name, torch.float32, None)
-    return q4_0_rotary(_ptr(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(),
-                       int(interleaved), amplitude, _ptr(q_norm), _ptr(k_norm), eps,
-                       weight_offset)
+    f32 = torch.float32
+    half = 0 if inv_freq is None else inv_freq.numel()
+    rot = q4_0_rotary(None if inv_freq is None else _typed(inv_freq, "inv_freq", f32, half),
+                      2 * half, interleaved, amplitude,
+                      None if q_norm is None else _typed(q_norm, "q_norm", f32, None),
+                      None if k_norm is None else _typed(k_norm, "k_norm", f32, None), eps,
+                      weight_offset)
+    # the weights' lengths, for kv_append to hold against the cache's heads
+    rot.norm_dims = {w.shape[0] for w in (q_norm, k_norm) if w is not None}
+    return rot
 
 
 def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
@@ -556,27 +572,25 @@ def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
     and v [n, heads * dim], or the same with the heads as a dimension; rows may
     be slices of wider ones.  positions int32 [n], slots int64 [n].  Returns the
     rotated q [n, q_heads, dim]: q_out, or a new tensor of q's type."""
-    import torch
     n, dim = k.shape[0], cache.dim
-    kw, ks = _rows(k, "k", n, cache.heads * dim)
-    _, vs = _rows(v, "v", n, kw)
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    width = cache.heads * dim
+    code = dtype_code(k)
+    if v.dtype is not k.dtype or (q is not None and q.dtype is not k.dtype):
         raise TypeError("q, k and v must have one type")
-    _typed(slots, "slots", torch.int64, n)
-    if positions is not None:
-        _typed(positions, "positions", torch.int32, n)
-    code, qs, heads, qcode = dtype_code(k), 0, 0, 0
+    if rot is not None and rot.norm_dims - {dim}:
+        raise ValueError(f"norm weights of {rot.norm_dims} do not fit heads of {dim}")
+    qs = heads = qcode = 0
     if q is not None:
-        qw, qs = _rows(q, "q", n)
-        heads = qw // dim
-        if qw % dim:
-            raise ValueError(f"q's rows of {qw} are no whole heads of {dim}")
+        heads = q.shape[1] if q.dim() == 3 else q.shape[1] // dim
+        qs = _rows(q, "q", n, heads * dim)
         if q_out is None:
             q_out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
         qcode = dtype_code(q_out)
         _typed(q_out, "q_out", q_out.dtype, n, heads, dim)
-    q4_0_kv_append(cache, rot, q, qs, k, ks, v, vs, code, q_out, qcode, heads, positions, slots,
-                   n, stream)
+    q4_0_kv_append(cache, rot, q, qs, k, _rows(k, "k", n, width), v, _rows(v, "v", n, width),
+                   code, q_out, qcode, heads,
+                   None if positions is None else _typed(positions, "positions", torch.int32, n),
+                   _typed(slots, "slots", torch.int64, n), n, stream)
     return q_out
 
 
@@ -585,26 +599,23 @@ def attention(cache, q, q_start, kv_len, table, window: int = 0, sinks: int = 0,
     """Attention of q [n, q_heads, dim] over `cache` (q4_0_attention): q_start
     int32 [batch + 1], kv_len int32 [batch], table int32 [batch, pages of the
     longest].  scale: dim ** -0.5 unless given.  Returns y, like q."""
-    import torch
     n, heads, dim = q.shape
     if dim != cache.dim:
         raise ValueError(f"q's heads of {dim} do not fit the cache's {cache.dim}")
     code = dtype_code(q)
-    _, qs = _rows(q, "q", n)
-    batch = kv_len.shape[0]
-    _typed(kv_len, "kv_len", torch.int32, batch)
-    _typed(q_start, "q_start", torch.int32, batch + 1)
-    _typed(table, "table", torch.int32, batch, None)
+    batch, width = kv_len.shape[0], table.shape[-1]
+    i32 = torch.int32
     if y is None:
         y = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
     else:
         _typed(y, "y", q.dtype, n, heads, dim)
-    width = table.shape[1]
     if ws is None:
         ws = workspace(q4_0_attention_workspace_size(cache, heads, code, n, width, batch, window,
                                                      sinks), q.device)
-    q4_0_attention(cache, q, qs, code, heads, y, n, q_start, kv_len, table, width, batch, window,
-                   sinks, dim ** -0.5 if scale is None else scale, ws, None, stream)
+    q4_0_attention(cache, q, _rows(q, "q", n, heads * dim), code, heads, y, n,
+                   _typed(q_start, "q_start", i32, batch + 1), _typed(kv_len, "kv_len", i32, batch),
+                   _typed(table, "table", i32, batch, width), width, batch, window, sinks,
+                   dim ** -0.5 if scale is None else scale, ws, None, stream)
     return y
 
 
@@ -617,37 +628,34 @@ def residual_norm(h, b=None, pre=None, post=None, gate=None, alpha: float = 1.0,
     [dim] or None (no norm).  Without b, y = N(h; pre).  Returns (h_out, y):
     as given, or new tensors (y of y_dtype, float32 unless given; None without
     pre).  h_out may be h."""
-    import torch
     n, dim = h.shape
-    if h.dtype != torch.float32:
+    f32 = torch.float32
+    if h.dtype is not f32:
         raise TypeError(f"h must be float32, not {h.dtype}")
-    _, hs = _rows(h, "h", n)
+    hs = _rows(h, "h", n, dim)
     bs = bcode = ys = ycode = grow = gcol = 0
-    if b is not None:
-        _, bs = _rows(b, "b", n, dim)
-        bcode = dtype_code(b)
+    if b is None:
+        h_out = h
+    else:
+        bs, bcode = _rows(b, "b", n, dim), dtype_code(b)
         if h_out is None:
-            h_out = torch.empty_strided((n, dim), (hs, 1), dtype=torch.float32, device=h.device)
-        elif h_out.dtype != torch.float32 or _rows(h_out, "h_out", n, dim)[1] != hs:
+            h_out = torch.empty_strided((n, dim), (hs, 1), dtype=f32, device=h.device)
+        elif h_out.dtype is not f32 or _rows(h_out, "h_out", n, dim) != hs:
             raise ValueError("h_out must be float32 with h's row stride")
         if gate is not None:
-            if gate.dtype != torch.float32 or gate.dim() != 2 \
-                    or gate.shape[0] not in (1, n) or gate.shape[1] not in (1, dim):
+            if gate.dtype is not f32 or gate.dim() != 2 or gate.shape[0] not in (1, n) \
+                    or gate.shape[1] not in (1, dim):
                 raise ValueError("gate must be float32 [n, dim], [n, 1] or [1, dim]")
             grow = gate.stride(0) if gate.shape[0] > 1 else 0
             gcol = gate.stride(1) if gate.shape[1] > 1 else 0
-    else:
-        h_out = h
-    if pre is not None:
-        _typed(pre, "pre", torch.float32, dim)
-        if y is None:
-            y = torch.empty((n, dim), dtype=y_dtype or torch.float32, device=h.device)
-        _, ys = _rows(y, "y", n, dim)
-        ycode = dtype_code(y)
-    else:
+    if pre is None:
         y = None
-    if post is not None:
-        _typed(post, "post", torch.float32, dim)
-    q4_0_residual_norm(b, bcode, bs, post, gate, grow, gcol, alpha, h, h_out, hs, pre,
-                       weight_offset, eps, y, ycode, ys, n, dim, stream)
+    else:
+        if y is None:
+            y = torch.empty((n, dim), dtype=y_dtype or f32, device=h.device)
+        ys, ycode = _rows(y, "y", n, dim), dtype_code(y)
+        pre = _typed(pre, "pre", f32, dim)
+    q4_0_residual_norm(b, bcode, bs, None if post is None else _typed(post, "post", f32, dim),
+                       gate, grow, gcol, alpha, h, h_out, hs, pre, weight_offset, eps, y, ycode,
+                       ys, n, dim, stream)
     return h_out, y

@@ -180,6 +180,8 @@ def test_conveniences_refuse_what_does_not_fit():
         q4.kv_append(c, None, q, kv.transpose(1, 2).contiguous().transpose(1, 2), kv, pos, slots)
     with pytest.raises(ValueError):
         q4.kv_append(c, None, q, kv, kv, pos, slots[:2])
+    with pytest.raises(ValueError):
+        q4.kv_append(c, q4.rotary(q_norm=torch.ones(32)), q, kv, kv, pos, slots)
     start, lens = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     table = torch.zeros(1, 2, dtype=torch.int32)
     with pytest.raises(ValueError):
