@@ -78,10 +78,11 @@ __device__ __forceinline__ float halves_sum(float x) {
     return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-// A factor applied where the value is a number: an infinity a row earned stays
-// one when the factor has vanished.
-__device__ __forceinline__ float scaled(float x, float f) {
-    return __builtin_isfinite(x) ? x * f : x;
+// exp2 of a difference of maxima, never 0: an infinity that a row earned
+// stays one, and what a vanished factor scales is far below a float32 step of
+// the sum it joins.
+__device__ __forceinline__ float factor_of(float d) {
+    return fmaxf(__builtin_amdgcn_exp2f(d), 1e-38f);
 }
 
 // The conversation whose tiles of R rows include tile `w` of the launch, and
@@ -89,7 +90,8 @@ __device__ __forceinline__ float scaled(float x, float f) {
 // q_start[s] G / R + s on: never fewer than its rows need, and known without a
 // sum over the conversations before it.
 struct Place {
-    int s, first, rows, tile;  // first token, rows of the conversation
+    int s, first, rows, tile;  // first token and rows of the conversation
+    int kv;                    // its length
 };
 
 // The last i < count with holds(i), where holds is true up to some index and
@@ -110,12 +112,28 @@ template <typename F> __device__ __forceinline__ int find_last(int count, F hold
 template <int R>
 __device__ __forceinline__ Place find_tile(const AttentionArgs &a, int group, int w) {
     Place p;
-    p.s = find_last(a.batch, [&](int s) {
-        return (int64_t)min(max(a.q_start[s], 0), a.n) * group / R + s <= w;
-    });
-    const meta_t qs = meta(a.q_start);
-    p.first = min(max(qs[p.s], 0), a.n);
-    const int end = min(max(qs[p.s + 1], p.first), a.n);
+    int end;
+    if (a.batch <= 64) {
+        // every lane's conversation in one round of loads
+        const int s = min((int)(threadIdx.x % 64), a.batch - 1);
+        const int b = min(max(a.q_start[s], 0), a.n), e = a.q_start[s + 1], kv = a.kv_len[s];
+        const bool below = (int64_t)b * group / R + s <= w && (int)(threadIdx.x % 64) < a.batch;
+        const int last = __popcll(__ballot(below)) - 1;
+        p.s = uniform(last < 0 ? 0 : last);
+        p.first = __builtin_amdgcn_readlane(b, p.s);
+        end = __builtin_amdgcn_readlane(e, p.s);
+        p.kv = __builtin_amdgcn_readlane(kv, p.s);
+    } else {
+        p.s = find_last(a.batch, [&](int s) {
+            return (int64_t)min(max(a.q_start[s], 0), a.n) * group / R + s <= w;
+        });
+        const meta_t qs = meta(a.q_start);
+        p.first = min(max(qs[p.s], 0), a.n);
+        end = qs[p.s + 1];
+        p.kv = meta(a.kv_len)[p.s];
+    }
+    end = min(max(end, p.first), a.n);
+    p.kv = max(p.kv, 0);
     p.rows = (end - p.first) * group;
     p.tile = w - (int)((int64_t)p.first * group / R + p.s);
     return p;
@@ -162,69 +180,65 @@ template <int KT> struct Reach {
     }
 };
 
-// Copies of 16 key rows into LDS.  One copy moves 1 KB (512 / DIM rows).
+// Copies of 16 key rows into LDS.  One copy moves 1 KB (512 / DIM rows).  Pages
+// are looked up 64 tiles at a time, one to a lane, so that the loop reads its
+// page from a register and never waits for the table.
 template <int DIM> struct Filler {
     static constexpr int kCopies = DIM / 32;
-    static constexpr int kBytes = 16 * DIM * 2;
     uint32_t off[kCopies];
-    const AttentionArgs &a;
+    const uint8_t *k, *v;  // of this head, on page 0
     const int32_t *table;
-    int head;
-    __device__ __forceinline__ Filler(const AttentionArgs &args, int s, int hk)
-        : a(args), table(args.table + (int64_t)s * args.table_stride), head(hk) {
-        const int lane = threadIdx.x % 64;
+    int64_t page_bytes;
+    int pages, table_stride, shift;
+    __device__ __forceinline__ Filler(const AttentionArgs &a, int s, int hk)
+        : table(a.table + (int64_t)s * a.table_stride),
+          page_bytes(((int64_t)a.cache.heads << a.cache.page_shift) * DIM * 2),
+          pages((int)a.cache.pages), table_stride(a.table_stride), shift(a.cache.page_shift) {
+        const int64_t at = ((int64_t)hk << shift) * DIM * 2;
+        k = (const uint8_t *)a.cache.k + at;
+        v = (const uint8_t *)a.cache.v + at;
 #pragma unroll
-        for (int j = 0; j < kCopies; ++j) {
-            const int row = j * (512 / DIM) + lane / (DIM / 8);
-            off[j] = row * DIM * 2 + ((lane % (DIM / 8)) ^ swz<DIM>(row)) * 16;
-        }
+        for (int j = 0; j < kCopies; ++j) off[j] = offset(j);
     }
-    // Keys k .. k + 15 of K and V; true if every copy was issued.  `parts`: 1 K,
-    // 2 V, 3 both.
-    template <int KT>
-    __device__ __forceinline__ bool fill(const Reach<KT> &r, int k, uint8_t *kbuf, uint8_t *vbuf,
-                                         int parts) {
+    // Byte offset of this lane's piece of copy j within the 16 rows.
+    static __device__ __forceinline__ uint32_t offset(int j) {
         const int lane = threadIdx.x % 64;
-        uint32_t blank = 0;
-        if (!r.none(k, 16)) {
-            const int shift = a.cache.page_shift;
-            const int slot = k >> shift;
-            int page = -1;
-            if (slot < a.table_stride) page = meta(table)[slot];
-            if (page >= 0 && page < a.cache.pages) {
-                const int64_t row = (((int64_t)page * a.cache.heads + head) << shift) +
-                                    (k & ((1 << shift) - 1));
-                const uint8_t *ks = (const uint8_t *)(a.cache.k + row * DIM);
-                const uint8_t *vs = (const uint8_t *)(a.cache.v + row * DIM);
-                if (r.each(k, 16)) {
-                    if (parts & 1)
+        const int row = j * (512 / DIM) + lane / (DIM / 8);
+        return row * DIM * 2 + ((lane % (DIM / 8)) ^ swz<DIM>(row)) * 16;
+    }
+    // The page of key `key` (of the lane's own choice), -1 if it has none.
+    __device__ __forceinline__ int look(int key) const {
+        const int slot = key >> shift;
+        const int page = slot < table_stride ? table[slot] : -1;
+        return page < pages ? max(page, -1) : -1;
+    }
+    // Keys key .. key + 15, of K or of V, from page `page` (wave-uniform); true
+    // if all its copies were issued and nothing else.
+    template <int KT>
+    __device__ __forceinline__ bool fill(const Reach<KT> &r, int page, int key, uint8_t *dst,
+                                         bool is_v) const {
+        const uint8_t *src = (is_v ? v : k) + page * page_bytes +
+                             (int64_t)((key & ((1 << shift) - 1)) * (DIM * 2));
+        if (page >= 0 && r.each(key, 16)) {
 #pragma unroll
-                        for (int j = 0; j < kCopies; ++j) dma16_at(ks, off[j], kbuf + j * 1024);
-                    if (parts & 2)
-#pragma unroll
-                        for (int j = 0; j < kCopies; ++j) dma16_at(vs, off[j], vbuf + j * 1024);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kCopies; ++j) {
-                        const int row16 = j * (512 / DIM) + lane / (DIM / 8);
-                        const bool seen = r.any(k + row16);
-                        if (parts & 1)
-                            dma16(seen ? (const void *)(ks + off[j]) : (const void *)&kZeroPiece,
-                                  kbuf + j * 1024);
-                        if (parts & 2)
-                            dma16(seen ? (const void *)(vs + off[j]) : (const void *)&kZeroPiece,
-                                  vbuf + j * 1024);
-                    }
-                }
-                return true;
-            }
-            blank = 0x7E007E00u;  // no such page: NaN keys for the rows that see them
+            for (int j = 0; j < kCopies; ++j) dma16_at(src, off[j], dst + j * 1024);
+            return true;
         }
-        const u4_t kv = {blank, blank, blank, blank}, zero = {0u, 0u, 0u, 0u};
-#pragma unroll
+        // No page: NaN keys for the rows that see them.  Rows that no row of
+        // the tile sees: zeros.
+        const int lane = threadIdx.x % 64;
+        const bool unseen = r.none(key, 16);
+        const uint32_t x = unseen || is_v ? 0u : 0x7E007E00u;
+        const u4_t blank = {x, x, x, x};
+#pragma nounroll
         for (int j = 0; j < kCopies; ++j) {
-            if (parts & 1) *(u4_t *)(kbuf + j * 1024 + lane * 16) = kv;
-            if (parts & 2) *(u4_t *)(vbuf + j * 1024 + lane * 16) = zero;
+            if (page < 0 || unseen)
+                *(u4_t *)(dst + j * 1024 + lane * 16) = blank;
+            else
+                dma16(r.any(key + j * (512 / DIM) + lane / (DIM / 8))
+                          ? (const void *)(src + offset(j))
+                          : (const void *)&kZeroPiece,
+                      dst + j * 1024);
         }
         return false;
     }
@@ -249,8 +263,12 @@ template <int DIM, bool F32> struct Rows {
     }
 
     // Row r (of the conversation's `rows`); rows past the end repeat the last.
-    __device__ __forceinline__ void load(const AttentionArgs &a, const Place &pl, int group,
-                                         int hk, int r, int position0) {
+    // take() forms the operands, so that other requests can go out in between.
+    struct Raw {
+        u4_t x[kParts * DIM / 16];
+    };
+    __device__ __forceinline__ void request(Raw &raw, const AttentionArgs &a, const Place &pl,
+                                            int group, int hk, int r, int position0) {
         const int half = threadIdx.x % 64 / 32;
         const int rr = min(r, pl.rows - 1);
         const int token = rr / group;
@@ -258,36 +276,42 @@ template <int DIM, bool F32> struct Rows {
         lo = a.window && p >= a.window ? p - a.window + 1 : 0;
         const int64_t at = (int64_t)(pl.first + token) * a.q_stride +
                            (int64_t)(hk * group + rr % group) * DIM + 8 * half;
+        const u4_t *src = (const u4_t *)((const uint8_t *)a.q + at * (F32 ? 4 : 2));
+#pragma unroll
+        for (int s = 0; s < DIM / 16; ++s)
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) raw.x[s * kParts + x] = src[s * (F32 ? 4 : 2) + x];
+        clear();
+    }
+    __device__ __forceinline__ void take(const Raw &raw) {
 #pragma unroll
         for (int s = 0; s < DIM / 16; ++s) {
             if (!F32) {
-                q[0][s] = *(const h8_t *)((const _Float16 *)a.q + at + 16 * s);
+                q[0][s] = __builtin_bit_cast(h8_t, raw.x[s]);
             } else {
-                const float *x = (const float *)a.q + at + 16 * s;
-                const f4_t x0 = *(const f4_t *)x, x1 = *(const f4_t *)(x + 4);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float v = i < 4 ? x0[i & 3] : x1[i & 3];
+                    // (a bit cast of the vector's element itself reads element 0)
+                    const uint32_t bits = raw.x[s * kParts + (i / 4) % kParts][i % 4];
+                    const float v = __builtin_bit_cast(float, bits);
                     const _Float16 hi = (_Float16)v;
                     q[0][s][i] = hi;
                     q[kParts - 1][s][i] = (_Float16)(v - (float)hi);
                 }
             }
         }
-        clear();
     }
 
     __device__ __forceinline__ bool sees(int key, int sinks) const {
         return key <= p && (key >= lo || key < sinks);
     }
 
-    // KT keys from k0 on, in LDS.  masked: some row sees not all of them.
-    // CAREFUL: values that are no numbers touch only the rows that see them.
-    template <int KT, bool CAREFUL>
-    __device__ __forceinline__ void step(const uint8_t *kbuf, const uint8_t *vbuf, int k0,
-                                         bool masked, int sinks, float c) {
+    // Scores of KT keys from k0 on, K in LDS.  masked: some row sees not all of
+    // them.
+    template <int KT>
+    __device__ __forceinline__ void scores(f16x_t (&s)[KT / 32], const uint8_t *kbuf, int k0,
+                                           bool masked, int sinks) const {
         const int lane = threadIdx.x % 64, half = lane / 32;
-        f16x_t s[KT / 32];
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t) {
 #pragma unroll
@@ -302,7 +326,7 @@ template <int DIM, bool F32> struct Rows {
                     s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[x][d], s[t], 0, 0, 0);
             }
         }
-        if (masked || CAREFUL) {
+        if (masked) {
 #pragma unroll
             for (int t = 0; t < KT / 32; ++t)
 #pragma unroll
@@ -310,6 +334,12 @@ template <int DIM, bool F32> struct Rows {
                     if (!sees(k0 + t * 32 + 8 * (i / 4) + 4 * half + i % 4, sinks))
                         s[t][i] = -INFINITY;
         }
+    }
+
+    // Scores to weights, in place; maximum, sum and what is accumulated so far
+    // brought along.
+    template <int KT>
+    __device__ __forceinline__ void weights(f16x_t (&s)[KT / 32], float c) {
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t)
@@ -318,13 +348,13 @@ template <int DIM, bool F32> struct Rows {
         top = halves_max(top) * c;
         if (__any(top > m + kLag)) {
             const float mn = fmaxf(m, top);
-            const float f = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            const float f = mn == -INFINITY ? 1.0f : factor_of(m - mn);
             m = mn;
             l *= f;
 #pragma unroll
             for (int d = 0; d < DIM / 32; ++d)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[d][i] = CAREFUL ? scaled(o[d][i], f) : o[d][i] * f;
+                for (int i = 0; i < 16; ++i) o[d][i] *= f;
         }
         const float base = m == -INFINITY ? 0.0f : kShift - m;
         float sum = 0.0f;
@@ -336,6 +366,14 @@ template <int DIM, bool F32> struct Rows {
                 sum += s[t][i];
             }
         l += sum;
+    }
+
+    // The weighted values of the same keys, V in LDS.  CAREFUL: values that are
+    // no numbers touch only the rows that see them.
+    template <int KT, bool CAREFUL>
+    __device__ __forceinline__ void mix(const f16x_t (&s)[KT / 32], const uint8_t *vbuf, int k0,
+                                        int sinks) {
+        const int lane = threadIdx.x % 64, half = lane / 32;
 #pragma unroll
         for (int b = 0; b < KT / 16; ++b) {
             h8_t w[kParts];
@@ -367,24 +405,24 @@ template <int DIM, bool F32> struct Rows {
                     for (int i = 0; i < 8; ++i) {
                         const float x = (float)v[i];
                         const bool bad = !__builtin_isfinite(x);
+                        const bool seen =
+                            sees(k0 + 16 * b + 8 * (i / 4) + 4 * half + i % 4, sinks);
                         up[i] = (_Float16)(bad && !(x < 0.0f) ? 1.0f : 0.0f);
                         down[i] = (_Float16)(bad && !(x > 0.0f) ? 1.0f : 0.0f);
-                        see[i] = (_Float16)(
-                            sees(k0 + 16 * b + 8 * (i / 4) + 4 * half + i % 4, sinks) ? 1.0f
-                                                                                      : 0.0f);
+                        see[i] = (_Float16)(seen ? 1.0f : 0.0f);
                         if (bad) v[i] = (_Float16)0.0f;
                     }
                     f16x_t zero;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
-                    const f16x_t u =
+                    const f16x_t ups =
                         __builtin_amdgcn_mfma_f32_32x32x16_f16(up, see, zero, 0, 0, 0);
-                    const f16x_t w2 =
+                    const f16x_t downs =
                         __builtin_amdgcn_mfma_f32_32x32x16_f16(down, see, zero, 0, 0, 0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        if (u[i] > 0.0f) o[d][i] += INFINITY;
-                        if (w2[i] > 0.0f) o[d][i] -= INFINITY;
+                        if (ups[i] > 0.0f) o[d][i] += INFINITY;
+                        if (downs[i] > 0.0f) o[d][i] -= INFINITY;
                     }
                 }
 #pragma unroll
@@ -392,6 +430,15 @@ template <int DIM, bool F32> struct Rows {
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[x], o[d], 0, 0, 0);
             }
         }
+    }
+
+    template <int KT, bool CAREFUL>
+    __device__ __forceinline__ void step(const uint8_t *kbuf, const uint8_t *vbuf, int k0,
+                                         bool masked, int sinks, float c) {
+        f16x_t s[KT / 32];
+        scores<KT>(s, kbuf, k0, masked, sinks);
+        weights<KT>(s, c);
+        mix<KT, CAREFUL>(s, vbuf, k0, sinks);
     }
 
     // Whether a product met something that is no number.
@@ -442,16 +489,20 @@ __device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
                                           int top_lo, float c, uint8_t *lds) {
     constexpr int KT = kPassKeys<DIM>;
     constexpr int kTile = KT * DIM * 2;
-    const int wave = uniform(threadIdx.x / 64);
+    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+    // this wave's share of a tile: 16 keys of K and V, or (32-key tiles) of one
+    const int at = 16 * (wave % (KT / 16));
+    int looked = 0;
     const auto fill = [&](int t, int stage) {
-        uint8_t *kbuf = lds + stage * 2 * kTile, *vbuf = kbuf + kTile;
-        const int k = r.key(t);
+        if ((t - t0) % 64 == 0) looked = f.look(r.key(min(t + lane, t1 - 1)) + at);
+        const int page = __builtin_amdgcn_readlane(looked, (t - t0) % 64);
+        const int k = r.key(t) + at;
+        uint8_t *dst = lds + stage * 2 * kTile + at * DIM * 2;
         if (KT == 64) {
-            const int at = 16 * wave;
-            f.fill(r, k + at, kbuf + at * DIM * 2, vbuf + at * DIM * 2, 3);
+            f.fill(r, page, k, dst, false);
+            f.fill(r, page, k, dst + kTile, true);
         } else {
-            const int at = 16 * (wave % 2);
-            f.fill(r, k + at, kbuf + at * DIM * 2, vbuf + at * DIM * 2, wave < 2 ? 1 : 2);
+            f.fill(r, page, k, dst + (wave < 2 ? 0 : kTile), wave >= 2);
         }
     };
     fill(t0, 0);
@@ -462,23 +513,22 @@ __device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
         if (t + 1 < t1) fill(t + 1, stage ^ 1);
         const int k = r.key(t);
         const uint8_t *kbuf = lds + stage * 2 * kTile;
-        w.template step<KT, CAREFUL>(kbuf, kbuf + kTile, k, !r.all(k, KT, top_lo), r.sinks, c);
+        w.template step<KT, CAREFUL>(kbuf, kbuf + kTile, k, CAREFUL || !r.all(k, KT, top_lo),
+                                     r.sinks, c);
     }
 }
 
 template <int DIM, bool F32>
-__global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void pass_kernel(AttentionArgs a, Plan pl, int base) {
+__global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void pass_kernel(AttentionArgs a, Plan pl,
+                                                                      int base) {
     constexpr int KT = kPassKeys<DIM>;
     __shared__ __align__(1024) uint8_t lds[2 * 2 * KT * DIM * 2];
-    const int hk = blockIdx.x % a.cache.heads;
-    const int rest = blockIdx.x / a.cache.heads;
-    const int split = rest % pl.splits;
-    Place at = find_tile<kPassRows>(a, pl.group, base + rest / pl.splits);
+    const int hk = blockIdx.x, split = blockIdx.y;
+    Place at = find_tile<kPassRows>(a, pl.group, base + blockIdx.z);
     const int count = (at.rows + kPassRows - 1) / kPassRows;
     if (at.tile < 0 || at.tile >= count) return;
     at.tile = count - 1 - at.tile;  // the tiles with the most keys first
-    const int kv = max(meta(a.kv_len)[at.s], 0);
-    const int position0 = kv - at.rows / pl.group;
+    const int position0 = at.kv - at.rows / pl.group;
     const int row0 = at.tile * kPassRows, row1 = min(row0 + kPassRows, at.rows);
     const int p0 = position(a, position0, row0 / pl.group);
     const int p1 = position(a, position0, (row1 - 1) / pl.group);
@@ -489,7 +539,11 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void pass_kernel(AttentionA
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int row = row0 + wave * 32 + lane % 32;
     Rows<DIM, F32> w;
-    w.load(a, at, pl.group, hk, row, position0);
+    {
+        typename Rows<DIM, F32>::Raw raw;
+        w.request(raw, a, at, pl.group, hk, row, position0);
+        w.take(raw);
+    }
     if (t0 < t1) {
         Filler<DIM> f(a, at.s, hk);
         const float c = a.scale * kLog2e;
@@ -518,64 +572,94 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void pass_kernel(AttentionA
 }
 
 // ---- few rows: every wave streams its own keys for the same 32 rows ---------
-// No barrier in the loop: a wave fills its own two stages and waits for its own
-// copies.  The waves' results are joined through LDS at the end.
+// No barrier in the loop: a wave fills its own K and V tile and waits for its
+// own copies.  One tile each, not two stages: K is requested again as soon as
+// the scores are formed, V as soon as it is mixed, and the other waves of the
+// workgroup cover what that leaves open, so nearly all of LDS is in flight.
+// The waves' results are joined through LDS at the end.
 constexpr int kStepRows = 32, kStepKeys = 32;
-template <int DIM> constexpr int kStepWaves = DIM > 128 ? 2 : 4;
 
 template <int DIM, bool F32, bool CAREFUL>
 __device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
-                                          const Reach<kStepKeys> &r, int t0, int t1, int stride,
-                                          int top_lo, float c, uint8_t *lds) {
+                                          const Reach<kStepKeys> &r, int t, int t1, int stride,
+                                          int top_lo, float c, uint8_t *kbuf, int look0,
+                                          int look1, bool started) {
     constexpr int KT = kStepKeys;
-    constexpr int kTile = KT * DIM * 2;
-    constexpr int kCopies = KT / 16 * 2 * Filler<DIM>::kCopies;
-    const auto fill = [&](int t, int stage) {
-        uint8_t *kbuf = lds + stage * 2 * kTile, *vbuf = kbuf + kTile;
+    constexpr int kCopies = KT / 16 * Filler<DIM>::kCopies;  // of K, or of V
+    constexpr int kHalf = 16 * DIM * 2;
+    uint8_t *vbuf = kbuf + 2 * kHalf;
+    const int lane = threadIdx.x % 64;
+    if (t >= t1) return;
+    int i = 0;  // the tile's lane in look0 and look1
+    int page0 = __builtin_amdgcn_readlane(look0, 0), page1 = __builtin_amdgcn_readlane(look1, 0);
+    bool counted = false;  // the copies requested last are all kCopies of them
+    if (!started) {
         const int k = r.key(t);
-        bool full = true;
-#pragma unroll
-        for (int at = 0; at < KT; at += 16)
-            full &= f.fill(r, k + at, kbuf + at * DIM * 2, vbuf + at * DIM * 2, 3);
-        return full;
-    };
-    if (t0 >= t1) return;
-    fill(t0, 0);
-    int stage = 0;
-    for (int t = t0; t < t1; t += stride) {
-        bool counted = false;
-        if (t + stride < t1) counted = fill(t + stride, stage ^ 1);
+        f.fill(r, page0, k, kbuf, false);
+        f.fill(r, page1, k + 16, kbuf + kHalf, false);
+        f.fill(r, page0, k, vbuf, true);
+        f.fill(r, page1, k + 16, vbuf + kHalf, true);
+    }
+    for (; t < t1; t += stride) {
+        const int k = r.key(t), next = r.key(t + stride);
+        const bool more = t + stride < t1;
+        f16x_t s[KT / 32];
+        // outstanding: K, then V
+        if (counted)
+            Q4_WAIT_VMCNT(kCopies);
+        else
+            Q4_WAIT_VMCNT(0);
+        Q4_WAIT_LGKM0();
+        asm volatile("" ::: "memory");
+        w.template scores<KT>(s, kbuf, k, CAREFUL || !r.all(k, KT, top_lo), r.sinks);
+        Q4_WAIT_LGKM0();
+        asm volatile("" ::: "memory");
+        counted = false;
+        if (more) {
+            i = (i + 1) % 64;
+            if (i == 0) {
+                const int mine = r.key(min(t + stride + lane * stride, t1 - 1));
+                look0 = f.look(mine);
+                look1 = f.look(mine + 16);
+            }
+            page0 = __builtin_amdgcn_readlane(look0, i);
+            page1 = __builtin_amdgcn_readlane(look1, i);
+            counted = f.fill(r, page0, next, kbuf, false);
+            counted &= f.fill(r, page1, next + 16, kbuf + kHalf, false);
+        }
+        w.template weights<KT>(s, c);
+        // outstanding: V, then the next K
         if (counted)
             Q4_WAIT_VMCNT(kCopies);
         else
             Q4_WAIT_VMCNT(0);
         asm volatile("" ::: "memory");
-        const int k = r.key(t);
-        const uint8_t *kbuf = lds + stage * 2 * kTile;
-        w.template step<KT, CAREFUL>(kbuf, kbuf + kTile, k, !r.all(k, KT, top_lo), r.sinks, c);
+        w.template mix<KT, CAREFUL>(s, vbuf, k, r.sinks);
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
-        stage ^= 1;
+        if (more) {
+            counted = f.fill(r, page0, next, vbuf, true);
+            counted &= f.fill(r, page1, next + 16, vbuf + kHalf, true);
+        }
     }
 }
 
-template <int DIM, bool F32>
-__global__ __launch_bounds__(64 * kStepWaves<DIM>) void step_kernel(AttentionArgs a, Plan pl, int base) {
-    constexpr int KT = kStepKeys, W = kStepWaves<DIM>;
-    constexpr int kStage = 2 * KT * DIM * 2;  // K and V
+template <int DIM, bool F32, int W>
+__global__ __launch_bounds__(64 * W) void step_kernel(AttentionArgs a, Plan pl, int base) {
+    constexpr int KT = kStepKeys;
+    constexpr int kHalf = 16 * DIM * 2;
     constexpr int kPitch = DIM + 4;
-    __shared__ __align__(1024) uint8_t lds[W * 2 * kStage];
+    // a wave's K and V tiles, later its rows
+    constexpr int kShare = 32 * kPitch * 4;
+    static_assert(4 * kHalf <= kShare && kShare % 256 == 0, "both fit");
+    __shared__ __align__(1024) uint8_t lds[W * kShare];
     __shared__ float ml[2][W][32];
-    static_assert(32 * kPitch * 4 <= 2 * kStage, "a wave's rows fit its own stages");
-    const int hk = blockIdx.x % a.cache.heads;
-    const int rest = blockIdx.x / a.cache.heads;
-    const int split = rest % pl.splits;
-    const Place at = find_tile<kStepRows>(a, pl.group, base + rest / pl.splits);
+    const int hk = blockIdx.x, split = blockIdx.y;
+    const Place at = find_tile<kStepRows>(a, pl.group, base + blockIdx.z);
     const int row0 = at.tile * kStepRows;
     if (row0 < 0 || row0 >= at.rows) return;
     const int row1 = min(row0 + kStepRows, at.rows);
-    const int kv = max(meta(a.kv_len)[at.s], 0);
-    const int position0 = kv - at.rows / pl.group;
+    const int position0 = at.kv - at.rows / pl.group;
     const int p0 = position(a, position0, row0 / pl.group);
     const int p1 = position(a, position0, (row1 - 1) / pl.group);
     const Reach<KT> r(a, p0, p1);
@@ -583,15 +667,40 @@ __global__ __launch_bounds__(64 * kStepWaves<DIM>) void step_kernel(AttentionArg
     const int per = (r.tiles + pl.splits - 1) / pl.splits;
     const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
-    Rows<DIM, F32> w;
-    w.load(a, at, pl.group, hk, row0 + lane % 32, position0);
-    uint8_t *mine = lds + wave * 2 * kStage;
+    uint8_t *mine = lds + wave * kShare;
     Filler<DIM> f(a, at.s, hk);
+    Rows<DIM, F32> w;
+    const int t = t0 + wave;
+    int look0 = -1, look1 = -1;
+    {
+        typename Rows<DIM, F32>::Raw raw;
+        if (t < t1) {
+            const int k = r.key(min(t + lane * W, t1 - 1));
+            look0 = f.look(k);
+            look1 = f.look(k + 16);
+        }
+        w.request(raw, a, at, pl.group, hk, row0 + lane % 32, position0);
+        if (t < t1) {
+            const int k = r.key(t);
+            const int page0 = __builtin_amdgcn_readlane(look0, 0);
+            const int page1 = __builtin_amdgcn_readlane(look1, 0);
+            f.fill(r, page0, k, mine, false);
+            f.fill(r, page1, k + 16, mine + kHalf, false);
+            f.fill(r, page0, k, mine + 2 * kHalf, true);
+            f.fill(r, page1, k + 16, mine + 3 * kHalf, true);
+        }
+        w.take(raw);
+    }
     const float c = a.scale * kLog2e;
-    step_loop<DIM, F32, false>(w, f, r, t0 + wave, t1, W, top_lo, c, mine);
+    step_loop<DIM, F32, false>(w, f, r, t, t1, W, top_lo, c, mine, look0, look1, true);
     if (__any(w.odd())) {
         w.clear();
-        step_loop<DIM, F32, true>(w, f, r, t0 + wave, t1, W, top_lo, c, mine);
+        if (t < t1) {
+            const int k = r.key(min(t + lane * W, t1 - 1));
+            look0 = f.look(k);
+            look1 = f.look(k + 16);
+        }
+        step_loop<DIM, F32, true>(w, f, r, t, t1, W, top_lo, c, mine, look0, look1, false);
     }
     // join the waves
     w.l = halves_sum(w.l);
@@ -600,17 +709,19 @@ __global__ __launch_bounds__(64 * kStepWaves<DIM>) void step_kernel(AttentionArg
     float m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int i = 0; i < W; ++i) m = fmaxf(m, ml[0][i][lane % 32]);
-    const float fs = w.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(w.m - m);
-    float *rows = (float *)mine;
+    const float fs = factor_of(w.m - (m == -INFINITY ? 0.0f : m));
+    if (lane % 32 < row1 - row0) {
+        float *mrow = (float *)mine + (lane % 32) * kPitch + 4 * (lane / 32);
 #pragma unroll
-    for (int d = 0; d < DIM / 32; ++d)
+        for (int d = 0; d < DIM / 32; ++d)
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            f4_t v;
+            for (int i = 0; i < 16; i += 4) {
+                f4_t v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = scaled(w.o[d][i + e], fs);
-            *(f4_t *)(rows + (lane % 32) * kPitch + 32 * d + 2 * i + 4 * (lane / 32)) = v;
-        }
+                for (int e = 0; e < 4; ++e) v[e] = w.o[d][i + e] * fs;
+                *(f4_t *)(mrow + 32 * d + 2 * i) = v;
+            }
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < (row1 - row0) * (DIM / 4); e += 64 * W) {
         const int rr = e / (DIM / 4), d = e % (DIM / 4) * 4;
@@ -620,11 +731,10 @@ __global__ __launch_bounds__(64 * kStepWaves<DIM>) void step_kernel(AttentionArg
         for (int i = 0; i < W; ++i) m = fmaxf(m, ml[0][i][rr]);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            const f4_t v = *(const f4_t *)((const float *)(lds + i * 2 * kStage) + rr * kPitch + d);
+            const f4_t v = *(const f4_t *)((const float *)(lds + i * kShare) + rr * kPitch + d);
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[x] += v[x];
-            if (ml[0][i][rr] != -INFINITY || ml[1][i][rr] != 0.0f)
-                l += scaled(ml[1][i][rr], __builtin_amdgcn_exp2f(ml[0][i][rr] - m));
+            l += ml[1][i][rr] * factor_of(ml[0][i][rr] - (m == -INFINITY ? 0.0f : m));
         }
         const int token = (row0 + rr) / pl.group;
         const int64_t out = (int64_t)(at.first + token) * a.q_heads + hk * pl.group +
@@ -646,20 +756,31 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
     __shared__ float factor[kMaxSplits];
     __shared__ float wave_m[4], wave_l[4];
     __shared__ f4_t sums[256];
-    const int64_t row = blockIdx.x;
+    const int64_t row = blockIdx.x, rows = (int64_t)a.n * a.q_heads;
     const int token = (int)(row / a.q_heads), dim = a.cache.dim;
+    const int x = threadIdx.x, wave = x / 64;
+    const int cols = dim / 4, lanes = 256 / cols, first = x / cols;
+    // what does not depend on the conversation is requested before it is known;
+    // a part that was not written is never used
+    constexpr int kAhead = 4;
+    f4_t ahead[kAhead];
+    const float *src = pl.part + row * dim + x % cols * 4;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int part = first + i * lanes;
+        if (part < pl.splits) ahead[i] = *(const f4_t *)(src + part * rows * dim);
+    }
+    float m = -INFINITY, l = 0.0f;
+    if (x < pl.splits) {
+        const float *ml = pl.part_ml + (x * rows + row) * 2;
+        m = ml[0], l = ml[1];
+    }
     // the last conversation that starts at or before the token
     const int s = find_last(a.batch, [&](int i) { return a.q_start[i] <= token; });
     const meta_t qs = meta(a.q_start);
-    const int first = min(max(qs[s], 0), a.n), end = min(max(qs[s + 1], first), a.n);
-    if (token < first || token >= end) return;
+    const int begin = min(max(qs[s], 0), a.n), end = min(max(qs[s + 1], begin), a.n);
+    if (token < begin || token >= end) return;
     const bool sees = max(meta(a.kv_len)[s], 0) - end + token >= 0;
-    const int x = threadIdx.x, wave = x / 64;
-    float m = -INFINITY, l = 0.0f;
-    if (x < pl.splits) {
-        const float *ml = pl.part_ml + ((int64_t)x * a.n * a.q_heads + row) * 2;
-        m = ml[0], l = ml[1];
-    }
     float top = m;
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i));
@@ -668,24 +789,26 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
     top = fmaxf(fmaxf(wave_m[0], wave_m[1]), fmaxf(wave_m[2], wave_m[3]));
     // a part that saw none of the row's keys wrote no elements: marked by -1
     const bool used = m != -INFINITY || l != 0.0f;
-    const float f = used ? __builtin_amdgcn_exp2f(m - top) : -1.0f;
+    const float f = used ? factor_of(m - (top == -INFINITY ? 0.0f : top)) : -1.0f;
     if (x < pl.splits) factor[x] = f;
-    l = used ? scaled(l, f) : 0.0f;
+    l = used ? l * f : 0.0f;
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) l += __shfl_xor(l, i);
     if (x % 64 == 0) wave_l[wave] = l;
     __syncthreads();
     l = wave_l[0] + wave_l[1] + wave_l[2] + wave_l[3];
-    const int cols = dim / 4, col = x % cols;
     f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = x / cols; i < pl.splits; i += 256 / cols) {
-        const float g = factor[i];
-        if (g == -1.0f) continue;
-        const f4_t v =
-            *(const f4_t *)(pl.part + ((int64_t)i * a.n * a.q_heads + row) * dim + col * 4);
+    const auto add = [&](const f4_t &v, int part) {
+        const float g = factor[part];
+        if (g == -1.0f) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += scaled(v[e], g);
-    }
+        for (int e = 0; e < 4; ++e) o[e] += v[e] * g;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (first + i * lanes < pl.splits) add(ahead[i], first + i * lanes);
+    for (int part = first + kAhead * lanes; part < pl.splits; part += lanes)
+        add(*(const f4_t *)(src + part * rows * dim), part);
     sums[x] = o;
     __syncthreads();
     if (x >= cols) return;
@@ -702,10 +825,18 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
 // ---- choices on the host ----------------------------------------------------
 struct Choice {
     bool pass;  // 128-row tiles; else 32-row ones, every wave on its own keys
+    int waves;  // of a 32-row workgroup
     int64_t tiles;
     int splits;
     size_t part, bytes;  // workspace: bytes of the partial rows, and in all
 };
+
+#ifndef TUNE_BALANCE
+#define TUNE_BALANCE 4
+#endif
+#ifndef TUNE_LEAST
+#define TUNE_LEAST 2
+#endif
 
 Choice choose(const AttentionArgs &a) {
     Choice ch;
@@ -713,7 +844,10 @@ Choice choose(const AttentionArgs &a) {
     const int64_t rows = (int64_t)a.n * (a.q_heads / heads);
     // more rows to a conversation than a 32-row tile holds: the waves share
     // the keys; up to that they share the rows and split the keys
-    ch.pass = rows > (int64_t)kStepRows * a.batch;
+#ifndef TUNE_PASS
+#define TUNE_PASS 32
+#endif
+    ch.pass = rows > (int64_t)TUNE_PASS * a.batch;
     const int R = ch.pass ? kPassRows : kStepRows;
     ch.tiles = rows / R + a.batch;
     const int64_t likely = (ch.pass ? rows / R + (a.batch + 1) / 2
@@ -727,12 +861,33 @@ Choice choose(const AttentionArgs &a) {
         if (near < keys) keys = near;
     }
     const int64_t most = (keys + KT - 1) / KT;
-    const int waves = dim > 128 ? kStepWaves<256> : kStepWaves<128>;
-    const int64_t slots = (int64_t)device_shape().cus * (ch.pass ? (dim > 128 ? 1 : 2)
-                                                                 : (dim > 64 ? 1 : 2));
-    int64_t splits = likely >= slots ? 1 : slots / likely;
-    const int64_t least = ch.pass ? 4 : 2 * waves;  // tiles a part should have
-    if (splits > most / least) splits = most / least;
+    const int64_t cus = device_shape().cus;
+    int64_t splits;
+    ch.waves = dim > 128 ? 2 : 4;
+    if (ch.pass) {
+        const int64_t slots = cus * (dim > 128 ? 1 : 2);
+        splits = likely >= slots ? 1 : slots / likely;
+        if (splits > most / 4) splits = most / 4;
+#ifdef TUNE_PASS1
+        splits = 1;
+#endif
+    } else {
+        const int64_t slots = cus * (dim > 64 ? 2 : 4);
+        if (a.batch == 1)
+            splits = slots / likely;
+        else
+            splits = (TUNE_BALANCE * slots / 2 + likely - 1) / likely;
+        const int64_t least = TUNE_LEAST * ch.waves;  // tiles a part should have
+        if (splits > most / least) splits = most / least;
+#ifdef TUNE_W8
+        if (splits < 2) {
+#else
+        if (splits < 2 && likely <= cus) {
+#endif
+            splits = 1;
+            ch.waves *= 2;
+        }
+    }
     if (splits > kMaxSplits) splits = kMaxSplits;
     const int64_t out = (int64_t)a.n * a.q_heads;
     const int64_t room = (int64_t)kWorkspaceBytes / (out * (dim + 2) * 4);
@@ -745,17 +900,21 @@ Choice choose(const AttentionArgs &a) {
 
 template <int DIM, bool F32>
 hipError_t run(const AttentionArgs &a, const Choice &ch, const Plan &pl, hipStream_t stream) {
-    // a launch's work items stay below 2^31
-    const int64_t each = (INT64_C(1) << 22) / (ch.splits * a.cache.heads);
-    for (int64_t base = 0; base < ch.tiles; base += each) {
-        const int64_t tiles = ch.tiles - base < each ? ch.tiles - base : each;
-        const dim3 grid((uint32_t)(tiles * ch.splits * a.cache.heads));
+    // heads fastest: the tiles of one head of a conversation come to the same
+    // die, eight heads to eight dies, and share its L2
+    for (int64_t base = 0; base < ch.tiles; base += 65535) {
+        const int64_t tiles = ch.tiles - base < 65535 ? ch.tiles - base : 65535;
+        const dim3 grid((uint32_t)a.cache.heads, (uint32_t)ch.splits, (uint32_t)tiles);
+        constexpr int W = DIM > 128 ? 2 : 4;
         if (ch.pass)
             hipLaunchKernelGGL((pass_kernel<DIM, F32>), grid, dim3(256), 0, stream, a, pl,
                                (int)base);
+        else if (ch.waves == W)
+            hipLaunchKernelGGL((step_kernel<DIM, F32, W>), grid, dim3(64 * W), 0, stream, a, pl,
+                               (int)base);
         else
-            hipLaunchKernelGGL((step_kernel<DIM, F32>), grid, dim3(64 * kStepWaves<DIM>), 0,
-                               stream, a, pl, (int)base);
+            hipLaunchKernelGGL((step_kernel<DIM, F32, 2 * W>), grid, dim3(128 * W), 0, stream, a,
+                               pl, (int)base);
     }
     if (ch.splits > 1)
         hipLaunchKernelGGL((join_kernel<F32>), dim3((uint32_t)(a.n * a.q_heads)), dim3(256), 0,
