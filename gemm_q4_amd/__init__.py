@@ -32,10 +32,11 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # Q4_0_LIBRARY names another build of the same library (a tuning variant)
 LIB_PATH = os.environ.get("Q4_0_LIBRARY") or os.path.join(_HERE, "libq4_0.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(
-        f"{LIB_PATH} is missing: build the HIP library first "
-        "(python -c 'import __graft_entry__ as g; g.build()')")
+for _path in (LIB_PATH, os.path.join(_HERE, "_bind.so")):
+    if not os.path.exists(_path):
+        raise ImportError(
+            f"{_path} is missing: build the HIP library first "
+            "(python -c 'import __graft_entry__ as g; g.build()')")
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -150,6 +151,12 @@ def _nbytes(ws, workspace_bytes):
 # against 2 us through a Stream object, as much as a small call's marshalling)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+from . import _bind  # noqa: E402  (torch is loaded; built beside the library)
+
+_bind.setup(*(ctypes.cast(getattr(_lib, _name), _vp).value
+              for _name in ("q4_0_kv_append", "q4_0_attention", "q4_0_residual_norm")),
+            _raw_stream)
 
 
 def _stream(stream, *tensors):
@@ -356,11 +363,13 @@ class q4_0_rotary(ctypes.Structure):
     _fields_ = [("inv_freq", _vp), ("rot_dim", _i64), ("interleaved", _int),
                 ("amplitude", _f32), ("q_norm", _vp), ("k_norm", _vp), ("eps", _f32),
                 ("weight_offset", _f32)]
-    norm_dims = frozenset()      # lengths of the weights, where they are known
 
 
 def _ref(struct):
-    return None if struct is None else ctypes.addressof(struct)
+    """Address of a descriptor: a ctypes structure, or kv_cache()'s or rotary()'s."""
+    if struct is None:
+        return None
+    return ctypes.addressof(struct) if isinstance(struct, ctypes.Structure) else struct.address
 
 
 def q4_0_kv_append(cache, rot, q, q_stride: int, k, k_stride: int, v, v_stride: int,
@@ -503,68 +512,26 @@ def matmul_routed(experts, n_experts: int, x, route, out: int, y=None, stream=No
     return y
 
 
-# The checks below cost as much as a small kernel if they are spelled out each
-# time: what fits is recognised in one expression, and only what does not is
-# looked at for its reason.
-def _typed(t, name: str, dtype, *shape):
-    """t's checks before its address goes to the library: type, shape (None:
-    any size) and dense rows.  Returns the address."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if len(t.shape) != len(shape) or any(s is not None and s != g
-                                         for s, g in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows(t, name: str, n: int, width: int):
-    """Row stride of [n, width] or [n, heads, dim] rows: dense within a row, any
-    distance between rows."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2:
-        w = shape[1]
-        dense = stride[1] == 1 or w == 1
-    elif len(shape) == 3:
-        w = shape[1] * shape[2]
-        dense = (stride[2] == 1 or shape[2] == 1) and (stride[1] == shape[2] or shape[1] == 1)
-    else:
-        raise ValueError(f"{name} must have two or three dimensions")
-    if not dense:
-        raise ValueError(f"{name}'s rows must be dense")
-    if shape[0] != n or w != width:
-        raise ValueError(f"{name} has shape {tuple(shape)}, which does not fit the call")
-    return stride[0] if n > 1 else w
+# The checks of the block operators' conveniences are made by the extension
+# module (csrc/q4_0_bind.cpp): here they would cost more than a small kernel.
+def _handle(stream):
+    """A stream argument as an integer, None for torch's current stream."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def kv_cache(k, v):
     """Descriptor of a paged cache: k and v float16 [pages, heads, page_size,
-    dim] CUDA tensors.  It holds their addresses: keep the tensors alive."""
-    shape = k.shape
-    if len(shape) != 4:
-        raise ValueError(f"k must be [pages, heads, page_size, dim], not {tuple(shape)}")
-    return q4_0_kv_cache(_typed(k, "k", torch.float16, *shape),
-                         _typed(v, "v", torch.float16, *shape), *shape)
+    dim] CUDA tensors, which it keeps alive.  Any call here that takes a
+    q4_0_kv_cache takes it too."""
+    return _bind.kv_cache(k, v)
 
 
 def rotary(inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q_norm=None,
            k_norm=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """Descriptor of a rotation (inv_freq: float32 [rot_dim / 2], or None) and of
-    per-head norms (float32 [dim] weights, or None).  It holds the tensors'
-    addresses: keep them alive."""
-    f32 = torch.float32
-    half = 0 if inv_freq is None else inv_freq.numel()
-    rot = q4_0_rotary(None if inv_freq is None else _typed(inv_freq, "inv_freq", f32, half),
-                      2 * half, interleaved, amplitude,
-                      None if q_norm is None else _typed(q_norm, "q_norm", f32, None),
-                      None if k_norm is None else _typed(k_norm, "k_norm", f32, None), eps,
-                      weight_offset)
-    # the weights' lengths, for kv_append to hold against the cache's heads
-    rot.norm_dims = {w.shape[0] for w in (q_norm, k_norm) if w is not None}
-    return rot
+    per-head norms (float32 [dim] weights, or None); it keeps the tensors
+    alive."""
+    return _bind.rotary(inv_freq, interleaved, amplitude, q_norm, k_norm, eps, weight_offset)
 
 
 def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
@@ -572,26 +539,12 @@ def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
     and v [n, heads * dim], or the same with the heads as a dimension; rows may
     be slices of wider ones.  positions int32 [n], slots int64 [n].  Returns the
     rotated q [n, q_heads, dim]: q_out, or a new tensor of q's type."""
-    n, dim = k.shape[0], cache.dim
-    width = cache.heads * dim
-    code = dtype_code(k)
-    if v.dtype is not k.dtype or (q is not None and q.dtype is not k.dtype):
-        raise TypeError("q, k and v must have one type")
-    if rot is not None and rot.norm_dims - {dim}:
-        raise ValueError(f"norm weights of {rot.norm_dims} do not fit heads of {dim}")
-    qs = heads = qcode = 0
-    if q is not None:
-        heads = q.shape[1] if q.dim() == 3 else q.shape[1] // dim
-        qs = _rows(q, "q", n, heads * dim)
-        if q_out is None:
-            q_out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
-        qcode = dtype_code(q_out)
-        _typed(q_out, "q_out", q_out.dtype, n, heads, dim)
-    q4_0_kv_append(cache, rot, q, qs, k, _rows(k, "k", n, width), v, _rows(v, "v", n, width),
-                   code, q_out, qcode, heads,
-                   None if positions is None else _typed(positions, "positions", torch.int32, n),
-                   _typed(slots, "slots", torch.int64, n), n, stream)
-    return q_out
+    if q is not None and q_out is None:
+        heads = q.shape[1] if q.dim() == 3 else q.shape[1] // cache.dim
+        q_out = torch.empty((q.shape[0], heads, cache.dim), dtype=q.dtype, device=q.device)
+    _check(_bind.kv_append(cache, rot, q, k, v, positions, slots, q_out, _handle(stream)),
+           "q4_0_kv_append")
+    return None if q is None else q_out
 
 
 def attention(cache, q, q_start, kv_len, table, window: int = 0, sinks: int = 0, scale=None,
@@ -599,23 +552,16 @@ def attention(cache, q, q_start, kv_len, table, window: int = 0, sinks: int = 0,
     """Attention of q [n, q_heads, dim] over `cache` (q4_0_attention): q_start
     int32 [batch + 1], kv_len int32 [batch], table int32 [batch, pages of the
     longest].  scale: dim ** -0.5 unless given.  Returns y, like q."""
-    n, heads, dim = q.shape
-    if dim != cache.dim:
-        raise ValueError(f"q's heads of {dim} do not fit the cache's {cache.dim}")
-    code = dtype_code(q)
-    batch, width = kv_len.shape[0], table.shape[-1]
-    i32 = torch.int32
     if y is None:
-        y = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
-    else:
-        _typed(y, "y", q.dtype, n, heads, dim)
+        y = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if ws is None:
-        ws = workspace(q4_0_attention_workspace_size(cache, heads, code, n, width, batch, window,
-                                                     sinks), q.device)
-    q4_0_attention(cache, q, _rows(q, "q", n, heads * dim), code, heads, y, n,
-                   _typed(q_start, "q_start", i32, batch + 1), _typed(kv_len, "kv_len", i32, batch),
-                   _typed(table, "table", i32, batch, width), width, batch, window, sinks,
-                   dim ** -0.5 if scale is None else scale, ws, None, stream)
+        ws = workspace(q4_0_attention_workspace_size(
+            cache, q.shape[1], dtype_code(q), q.shape[0], table.shape[-1], kv_len.shape[0], window,
+            sinks), q.device)
+    if scale is None:
+        scale = cache.dim ** -0.5
+    _check(_bind.attention(cache, q, q_start, kv_len, table, window, sinks, scale, y, ws,
+                           _handle(stream)), "q4_0_attention")
     return y
 
 
@@ -628,34 +574,14 @@ def residual_norm(h, b=None, pre=None, post=None, gate=None, alpha: float = 1.0,
     [dim] or None (no norm).  Without b, y = N(h; pre).  Returns (h_out, y):
     as given, or new tensors (y of y_dtype, float32 unless given; None without
     pre).  h_out may be h."""
-    n, dim = h.shape
-    f32 = torch.float32
-    if h.dtype is not f32:
-        raise TypeError(f"h must be float32, not {h.dtype}")
-    hs = _rows(h, "h", n, dim)
-    bs = bcode = ys = ycode = grow = gcol = 0
     if b is None:
         h_out = h
-    else:
-        bs, bcode = _rows(b, "b", n, dim), dtype_code(b)
-        if h_out is None:
-            h_out = torch.empty_strided((n, dim), (hs, 1), dtype=f32, device=h.device)
-        elif h_out.dtype is not f32 or _rows(h_out, "h_out", n, dim) != hs:
-            raise ValueError("h_out must be float32 with h's row stride")
-        if gate is not None:
-            if gate.dtype is not f32 or gate.dim() != 2 or gate.shape[0] not in (1, n) \
-                    or gate.shape[1] not in (1, dim):
-                raise ValueError("gate must be float32 [n, dim], [n, 1] or [1, dim]")
-            grow = gate.stride(0) if gate.shape[0] > 1 else 0
-            gcol = gate.stride(1) if gate.shape[1] > 1 else 0
+    elif h_out is None:
+        h_out = torch.empty_strided(h.shape, h.stride(), dtype=h.dtype, device=h.device)
     if pre is None:
         y = None
-    else:
-        if y is None:
-            y = torch.empty((n, dim), dtype=y_dtype or f32, device=h.device)
-        ys, ycode = _rows(y, "y", n, dim), dtype_code(y)
-        pre = _typed(pre, "pre", f32, dim)
-    q4_0_residual_norm(b, bcode, bs, None if post is None else _typed(post, "post", f32, dim),
-                       gate, grow, gcol, alpha, h, h_out, hs, pre, weight_offset, eps, y, ycode,
-                       ys, n, dim, stream)
+    elif y is None:
+        y = torch.empty(h.shape, dtype=y_dtype or torch.float32, device=h.device)
+    _check(_bind.residual_norm(h, b, pre, post, gate, alpha, eps, weight_offset, h_out, y,
+                               _handle(stream)), "q4_0_residual_norm")
     return h_out, y
