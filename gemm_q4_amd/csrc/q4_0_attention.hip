@@ -477,67 +477,95 @@ __device__ __forceinline__ void put_ml(const AttentionArgs &a, const Plan &pl, i
     ml[1] = l;
 }
 
-// ---- many rows: four waves of 32 rows share each key tile -------------------
-// Two stages of KT keys in LDS: while the waves work on one, the copies of the
-// next are in flight.
-template <int DIM> constexpr int kPassKeys = DIM > 128 ? 32 : 64;
-constexpr int kPassRows = 128;
+// ---- many rows: waves of 32 rows share each key tile ------------------------
+// RW waves of 32 rows work on one key tile; KW such groups take every KW-th
+// tile each and are joined through LDS at the end.  Two stages of KT keys to a
+// group: while its waves work on one, the copies of the next are in flight.
+// RW = 4, KW = 1 reads a key least often; RW = 2, KW = 4 (or 2) keeps the
+// device busy when there are few rows.
+template <int DIM, int RW, int KW> struct Pass {
+    static constexpr int KT = KW > 1 || DIM > 128 ? 32 : 64;
+    static constexpr int kTile = KT * DIM * 2;
+    static constexpr int kPitch = DIM + 4, kShare = 32 * kPitch * 4;
+    static constexpr int kStages = KW * 4 * kTile;
+    static constexpr int kLds = KW > 1 && RW * KW * kShare > kStages ? RW * KW * kShare : kStages;
+    static constexpr int kThreads = 64 * RW * KW;
+    // two workgroups to a compute unit, or eight waves
+    static constexpr int kWavesPerSimd = DIM > 128 ? 1 : 2;
+};
 
-template <int DIM, bool F32, bool CAREFUL>
+template <int DIM, bool F32, int RW, int KW, bool CAREFUL>
 __device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
-                                          const Reach<kPassKeys<DIM>> &r, int t0, int t1,
+                                          const Reach<Pass<DIM, RW, KW>::KT> &r, int t0, int t1,
                                           int top_lo, float c, uint8_t *lds) {
-    constexpr int KT = kPassKeys<DIM>;
-    constexpr int kTile = KT * DIM * 2;
+    using P = Pass<DIM, RW, KW>;
+    constexpr int KT = P::KT, kTile = P::kTile, kGroups = KT / 16;
+    constexpr bool kBoth = RW <= kGroups;  // a wave copies K and V of its keys, or one of them
+    constexpr int kMine = kBoth ? kGroups / RW : 1;
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
-    // this wave's share of a tile: 16 keys of K and V, or (32-key tiles) of one
-    const int at = 16 * (wave % (KT / 16));
-    int looked = 0;
-    const auto fill = [&](int t, int stage) {
-        if ((t - t0) % 64 == 0) looked = f.look(r.key(min(t + lane, t1 - 1)) + at);
-        const int page = __builtin_amdgcn_readlane(looked, (t - t0) % 64);
-        const int k = r.key(t) + at;
-        uint8_t *dst = lds + stage * 2 * kTile + at * DIM * 2;
-        if (KT == 64) {
-            f.fill(r, page, k, dst, false);
-            f.fill(r, page, k, dst + kTile, true);
-        } else {
-            f.fill(r, page, k, dst + (wave < 2 ? 0 : kTile), wave >= 2);
+    const int rw = wave % RW;
+    uint8_t *mine = lds + wave / RW * 4 * kTile;
+    const int at = 16 * (kBoth ? rw * kMine : rw % kGroups);
+    t0 += wave / RW;
+    const int count = (t1 - t0 + KW - 1) / KW;  // this group's tiles
+    int looked[kMine];
+    const auto fill = [&](int i) {
+        if (i % 64 == 0) {
+            const int key = r.key(min(t0 + (i + lane) * KW, t1 - 1)) + at;
+#pragma unroll
+            for (int x = 0; x < kMine; ++x) looked[x] = f.look(key + 16 * x);
+        }
+        const int k = r.key(t0 + i * KW) + at;
+        uint8_t *dst = mine + (i & 1) * 2 * kTile + at * DIM * 2;
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) {
+            const int page = __builtin_amdgcn_readlane(looked[x], i % 64);
+            uint8_t *d = dst + 16 * x * DIM * 2;
+            if (kBoth) {
+                f.fill(r, page, k + 16 * x, d, false);
+                f.fill(r, page, k + 16 * x, d + kTile, true);
+            } else {
+                f.fill(r, page, k, d + (rw < kGroups ? 0 : kTile), rw >= kGroups);
+            }
         }
     };
-    fill(t0, 0);
-    for (int t = t0; t < t1; ++t) {
-        const int stage = (t - t0) & 1;
+    if (count > 0) fill(0);
+    // every group goes through as many barriers as the first
+    const int rounds = uniform((t1 - t0 + wave / RW + KW - 1) / KW);
+    for (int i = 0; i < rounds; ++i) {
         Q4_WAIT_VMCNT(0);
         __syncthreads();
-        if (t + 1 < t1) fill(t + 1, stage ^ 1);
-        const int k = r.key(t);
-        const uint8_t *kbuf = lds + stage * 2 * kTile;
+        if (i + 1 < count) fill(i + 1);
+        if (i >= count) continue;
+        const int k = r.key(t0 + i * KW);
+        const uint8_t *kbuf = mine + (i & 1) * 2 * kTile;
         w.template step<KT, CAREFUL>(kbuf, kbuf + kTile, k, CAREFUL || !r.all(k, KT, top_lo),
                                      r.sinks, c);
     }
 }
 
-template <int DIM, bool F32>
-__global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void pass_kernel(AttentionArgs a, Plan pl,
-                                                                      int base) {
-    constexpr int KT = kPassKeys<DIM>;
-    __shared__ __align__(1024) uint8_t lds[2 * 2 * KT * DIM * 2];
+template <int DIM, bool F32, int RW, int KW>
+__global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
+                             (Pass<DIM, RW, KW>::kWavesPerSimd)) void pass_kernel(AttentionArgs a, Plan pl, int base) {
+    using P = Pass<DIM, RW, KW>;
+    __shared__ __align__(1024) uint8_t lds[P::kLds];
+    __shared__ float ml[2][KW][32 * RW];
+    constexpr int R = 32 * RW;
     const int hk = blockIdx.x, split = blockIdx.y;
-    Place at = find_tile<kPassRows>(a, pl.group, base + blockIdx.z);
-    const int count = (at.rows + kPassRows - 1) / kPassRows;
+    Place at = find_tile<R>(a, pl.group, base + blockIdx.z);
+    const int count = (at.rows + R - 1) / R;
     if (at.tile < 0 || at.tile >= count) return;
     at.tile = count - 1 - at.tile;  // the tiles with the most keys first
     const int position0 = at.kv - at.rows / pl.group;
-    const int row0 = at.tile * kPassRows, row1 = min(row0 + kPassRows, at.rows);
+    const int row0 = at.tile * R, row1 = min(row0 + R, at.rows);
     const int p0 = position(a, position0, row0 / pl.group);
     const int p1 = position(a, position0, (row1 - 1) / pl.group);
-    const Reach<KT> r(a, p0, p1);
+    const Reach<P::KT> r(a, p0, p1);
     const int top_lo = a.window && p1 >= a.window ? p1 - a.window + 1 : 0;
     const int per = (r.tiles + pl.splits - 1) / pl.splits;
     const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int row = row0 + wave * 32 + lane % 32;
+    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+    const int mine = wave % RW * 32 + lane % 32, row = row0 + mine;
     Rows<DIM, F32> w;
     {
         typename Rows<DIM, F32>::Raw raw;
@@ -547,19 +575,68 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void pass_kernel(AttentionA
     if (t0 < t1) {
         Filler<DIM> f(a, at.s, hk);
         const float c = a.scale * kLog2e;
-        pass_loop<DIM, F32, false>(w, f, r, t0, t1, top_lo, c, lds);
+        pass_loop<DIM, F32, RW, KW, false>(w, f, r, t0, t1, top_lo, c, lds);
         if (__syncthreads_or(w.odd())) {
             w.clear();
-            pass_loop<DIM, F32, true>(w, f, r, t0, t1, top_lo, c, lds);
+            pass_loop<DIM, F32, RW, KW, true>(w, f, r, t0, t1, top_lo, c, lds);
         }
     }
+    float l = halves_sum(w.l), m = w.m;
+    const int half = lane / 32;
+    if (KW > 1) {
+        // join the groups: the first takes over its rows' sum
+        if (lane < 32) ml[0][wave / RW][mine] = m, ml[1][wave / RW][mine] = l;
+        __syncthreads();
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) top = fmaxf(top, ml[0][i][mine]);
+        const float zero = top == -INFINITY ? 0.0f : top;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) l += ml[1][i][mine] * factor_of(ml[0][i][mine] - zero);
+        const float fs = factor_of(m - zero);
+        m = top;
+        float *share = (float *)(lds + wave * P::kShare) + (lane % 32) * P::kPitch + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                f4_t v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = w.o[d][i + e] * fs;
+                *(f4_t *)(share + 32 * d + 2 * i) = v;
+            }
+        __syncthreads();
+        if (pl.splits > 1 && wave < RW && lane < 32 && row < row1) {
+            const int64_t out = (int64_t)(at.first + row / pl.group) * a.q_heads +
+                                hk * pl.group + row % pl.group;
+            put_ml(a, pl, split, out, m, l);
+        }
+        if (wave < RW && lane < 32) ml[1][0][mine] = l;
+        __syncthreads();
+        if (pl.splits > 1 && t0 >= t1) return;
+        for (int e = threadIdx.x; e < (row1 - row0) * (DIM / 4); e += P::kThreads) {
+            const int rr = e / (DIM / 4), d = e % (DIM / 4) * 4;
+            const float *src = (const float *)(lds + rr / 32 * P::kShare) + rr % 32 * P::kPitch + d;
+            f4_t o = *(const f4_t *)src;
+#pragma unroll
+            for (int i = 1; i < KW; ++i) {
+                const f4_t v = *(const f4_t *)(src + i * RW * P::kShare / 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[x] += v[x];
+            }
+            const int token = (row0 + rr) / pl.group;
+            const int64_t out = (int64_t)(at.first + token) * a.q_heads + hk * pl.group +
+                                (row0 + rr) % pl.group;
+            put4<F32>(a, pl, split, out, DIM, d, o, ml[1][0][rr], position0 + token >= 0);
+        }
+        return;
+    }
     if (row >= row1) return;
-    const float l = halves_sum(w.l);
     const int64_t out = (int64_t)(at.first + row / pl.group) * a.q_heads + hk * pl.group +
                         row % pl.group;
-    const int half = lane / 32;
     if (pl.splits > 1) {
-        if (half == 0) put_ml(a, pl, split, out, w.m, l);
+        if (half == 0) put_ml(a, pl, split, out, m, l);
         if (t0 >= t1) return;
     }
 #pragma unroll
@@ -824,7 +901,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
 
 // ---- choices on the host ----------------------------------------------------
 struct Choice {
-    bool pass;  // 128-row tiles; else 32-row ones, every wave on its own keys
+    // rows of a tile: 128 and 64 (waves share the keys, or half of them), 32
+    // (every wave on its own keys)
+    int rows;
     int waves;  // of a 32-row workgroup
     int64_t tiles;
     int splits;
@@ -842,35 +921,31 @@ Choice choose(const AttentionArgs &a) {
     Choice ch;
     const int dim = a.cache.dim, heads = a.cache.heads;
     const int64_t rows = (int64_t)a.n * (a.q_heads / heads);
+    const int64_t cus = device_shape().cus;
     // more rows to a conversation than a 32-row tile holds: the waves share
     // the keys; up to that they share the rows and split the keys
-#ifndef TUNE_PASS
-#define TUNE_PASS 32
-#endif
-    ch.pass = rows > (int64_t)TUNE_PASS * a.batch;
-    const int R = ch.pass ? kPassRows : kStepRows;
+    if (rows <= (int64_t)kStepRows * a.batch)
+        ch.rows = 32;
+    else
+        ch.rows = (rows / 128 + (a.batch + 1) / 2) * heads >= cus ? 128 : 64;
+    const int R = ch.rows;
     ch.tiles = rows / R + a.batch;
-    const int64_t likely = (ch.pass ? rows / R + (a.batch + 1) / 2
-                                    : (rows / R > a.batch ? rows / R : a.batch)) *
+    const int64_t likely = (R > 32 ? rows / R + (a.batch + 1) / 2
+                                   : (rows / R > a.batch ? rows / R : a.batch)) *
                            heads;
     // the key tiles a row tile can have at most
-    const int KT = ch.pass ? (dim > 128 ? kPassKeys<256> : kPassKeys<128>) : kStepKeys;
+    const int KT = R == 128 && dim <= 128 ? 64 : 32;
     int64_t keys = (int64_t)a.table_stride << a.cache.page_shift;
     if (a.window) {
         const int64_t near = (int64_t)a.window + a.sinks + 2 * R + 2 * KT;
         if (near < keys) keys = near;
     }
     const int64_t most = (keys + KT - 1) / KT;
-    const int64_t cus = device_shape().cus;
     int64_t splits;
     ch.waves = dim > 128 ? 2 : 4;
-    if (ch.pass) {
-        const int64_t slots = cus * (dim > 128 ? 1 : 2);
-        splits = likely >= slots ? 1 : slots / likely;
-        if (splits > most / 4) splits = most / 4;
-#ifdef TUNE_PASS1
-        splits = 1;
-#endif
+    if (R > 32) {
+        splits = cus / likely;
+        if (splits > most / 16) splits = most / 16;
     } else {
         const int64_t slots = cus * (dim > 64 ? 2 : 4);
         if (a.batch == 1)
@@ -879,11 +954,7 @@ Choice choose(const AttentionArgs &a) {
             splits = (TUNE_BALANCE * slots / 2 + likely - 1) / likely;
         const int64_t least = TUNE_LEAST * ch.waves;  // tiles a part should have
         if (splits > most / least) splits = most / least;
-#ifdef TUNE_W8
-        if (splits < 2) {
-#else
         if (splits < 2 && likely <= cus) {
-#endif
             splits = 1;
             ch.waves *= 2;
         }
@@ -900,15 +971,18 @@ Choice choose(const AttentionArgs &a) {
 
 template <int DIM, bool F32>
 hipError_t run(const AttentionArgs &a, const Choice &ch, const Plan &pl, hipStream_t stream) {
+    constexpr int W = DIM > 128 ? 2 : 4;
     // heads fastest: the tiles of one head of a conversation come to the same
     // die, eight heads to eight dies, and share its L2
     for (int64_t base = 0; base < ch.tiles; base += 65535) {
         const int64_t tiles = ch.tiles - base < 65535 ? ch.tiles - base : 65535;
         const dim3 grid((uint32_t)a.cache.heads, (uint32_t)ch.splits, (uint32_t)tiles);
-        constexpr int W = DIM > 128 ? 2 : 4;
-        if (ch.pass)
-            hipLaunchKernelGGL((pass_kernel<DIM, F32>), grid, dim3(256), 0, stream, a, pl,
+        if (ch.rows == 128)
+            hipLaunchKernelGGL((pass_kernel<DIM, F32, 4, 1>), grid, dim3(256), 0, stream, a, pl,
                                (int)base);
+        else if (ch.rows == 64)
+            hipLaunchKernelGGL((pass_kernel<DIM, F32, 2, W>), grid, dim3(128 * W), 0, stream, a,
+                               pl, (int)base);
         else if (ch.waves == W)
             hipLaunchKernelGGL((step_kernel<DIM, F32, W>), grid, dim3(64 * W), 0, stream, a, pl,
                                (int)base);
