@@ -327,6 +327,7 @@ template <int DIM, bool F32> struct Rows {
             }
         }
         if (masked) {
+            asm volatile("; masked tile");  // a branch, not a select in every tile
 #pragma unroll
             for (int t = 0; t < KT / 32; ++t)
 #pragma unroll
@@ -336,10 +337,15 @@ template <int DIM, bool F32> struct Rows {
         }
     }
 
-    // Scores to weights, in place; maximum, sum and what is accumulated so far
-    // brought along.
+    // Weights of KT keys as the second product's B operands, 16 keys each.
+    template <int KT> struct Weights {
+        h8_t w[KT / 16][kParts];
+    };
+
+    // Scores to weights; maximum, sum and what is accumulated so far brought
+    // along.  The sum is of the rounded weights, two at a time.
     template <int KT>
-    __device__ __forceinline__ void weights(f16x_t (&s)[KT / 32], float c) {
+    __device__ __forceinline__ void weights(Weights<KT> &out, f16x_t (&s)[KT / 32], float c) {
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t)
@@ -357,32 +363,37 @@ template <int DIM, bool F32> struct Rows {
                 for (int i = 0; i < 16; ++i) o[d][i] *= f;
         }
         const float base = m == -INFINITY ? 0.0f : kShift - m;
-        float sum = 0.0f;
+        const h2_t ones = {(_Float16)1.0f, (_Float16)1.0f};
 #pragma unroll
-        for (int t = 0; t < KT / 32; ++t)
+        for (int b = 0; b < KT / 16; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, base));
-                sum += s[t][i];
+            for (int i = 0; i < 8; i += 2) {
+                const float x0 =
+                    __builtin_amdgcn_exp2f(fmaf(s[b / 2][8 * (b % 2) + i], c, base));
+                const float x1 =
+                    __builtin_amdgcn_exp2f(fmaf(s[b / 2][8 * (b % 2) + i + 1], c, base));
+                const h2_t hi = {(_Float16)x0, (_Float16)x1};
+                out.w[b][0][i] = hi[0];
+                out.w[b][0][i + 1] = hi[1];
+                l = __builtin_amdgcn_fdot2(hi, ones, l, false);
+                if (F32) {
+                    const h2_t lo = {(_Float16)(x0 - (float)hi[0]), (_Float16)(x1 - (float)hi[1])};
+                    out.w[b][kParts - 1][i] = lo[0];
+                    out.w[b][kParts - 1][i + 1] = lo[1];
+                    l = __builtin_amdgcn_fdot2(lo, ones, l, false);
+                }
             }
-        l += sum;
     }
 
     // The weighted values of the same keys, V in LDS.  CAREFUL: values that are
     // no numbers touch only the rows that see them.
     template <int KT, bool CAREFUL>
-    __device__ __forceinline__ void mix(const f16x_t (&s)[KT / 32], const uint8_t *vbuf, int k0,
+    __device__ __forceinline__ void mix(const Weights<KT> &ws, const uint8_t *vbuf, int k0,
                                         int sinks) {
         const int lane = threadIdx.x % 64, half = lane / 32;
 #pragma unroll
         for (int b = 0; b < KT / 16; ++b) {
-            h8_t w[kParts];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = s[b / 2][8 * (b % 2) + i];
-                w[0][i] = (_Float16)x;
-                if (F32) w[kParts - 1][i] = (_Float16)(x - (float)w[0][i]);
-            }
+            const h8_t *w = ws.w[b];
             const int key = 16 * b + 4 * half + lane % 16 / 4;
             const int piece = 2 * (lane / 16 % 2) + lane % 4 / 2;
             const uint8_t *r0 = vbuf + key * DIM * 2 + 8 * (lane % 2);
@@ -393,10 +404,8 @@ template <int DIM, bool F32> struct Rows {
                     (lds_s4_t)(r0 + ((4 * d + piece) ^ swz<DIM>(key)) * 16));
                 const s4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                     (lds_s4_t)(r1 + ((4 * d + piece) ^ swz<DIM>(key + 8)) * 16));
-                h8_t v;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = __builtin_bit_cast(_Float16, (short)(i < 4 ? v0[i & 3] : v1[i & 3]));
+                h8_t v = __builtin_bit_cast(
+                    h8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
                 if (CAREFUL) {
                     // what is no number leaves the product; rows that see it
                     // are given it afterwards (both signs: NaN)
@@ -437,8 +446,9 @@ template <int DIM, bool F32> struct Rows {
                                          bool masked, int sinks, float c) {
         f16x_t s[KT / 32];
         scores<KT>(s, kbuf, k0, masked, sinks);
-        weights<KT>(s, c);
-        mix<KT, CAREFUL>(s, vbuf, k0, sinks);
+        Weights<KT> ws;
+        weights<KT>(ws, s, c);
+        mix<KT, CAREFUL>(ws, vbuf, k0, sinks);
     }
 
     // Whether a product met something that is no number.
@@ -704,14 +714,15 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
             counted = f.fill(r, page0, next, kbuf, false);
             counted &= f.fill(r, page1, next + 16, kbuf + kHalf, false);
         }
-        w.template weights<KT>(s, c);
+        typename Rows<DIM, F32>::template Weights<KT> ws;
+        w.template weights<KT>(ws, s, c);
         // outstanding: V, then the next K
         if (counted)
             Q4_WAIT_VMCNT(kCopies);
         else
             Q4_WAIT_VMCNT(0);
         asm volatile("" ::: "memory");
-        w.template mix<KT, CAREFUL>(s, vbuf, k, r.sinks);
+        w.template mix<KT, CAREFUL>(ws, vbuf, k, r.sinks);
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
         if (more) {
