@@ -49,7 +49,8 @@ constexpr float kShift = 7.0f, kLag = 8.0f;
 // The work of a launch, as the kernels and the joining kernel see it.
 struct Plan {
     int group;      // query heads per key/value head
-    int splits;     // parts of the key axis
+    int splits;     // parts of the key axis, at most
+    int least;      // key tiles of a part, at least
     float *part;    // splits > 1: unnormalised rows [split][n * q_heads][dim]
     float *part_ml; // and their (maximum, sum) [split][n * q_heads][2]
 };
@@ -572,7 +573,7 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
     const int p1 = position(a, position0, (row1 - 1) / pl.group);
     const Reach<P::KT> r(a, p0, p1);
     const int top_lo = a.window && p1 >= a.window ? p1 - a.window + 1 : 0;
-    const int per = (r.tiles + pl.splits - 1) / pl.splits;
+    const int per = max((r.tiles + pl.splits - 1) / pl.splits, pl.least);
     const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int mine = wave % RW * 32 + lane % 32, row = row0 + mine;
@@ -752,7 +753,7 @@ __global__ __launch_bounds__(64 * W) void step_kernel(AttentionArgs a, Plan pl, 
     const int p1 = position(a, position0, (row1 - 1) / pl.group);
     const Reach<KT> r(a, p0, p1);
     const int top_lo = a.window && p1 >= a.window ? p1 - a.window + 1 : 0;
-    const int per = (r.tiles + pl.splits - 1) / pl.splits;
+    const int per = max((r.tiles + pl.splits - 1) / pl.splits, pl.least);
     const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     uint8_t *mine = lds + wave * kShare;
@@ -918,29 +919,29 @@ struct Choice {
     int waves;  // of a 32-row workgroup
     int64_t tiles;
     int splits;
+    int least;  // key tiles of a part, at least
     size_t part, bytes;  // workspace: bytes of the partial rows, and in all
 };
 
-#ifndef TUNE_BALANCE
-#define TUNE_BALANCE 4
-#endif
-#ifndef TUNE_LEAST
-#define TUNE_LEAST 2
-#endif
-
+// How a call is cut into work items.  The host knows the sizes, not the
+// conversations' lengths: those may change between replays of a graph.
 Choice choose(const AttentionArgs &a) {
     Choice ch;
     const int dim = a.cache.dim, heads = a.cache.heads;
     const int64_t rows = (int64_t)a.n * (a.q_heads / heads);
     const int64_t cus = device_shape().cus;
-    // more rows to a conversation than a 32-row tile holds: the waves share
-    // the keys; up to that they share the rows and split the keys
+    // Up to as many rows to a conversation as a 32-row tile holds, the waves of
+    // a workgroup share the rows and split the keys.  With more, they share the
+    // keys: 128 rows to a tile if that gives every compute unit one, 64 if not
+    // (512 tokens of 4 heads to each of 8 key/value heads, 1100 keys each: 21 us
+    // on 64-row tiles; 35 us on 128-row ones, 48 us with their key axis split).
     if (rows <= (int64_t)kStepRows * a.batch)
         ch.rows = 32;
     else
         ch.rows = (rows / 128 + (a.batch + 1) / 2) * heads >= cus ? 128 : 64;
     const int R = ch.rows;
     ch.tiles = rows / R + a.batch;
+    // the items that are likely to have work: not all tiles do
     const int64_t likely = (R > 32 ? rows / R + (a.batch + 1) / 2
                                    : (rows / R > a.batch ? rows / R : a.batch)) *
                            heads;
@@ -956,25 +957,33 @@ Choice choose(const AttentionArgs &a) {
     ch.waves = dim > 128 ? 2 : 4;
     if (R > 32) {
         splits = cus / likely;
-        if (splits > most / 16) splits = most / 16;
+        ch.least = 16;
     } else {
+        // workgroups that run at once: two to a compute unit, four of 64-wide heads
         const int64_t slots = cus * (dim > 64 ? 2 : 4);
-        if (a.batch == 1)
+        if (a.batch == 1) {
             splits = slots / likely;
-        else
-            splits = (TUNE_BALANCE * slots / 2 + likely - 1) / likely;
-        const int64_t least = TUNE_LEAST * ch.waves;  // tiles a part should have
-        if (splits > most / least) splits = most / least;
-        if (splits < 2 && likely <= cus) {
-            splits = 1;
-            ch.waves *= 2;
+            ch.least = 2 * ch.waves;
+        } else {
+            // Several conversations are of several lengths: more parts than run
+            // at once, so that the long ones do not end alone, but of 1024
+            // keys at least (a part costs about 4 us beside its keys).  64
+            // conversations of 400 to 8192 keys: 217 us unsplit, 205 us so, 221
+            // us in parts of 512; 32 of 4096 keys of 256: 106, 98 and 106 us.
+            splits = (4 * slots + likely - 1) / likely;
+            ch.least = 32;
         }
+        // too few keys to split: the workgroup's own waves take them, eight
+        // (four) instead of four (two) while there are units to spare
+        if (most / ch.least < 2 && likely <= cus) ch.waves *= 2;
     }
+    if (splits > most / ch.least) splits = most / ch.least;
     if (splits > kMaxSplits) splits = kMaxSplits;
     const int64_t out = (int64_t)a.n * a.q_heads;
     const int64_t room = (int64_t)kWorkspaceBytes / (out * (dim + 2) * 4);
     if (splits > room) splits = room;
     ch.splits = splits < 2 ? 1 : (int)splits;
+    if (ch.splits == 1) ch.least = 1;
     ch.part = ch.splits > 1 ? (size_t)ch.splits * (size_t)out * (size_t)dim * 4u : 0;
     ch.bytes = ch.splits > 1 ? ch.part + (size_t)ch.splits * (size_t)out * 8u : 0;
     return ch;
@@ -1022,7 +1031,7 @@ size_t attention_workspace_bytes(const AttentionArgs &a, int) { return choose(a)
 
 hipError_t launch_attention(const AttentionArgs &a, int x_f16, void *ws, hipStream_t stream) {
     const Choice ch = choose(a);
-    const Plan pl = {a.q_heads / a.cache.heads, ch.splits, (float *)ws,
+    const Plan pl = {a.q_heads / a.cache.heads, ch.splits, ch.least, (float *)ws,
                      (float *)((uint8_t *)ws + ch.part)};
     return x_f16 ? by_dim<false>(a, ch, pl, stream) : by_dim<true>(a, ch, pl, stream);
 }
