@@ -444,8 +444,8 @@ int q4_0_attention_workspace_size(const q4_0_kv_cache *cache, int64_t q_heads, i
  *   y    : DEVICE rows of dim elements of y_dtype, y_stride apart, with
  *          pre (DEVICE float32 [dim]); or NULL: no second norm, pre ignored.
  * The residual stream and all sums are float32; a binary16 y is rounded once.
- * Rows whose sizes, bases or strides are no multiple of 16 bytes are taken
- * element by element.  1 <= n <= Q4_0_MAX_N, 1 <= dim <= 32768
+ * Any sizes, bases and strides; whole multiples of 16 bytes (8 of binary16) are
+ * fastest.  1 <= n <= Q4_0_MAX_N, 1 <= dim <= 32768
  * (Q4_0_EUNSUPPORTED above); at least one of b and y.  Needs no workspace. */
 int q4_0_residual_norm(const void *b, int b_dtype, int64_t b_stride, const float *post,
                        const float *gate, int64_t gate_row, int64_t gate_col, float alpha,
