@@ -470,3 +470,72 @@ def test_workspace_contents_do_not_matter():
         ws = torch.full((max(need, 256),), fill, dtype=torch.uint8, device=DEV)
         got.append(q4.attention(cache, q, start, lens, table, ws=ws))
     assert torch.equal(got[0], got[1]) and torch.isfinite(got[0]).all()
+
+
+def test_block_operators_allocate_no_device_memory():
+    """Free device memory is unchanged by calls with caller-owned buffers (after
+    a first round that loads the code)."""
+    n, hq, hk, dim = 70, 8, 2, 128
+    kc, vc = (torch.zeros(64, hk, 16, dim, dtype=torch.float16, device=DEV) for _ in range(2))
+    cache, rot = q4.kv_cache(kc, vc), q4.rotary(torch.ones(64, device=DEV))
+    qkv = torch.randn(n, (hq + 2 * hk) * dim, device=DEV)
+    parts = qkv.split([hq * dim, hk * dim, hk * dim], dim=1)
+    pos, slots = torch.arange(n, device=DEV).int(), torch.arange(n, device=DEV)
+    q, y = torch.empty(n, hq, dim, device=DEV), torch.empty(n, hq, dim, device=DEV)
+    ws = torch.empty(q4.WORKSPACE_MAX, dtype=torch.uint8, device=DEV)
+    table = torch.arange(64, dtype=torch.int32, device=DEV)[None]
+    one, all_ = (torch.tensor([0, k], dtype=torch.int32, device=DEV) for k in (1, n))
+    lens = torch.tensor([1000], dtype=torch.int32, device=DEV)
+    h, w = torch.randn(n, hq * dim, device=DEV), torch.ones(hq * dim, device=DEV)
+    oh, oy = torch.empty_like(h), torch.empty_like(h)
+
+    def round_():
+        q4.kv_append(cache, rot, *parts, pos, slots, q_out=q)
+        q4.attention(cache, q, all_, lens, table, y=y, ws=ws)
+        q4.attention(cache, q[:1], one, lens, table, y=y[:1], ws=ws)      # split, joined
+        q4.residual_norm(h, y.flatten(1), w, w, h_out=oh, y=oy)
+
+    round_()
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    for _ in range(5):
+        round_()
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] == before
+
+
+def test_example_decodes_what_one_pass_gives():
+    """The example's captured decode steps against one pass over the whole text;
+    with a window and first tokens, and without.  Decode takes activations in 22
+    bits, a pass of more rows in binary16: a dozen roundings of 2^-11 along the
+    way, of which the two that norms rescale count most."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "decoder_block.py")
+    spec = importlib.util.spec_from_file_location("decoder_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for args in ({}, dict(window=0, sinks=0, prompts=(3, 100), steps=6, heads=8, dim=128, seed=4)):
+        got, want = example.run(**args)
+        assert torch.isfinite(got).all()
+        assert float((got - want).norm() / want.norm()) < 12 * H16
+
+
+def test_calls_refuse_tensors_on_the_host():
+    k = torch.zeros(2, 2, 16, 64, dtype=torch.float16, device=DEV)
+    c = q4.kv_cache(k, k.clone())
+    q = torch.zeros(1, 4, 64, device=DEV)
+    start = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([1], dtype=torch.int32)
+    table = torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):
+        q4.attention(c, q, start, lens, table)
+    kv = torch.zeros(1, 2, 64, device=DEV)
+    slots = torch.zeros(1, dtype=torch.int64, device=DEV)
+    with pytest.raises(ValueError):
+        q4.kv_append(c, q4.rotary(torch.ones(32)), q, kv, kv, start[:1], slots)
+    with pytest.raises(ValueError):
+        q4.residual_norm(kv[0], kv[0], torch.ones(64))
+    with pytest.raises(ValueError):
+        q4.kv_append(c, None, q, kv, kv, None, slots.cpu())
