@@ -41,11 +41,6 @@ typedef __attribute__((address_space(3))) s4_t *lds_s4_t;
 typedef const __attribute__((address_space(4))) int32_t *meta_t;
 
 constexpr float kLog2e = 1.4426950408889634f;
-// Weights are held as 2^kShift exp(s - m): with m allowed to lag behind the
-// true maximum by kLag (in powers of two) before the accumulators are rescaled,
-// the largest is 2^15 < 65504, and the smallest binary16 step is 2^-32 of it.
-constexpr float kShift = 7.0f, kLag = 8.0f;
-
 // The work of a launch, as the kernels and the joining kernel see it.
 struct Plan {
     int group;      // query heads per key/value head
@@ -83,7 +78,7 @@ __device__ __forceinline__ float halves_sum(float x) {
 // stays one, and what a vanished factor scales is far below a float32 step of
 // the sum it joins.
 __device__ __forceinline__ float factor_of(float d) {
-    return fmaxf(__builtin_amdgcn_exp2f(d), 1e-38f);
+    return fmaxf(__builtin_amdgcn_exp2f(d), 2e-38f);
 }
 
 // The conversation whose tiles of R rows include tile `w` of the launch, and
@@ -249,9 +244,16 @@ template <int DIM> struct Filler {
 // (this lane's half of the keys) and unnormalised result.
 template <int DIM, bool F32> struct Rows {
     static constexpr int kParts = F32 ? 2 : 1;
+    // Weights are held as 2^kShift exp(s - m), where m may lag behind the true
+    // maximum by kLag (in powers of two) before the accumulators are rescaled:
+    // 2^15 < 65504 at most.  Binary16's smallest step is then 2^-32 of the
+    // largest weight; float32 rows rescale more often and keep 2^-39, so that
+    // a hundred thousand faint weights beside a strong one keep their sum.
+    static constexpr float kShift = F32 ? 14.0f : 7.0f, kLag = F32 ? 1.0f : 8.0f;
     h8_t q[kParts][DIM / 16];
     f16x_t o[DIM / 32];
     float m, l;
+    float c;    // scores to powers of two
     int p, lo;  // position, first key of the window
 
     __device__ __forceinline__ void clear() {
@@ -275,6 +277,7 @@ template <int DIM, bool F32> struct Rows {
         const int token = rr / group;
         p = position(a, position0, token);
         lo = a.window && p >= a.window ? p - a.window + 1 : 0;
+        c = a.scale * kLog2e;
         const int64_t at = (int64_t)(pl.first + token) * a.q_stride +
                            (int64_t)(hk * group + rr % group) * DIM + 8 * half;
         const u4_t *src = (const u4_t *)((const uint8_t *)a.q + at * (F32 ? 4 : 2));
@@ -285,20 +288,33 @@ template <int DIM, bool F32> struct Rows {
         clear();
     }
     __device__ __forceinline__ void take(const Raw &raw) {
+        int e = 0;
+        if (F32) {
+            // the row's largest element brought into [1/2, 1), so that its parts
+            // are neither infinite nor faint whatever q's magnitude
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kParts * DIM / 4; ++i) {
+                const uint32_t bits = raw.x[i / 4][i % 4];
+                top = fmaxf(top, fabsf(__builtin_bit_cast(float, bits)));
+            }
+            e = __builtin_amdgcn_frexp_expf(halves_max(top));
+            c = __builtin_amdgcn_ldexpf(c, e);
+        }
 #pragma unroll
         for (int s = 0; s < DIM / 16; ++s) {
             if (!F32) {
                 q[0][s] = __builtin_bit_cast(h8_t, raw.x[s]);
-            } else {
+                continue;
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // (a bit cast of the vector's element itself reads element 0)
-                    const uint32_t bits = raw.x[s * kParts + (i / 4) % kParts][i % 4];
-                    const float v = __builtin_bit_cast(float, bits);
-                    const _Float16 hi = (_Float16)v;
-                    q[0][s][i] = hi;
-                    q[kParts - 1][s][i] = (_Float16)(v - (float)hi);
-                }
+            for (int i = 0; i < 8; ++i) {
+                // (a bit cast of the vector's element itself reads element 0)
+                const uint32_t bits = raw.x[s * kParts + (i / 4) % kParts][i % 4];
+                const float v = __builtin_amdgcn_ldexpf(__builtin_bit_cast(float, bits), -e);
+                const _Float16 hi = (_Float16)v;
+                q[0][s][i] = hi;
+                q[kParts - 1][s][i] = (_Float16)(v - (float)hi);
             }
         }
     }
@@ -346,7 +362,7 @@ template <int DIM, bool F32> struct Rows {
     // Scores to weights; maximum, sum and what is accumulated so far brought
     // along.  The sum is of the rounded weights, two at a time.
     template <int KT>
-    __device__ __forceinline__ void weights(Weights<KT> &out, f16x_t (&s)[KT / 32], float c) {
+    __device__ __forceinline__ void weights(Weights<KT> &out, f16x_t (&s)[KT / 32]) {
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t)
@@ -444,11 +460,11 @@ template <int DIM, bool F32> struct Rows {
 
     template <int KT, bool CAREFUL>
     __device__ __forceinline__ void step(const uint8_t *kbuf, const uint8_t *vbuf, int k0,
-                                         bool masked, int sinks, float c) {
+                                         bool masked, int sinks) {
         f16x_t s[KT / 32];
         scores<KT>(s, kbuf, k0, masked, sinks);
         Weights<KT> ws;
-        weights<KT>(ws, s, c);
+        weights<KT>(ws, s);
         mix<KT, CAREFUL>(ws, vbuf, k0, sinks);
     }
 
@@ -508,7 +524,7 @@ template <int DIM, int RW, int KW> struct Pass {
 template <int DIM, bool F32, int RW, int KW, bool CAREFUL>
 __device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
                                           const Reach<Pass<DIM, RW, KW>::KT> &r, int t0, int t1,
-                                          int top_lo, float c, uint8_t *lds) {
+                                          int top_lo, uint8_t *lds) {
     using P = Pass<DIM, RW, KW>;
     constexpr int KT = P::KT, kTile = P::kTile, kGroups = KT / 16;
     constexpr bool kBoth = RW <= kGroups;  // a wave copies K and V of its keys, or one of them
@@ -551,7 +567,7 @@ __device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
         const int k = r.key(t0 + i * KW);
         const uint8_t *kbuf = mine + (i & 1) * 2 * kTile;
         w.template step<KT, CAREFUL>(kbuf, kbuf + kTile, k, CAREFUL || !r.all(k, KT, top_lo),
-                                     r.sinks, c);
+                                     r.sinks);
     }
 }
 
@@ -585,11 +601,10 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
     }
     if (t0 < t1) {
         Filler<DIM> f(a, at.s, hk);
-        const float c = a.scale * kLog2e;
-        pass_loop<DIM, F32, RW, KW, false>(w, f, r, t0, t1, top_lo, c, lds);
+        pass_loop<DIM, F32, RW, KW, false>(w, f, r, t0, t1, top_lo, lds);
         if (__syncthreads_or(w.odd())) {
             w.clear();
-            pass_loop<DIM, F32, RW, KW, true>(w, f, r, t0, t1, top_lo, c, lds);
+            pass_loop<DIM, F32, RW, KW, true>(w, f, r, t0, t1, top_lo, lds);
         }
     }
     float l = halves_sum(w.l), m = w.m;
@@ -670,7 +685,7 @@ constexpr int kStepRows = 32, kStepKeys = 32;
 template <int DIM, bool F32, bool CAREFUL>
 __device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
                                           const Reach<kStepKeys> &r, int t, int t1, int stride,
-                                          int top_lo, float c, uint8_t *kbuf, int look0,
+                                          int top_lo, uint8_t *kbuf, int look0,
                                           int look1, bool started) {
     constexpr int KT = kStepKeys;
     constexpr int kCopies = KT / 16 * Filler<DIM>::kCopies;  // of K, or of V
@@ -716,7 +731,7 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
             counted &= f.fill(r, page1, next + 16, kbuf + kHalf, false);
         }
         typename Rows<DIM, F32>::template Weights<KT> ws;
-        w.template weights<KT>(ws, s, c);
+        w.template weights<KT>(ws, s);
         // outstanding: V, then the next K
         if (counted)
             Q4_WAIT_VMCNT(kCopies);
@@ -733,8 +748,10 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
     }
 }
 
+// (two waves to a SIMD: a second workgroup of four, or one of eight)
 template <int DIM, bool F32, int W>
-__global__ __launch_bounds__(64 * W) void step_kernel(AttentionArgs a, Plan pl, int base) {
+__global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(AttentionArgs a, Plan pl,
+                                                                         int base) {
     constexpr int KT = kStepKeys;
     constexpr int kHalf = 16 * DIM * 2;
     constexpr int kPitch = DIM + 4;
@@ -780,8 +797,7 @@ __global__ __launch_bounds__(64 * W) void step_kernel(AttentionArgs a, Plan pl, 
         }
         w.take(raw);
     }
-    const float c = a.scale * kLog2e;
-    step_loop<DIM, F32, false>(w, f, r, t, t1, W, top_lo, c, mine, look0, look1, true);
+    step_loop<DIM, F32, false>(w, f, r, t, t1, W, top_lo, mine, look0, look1, true);
     if (__any(w.odd())) {
         w.clear();
         if (t < t1) {
@@ -789,7 +805,7 @@ __global__ __launch_bounds__(64 * W) void step_kernel(AttentionArgs a, Plan pl, 
             look0 = f.look(k);
             look1 = f.look(k + 16);
         }
-        step_loop<DIM, F32, true>(w, f, r, t, t1, W, top_lo, c, mine, look0, look1, false);
+        step_loop<DIM, F32, true>(w, f, r, t, t1, W, top_lo, mine, look0, look1, false);
     }
     // join the waves
     w.l = halves_sum(w.l);

@@ -227,6 +227,45 @@ def test_attention_large_scores(half):
     check([(1, 500), (30, 200), (1, 3)], 4, 1, 128, 16, 0, 0, half, seed=1, q_scale=60.0)
 
 
+@pytest.mark.parametrize("lengths", [[(1, 300), (1, 40)], [(90, 120)], [(300, 300)]])
+@pytest.mark.parametrize("magnitude", [1e-12, 1e-4, 1e5, 1e20])
+def test_attention_float32_queries_of_any_magnitude(magnitude, lengths):
+    """Float32 queries far outside binary16's range, the scale bringing the
+    scores back."""
+    kc, vc, q, start, lens, table = batch_inputs(lengths, 4, 2, 128, 16, False, 21)
+    q = (q * np.float32(magnitude)).astype(np.float32)
+    scale = float(np.float32(0.088 / magnitude))
+    ref, absolute, score = block.attend(kc, vc, q, start, lens, table, 0, 0, scale)
+    tk, tv = dev(kc), dev(vc)
+    y = q4.attention(q4.kv_cache(tk, tv), dev(q), dev(start), dev(lens), dev(table), scale=scale)
+    near(y, ref, attention_tol(ref, absolute, score, 300, 128, False))
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("gap", [3.0, 14.0, 18.0])
+def test_attention_many_faint_weights_beside_a_strong_one(gap, half):
+    """The first key takes most of the weight, 40000 equal ones share the rest:
+    their sum, a known value, has to survive."""
+    n, dim = 40001, 64
+    page, pages = 256, 160
+    kc, vc = (torch.zeros(pages, 1, page, dim, dtype=torch.float16, device=DEV) for _ in range(2))
+    kc[0, 0, 0, 0] = 8.0
+    vc[:, 0, :, 1] = 1.0
+    vc[0, 0, 0, 1] = -1.0
+    q = torch.zeros(1, 2, dim, dtype=torch.float16 if half else torch.float32, device=DEV)
+    q[:, :, 0] = gap
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    y = q4.attention(q4.kv_cache(kc, vc), q, torch.tensor([0, 1], dtype=torch.int32, device=DEV),
+                     torch.tensor([n], dtype=torch.int32, device=DEV), table, scale=0.125)
+    faint = (n - 1) * np.exp(-float(q[0, 0, 0]))
+    want = (faint - 1.0) / (faint + 1.0)
+    # equal weights are off by one rounding, alike: of 2^-11, or 2^-16 where they lie
+    # 2^-26 below the strong one; and float32 sums of 40000
+    tol = (H16 if half else 2.0 ** -16) * 4 + n * H32 * 2
+    assert (y[0, :, 1].double() - want).abs().max() < tol + abs(want) * H16 * half
+    assert (y[0, :, 2:] == 0).all()
+
+
 @pytest.mark.parametrize("half", [True, False])
 def test_attention_rows_that_see_nothing(half):
     """More new tokens than cached positions: the first rows see nothing and
