@@ -215,7 +215,7 @@ template <int DIM> struct Filler {
                                          bool is_v) const {
         const uint8_t *src = (is_v ? v : k) + page * page_bytes +
                              (int64_t)((key & ((1 << shift) - 1)) * (DIM * 2));
-        if (page >= 0 && r.each(key, 16)) {
+        if (__builtin_expect(page >= 0 && r.each(key, 16), 1)) {
 #pragma unroll
             for (int j = 0; j < kCopies; ++j) dma16_at(src, off[j], dst + j * 1024);
             return true;
@@ -602,7 +602,7 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
     if (t0 < t1) {
         Filler<DIM> f(a, at.s, hk);
         pass_loop<DIM, F32, RW, KW, false>(w, f, r, t0, t1, top_lo, lds);
-        if (__syncthreads_or(w.odd())) {
+        if (__builtin_expect(__syncthreads_or(w.odd()), 0)) {
             w.clear();
             pass_loop<DIM, F32, RW, KW, true>(w, f, r, t0, t1, top_lo, lds);
         }
@@ -720,7 +720,7 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
         counted = false;
         if (more) {
             i = (i + 1) % 64;
-            if (i == 0) {
+            if (__builtin_expect(i == 0, 0)) {
                 const int mine = r.key(min(t + stride + lane * stride, t1 - 1));
                 look0 = f.look(mine);
                 look1 = f.look(mine + 16);
@@ -798,7 +798,7 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Attenti
         w.take(raw);
     }
     step_loop<DIM, F32, false>(w, f, r, t, t1, W, top_lo, mine, look0, look1, true);
-    if (__any(w.odd())) {
+    if (__builtin_expect(__any(w.odd()), 0)) {
         w.clear();
         if (t < t1) {
             const int k = r.key(min(t + lane * W, t1 - 1));
@@ -977,18 +977,16 @@ Choice choose(const AttentionArgs &a) {
     } else {
         // workgroups that run at once: two to a compute unit, four of 64-wide heads
         const int64_t slots = cus * (dim > 64 ? 2 : 4);
-        if (a.batch == 1) {
-            splits = slots / likely;
-            ch.least = 2 * ch.waves;
-        } else {
-            // Several conversations are of several lengths: more parts than run
-            // at once, so that the long ones do not end alone, but of 1024
-            // keys at least (a part costs about 4 us beside its keys).  64
-            // conversations of 400 to 8192 keys: 217 us unsplit, 205 us so, 221
-            // us in parts of 512; 32 of 4096 keys of 256: 106, 98 and 106 us.
-            splits = (4 * slots + likely - 1) / likely;
-            ch.least = 32;
-        }
+        // One conversation: as many parts as run at once.  Several are of
+        // several lengths: more, so that the long ones do not end alone, but of
+        // 1024 keys at least (a part costs about 4 us beside its keys), or of
+        // what gives every slot one where there are fewer.  64 conversations of
+        // 400 to 8192 keys: 217 us unsplit, 205 us so, 221 us in parts of 512;
+        // 32 of 4096 keys of 256: 106, 98 and 106 us; 2 of 1700 keys: 17 us
+        // unsplit, 10 us in parts of 256.
+        splits = ((a.batch == 1 ? 1 : 4) * slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
+        const int64_t fair = (most * likely + slots - 1) / slots;
+        ch.least = fair > 32 ? 32 : fair < 2 * ch.waves ? 2 * ch.waves : (int)fair;
         // too few keys to split: the workgroup's own waves take them, eight
         // (four) instead of four (two) while there are units to spare
         if (most / ch.least < 2 && likely <= cus) ch.waves *= 2;
