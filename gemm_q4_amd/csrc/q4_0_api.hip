@@ -856,6 +856,6 @@ const char *q4_0_strerror(int status) {
     }
 }
 
-int q4_0_version(void) { return 20000; }
+int q4_0_version(void) { return 20100; }
 
 }  // extern "C"

