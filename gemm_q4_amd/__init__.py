@@ -519,6 +519,17 @@ def _handle(stream):
     return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
+def _new(stream, *args, **kw):
+    """torch.empty for a call on `stream`: what the call alone holds goes back to
+    that stream's pool, where its next owner is ordered after the call."""
+    if stream is None:
+        return torch.empty(*args, **kw)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=kw["device"])
+    with torch.cuda.stream(stream):
+        return torch.empty(*args, **kw)
+
+
 def kv_cache(k, v):
     """Descriptor of a paged cache: k and v float16 [pages, heads, page_size,
     dim] CUDA tensors, which it keeps alive.  Any call here that takes a
@@ -541,7 +552,7 @@ def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
     rotated q [n, q_heads, dim]: q_out, or a new tensor of q's type."""
     if q is not None and q_out is None:
         heads = q.shape[1] if q.dim() == 3 else q.shape[1] // cache.dim
-        q_out = torch.empty((q.shape[0], heads, cache.dim), dtype=q.dtype, device=q.device)
+        q_out = _new(stream, (q.shape[0], heads, cache.dim), dtype=q.dtype, device=q.device)
     _check(_bind.kv_append(cache, rot, q, k, v, positions, slots, q_out, _handle(stream)),
            "q4_0_kv_append")
     return None if q is None else q_out
@@ -553,11 +564,11 @@ def attention(cache, q, q_start, kv_len, table, window: int = 0, sinks: int = 0,
     int32 [batch + 1], kv_len int32 [batch], table int32 [batch, pages of the
     longest].  scale: dim ** -0.5 unless given.  Returns y, like q."""
     if y is None:
-        y = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        y = _new(stream, q.shape, dtype=q.dtype, device=q.device)
     if ws is None:
-        ws = workspace(q4_0_attention_workspace_size(
-            cache, q.shape[1], dtype_code(q), q.shape[0], table.shape[-1], kv_len.shape[0], window,
-            sinks), q.device)
+        need = q4_0_attention_workspace_size(cache, q.shape[1], dtype_code(q), q.shape[0],
+                                             table.shape[-1], kv_len.shape[0], window, sinks)
+        ws = _new(stream, need, dtype=torch.uint8, device=q.device) if need else None
     if scale is None:
         scale = cache.dim ** -0.5
     _check(_bind.attention(cache, q, q_start, kv_len, table, window, sinks, scale, y, ws,
@@ -577,11 +588,16 @@ def residual_norm(h, b=None, pre=None, post=None, gate=None, alpha: float = 1.0,
     if b is None:
         h_out = h
     elif h_out is None:
-        h_out = torch.empty_strided(h.shape, h.stride(), dtype=h.dtype, device=h.device)
+        if h.is_contiguous():
+            h_out = _new(stream, h.shape, dtype=h.dtype, device=h.device)
+        else:           # rows as far apart as h's
+            n, dim = h.shape
+            h_out = _new(stream, (n, max(h.stride(0), dim)), dtype=h.dtype,
+                         device=h.device)[:, :dim]
     if pre is None:
         y = None
     elif y is None:
-        y = torch.empty(h.shape, dtype=y_dtype or torch.float32, device=h.device)
+        y = _new(stream, h.shape, dtype=y_dtype or torch.float32, device=h.device)
     _check(_bind.residual_norm(h, b, pre, post, gate, alpha, eps, weight_offset, h_out, y,
                                _handle(stream)), "q4_0_residual_norm")
     return h_out, y

@@ -496,6 +496,39 @@ def test_block_operators_on_another_stream_and_replayed():
             assert torch.equal(g, e), i
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_conveniences_on_a_given_stream(handle):
+    """Outputs and workspaces that a call on another stream allocates are not
+    given away before it has run: many calls in flight there, with allocations
+    on the current stream in between."""
+    torch.manual_seed(3)
+    k, v = (torch.randn(300, 2, 16, 64, device=DEV).half() for _ in range(2))
+    cache = q4.kv_cache(k, v)
+    q = torch.randn(1, 4, 64, device=DEV)
+    start = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([4700], dtype=torch.int32, device=DEV)
+    table = torch.arange(300, dtype=torch.int32, device=DEV)[None]
+    h, w = torch.randn(3, 256, device=DEV), torch.ones(256, device=DEV)
+    assert q4.q4_0_attention_workspace_size(cache, 4, q4.F32, 1, 300, 1) > 0
+    want = q4.attention(cache, q, start, lens, table), q4.residual_norm(h, h * 2, w, w)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    torch.cuda.synchronize()
+    got = []
+    twice = h * 2
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got.append((q4.attention(cache, q, start, lens, table, stream=stream),
+                    q4.residual_norm(h, twice, w, w, stream=stream)))
+        for size in (1 << 12, 1 << 16, 1 << 20):
+            torch.empty(size, dtype=torch.uint8, device=DEV).fill_(255)
+        side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for y, (oh, oy) in got:
+        assert torch.equal(y, want[0]) and torch.equal(oy, want[1][1])
+        assert torch.equal(oh, want[1][0])
+
+
 def test_workspace_contents_do_not_matter():
     k, v = (torch.randn(64, 2, 16, 64, device=DEV).half() for _ in range(2))
     cache = q4.kv_cache(k, v)
