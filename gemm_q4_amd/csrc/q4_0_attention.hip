@@ -179,7 +179,10 @@ template <int KT> struct Reach {
 // Copies of 16 key rows into LDS.  One copy moves 1 KB (512 / DIM rows).  Pages
 // are looked up 64 tiles at a time, one to a lane, so that the loop reads its
 // page from a register and never waits for the table.
-template <int DIM> struct Filler {
+// ONCE: every key is read by one workgroup, and the copies carry the
+// non-temporal hint (131071 keys: 94 us without, 83 us with; 64 conversations
+// 206 and 183 us).  Where other tiles read the same keys it gains nothing.
+template <int DIM, bool ONCE> struct Filler {
     static constexpr int kCopies = DIM / 32;
     uint32_t off[kCopies];
     const uint8_t *k, *v;  // of this head, on page 0
@@ -217,7 +220,12 @@ template <int DIM> struct Filler {
                              (int64_t)((key & ((1 << shift) - 1)) * (DIM * 2));
         if (__builtin_expect(page >= 0 && r.each(key, 16), 1)) {
 #pragma unroll
-            for (int j = 0; j < kCopies; ++j) dma16_at(src, off[j], dst + j * 1024);
+            for (int j = 0; j < kCopies; ++j) {
+                if (ONCE)
+                    dma16_once_at(src, off[j], dst + j * 1024);
+                else
+                    dma16_at(src, off[j], dst + j * 1024);
+            }
             return true;
         }
         // No page: NaN keys for the rows that see them.  Rows that no row of
@@ -530,7 +538,7 @@ template <int DIM, int RW, int KW> struct Pass {
 };
 
 template <int DIM, bool F32, int RW, int KW, bool CAREFUL>
-__device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
+__device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM, false> &f,
                                           const Reach<Pass<DIM, RW, KW>::KT> &r, int t0, int t1,
                                           int top_lo, uint8_t *lds) {
     using P = Pass<DIM, RW, KW>;
@@ -608,7 +616,7 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
         w.take(raw);
     }
     if (t0 < t1) {
-        Filler<DIM> f(a, at.s, hk);
+        Filler<DIM, false> f(a, at.s, hk);
         pass_loop<DIM, F32, RW, KW, false>(w, f, r, t0, t1, top_lo, lds);
         if (__builtin_expect(__syncthreads_or(w.odd()), 0)) {
             w.clear();
@@ -690,18 +698,17 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
 // The waves' results are joined through LDS at the end.
 //
 // Bound by the bytes of K and V: one conversation of 131071 keys (32 + 8 heads of
-// 128) in 94 us, 5.7 TB/s, and 5 us for joining its parts, where a plain
-// streaming read of 512 MiB reaches 5.2; two stages a wave instead of one tile
-// refilled in parts: 96 us.
+// 128) in 83 us, 6.5 TB/s, and 5 us for joining its parts, where a plain
+// streaming read of 512 MiB reaches 7.1.
 constexpr int kStepRows = 32, kStepKeys = 32;
 
 template <int DIM, bool F32, bool CAREFUL>
-__device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM> &f,
+__device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM, true> &f,
                                           const Reach<kStepKeys> &r, int t, int t1, int stride,
                                           int top_lo, uint8_t *kbuf, int look0,
                                           int look1, bool started) {
     constexpr int KT = kStepKeys;
-    constexpr int kCopies = KT / 16 * Filler<DIM>::kCopies;  // of K, or of V
+    constexpr int kCopies = KT / 16 * Filler<DIM, true>::kCopies;  // of K, or of V
     constexpr int kHalf = 16 * DIM * 2;
     uint8_t *vbuf = kbuf + 2 * kHalf;
     const int lane = threadIdx.x % 64;
@@ -787,7 +794,7 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Attenti
     const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     uint8_t *mine = lds + wave * kShare;
-    Filler<DIM> f(a, at.s, hk);
+    Filler<DIM, true> f(a, at.s, hk);
     Rows<DIM, F32> w;
     const int t = t0 + wave;
     int look0 = -1, look1 = -1;
