@@ -187,15 +187,17 @@ hipError_t run(const NormArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Waves per row: the fewest that hold the row in two chunks a lane, so that a
-// row's loads are all in flight at once; 16 waves and up to eight chunks above.
+// Waves per row: up to eight, two chunks a lane, so that a row's loads are all
+// in flight at once and one row alone is short; then more chunks (rows of 5120,
+// 16383 of them: 196 us on eight waves, 204 on sixteen, 221 on four), and
+// sixteen waves only for what eight cannot hold.
 template <bool RAGGED, bool BF16, bool YF16>
 hipError_t by_size(const NormArgs &a, hipStream_t stream) {
     const int lanes = (a.dim + 3) / 4;
     if (lanes <= 128) return run<1, 2, RAGGED, BF16, YF16>(a, stream);
     if (lanes <= 512) return run<4, 2, RAGGED, BF16, YF16>(a, stream);
     if (lanes <= 1024) return run<8, 2, RAGGED, BF16, YF16>(a, stream);
-    if (lanes <= 2048) return run<16, 2, RAGGED, BF16, YF16>(a, stream);
+    if (lanes <= 2048) return run<8, 4, RAGGED, BF16, YF16>(a, stream);
     static_assert(kNormMaxDim == 16 * 64 * 4 * 8, "eight chunks hold the widest row");
     return run<16, 8, RAGGED, BF16, YF16>(a, stream);
 }
