@@ -1001,9 +1001,10 @@ Choice choose(const AttentionArgs &a) {
         // several lengths: more, so that the long ones do not end alone, but of
         // 1024 keys at least (a part costs about 4 us beside its keys), or of
         // what gives every slot one where there are fewer.  64 conversations of
-        // 400 to 8192 keys: 217 us unsplit, 205 us so, 221 us in parts of 512;
-        // 32 of 4096 keys of 256: 106, 98 and 106 us; 2 of 1700 keys: 17 us
-        // unsplit, 10 us in parts of 256.
+        // 400 to 8192 keys, joining included: 209 us unsplit, 187 us so, 203 us
+        // in parts of 512; 32 of 4096 keys of 256: 95 us in three parts, 94 us
+        // in four, 105 us in eight; 2 of 1700 keys: 17 us unsplit, 10 us in
+        // parts of 256.
         splits = ((a.batch == 1 ? 1 : 4) * slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
         const int64_t fair = (most * likely + slots - 1) / slots;
         ch.least = fair > 32 ? 32 : fair < 2 * ch.waves ? 2 * ch.waves : (int)fair;

@@ -5,7 +5,7 @@
 // CH chunks of VEC elements to a lane, and the two sums of squares (of the
 // block's output, then of the new residual) are reductions over those waves.
 // Bound by the bytes of b, h, h_out and y, each read or written once: 16383 rows
-// of 5120 (binary16 b and y) in 200 us, 5.0 TB/s, where a copy of as many bytes
+// of 5120 (binary16 b and y) in 196 us, 5.1 TB/s, where a copy of as many bytes
 // reaches 4.8 to 5.4; rows of 5119 take 4 % longer.  One row of 2560 takes
 // 3.2 us, one launch.
 #include "q4_0_device.h"
