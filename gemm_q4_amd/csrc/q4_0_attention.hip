@@ -589,7 +589,9 @@ __device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM, false> 
 
 template <int DIM, bool F32, int RW, int KW>
 __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
-                             (Pass<DIM, RW, KW>::kWavesPerSimd)) void pass_kernel(AttentionArgs a, Plan pl, int base) {
+                             (Pass<DIM, RW, KW>::kWavesPerSimd)) void pass_kernel(AttentionArgs a,
+                                                                                  Plan pl,
+                                                                                  int base) {
     using P = Pass<DIM, RW, KW>;
     __shared__ __align__(1024) uint8_t lds[P::kLds];
     __shared__ float ml[2][KW][32 * RW];

@@ -282,6 +282,39 @@ def test_attention_long_axis(lengths, half):
     check(lengths, 8, 2, 64, 16, 700, 40, half, seed=12)
 
 
+@pytest.mark.parametrize("count,tokens,longest", [(65, 1, 90), (150, 1, 40), (300, 3, 30),
+                                                  (4500, 1, 9), (130, 40, 50)])
+def test_attention_many_conversations(count, tokens, longest):
+    """More conversations than one look of 64 lanes finds, empty ones among
+    them, and leading tokens that none of them holds."""
+    rng = np.random.default_rng(count)
+    kvs = rng.integers(0, longest + 1, count)
+    news = np.minimum(kvs, rng.integers(0, tokens + 1, count))
+    lengths = [(int(a), int(b)) for a, b in zip(news, kvs)]
+    kc, vc, q, start, lens, table = batch_inputs(lengths, 2, 1, 64, 16, True, 5)
+    spare = 3
+    q = np.concatenate([q[:spare], q])
+    start = start + np.int32(spare)
+    ref, absolute, score = block.attend(kc, vc, q, start, lens, table, 0, 0, 0.125)
+    tk, tv = dev(kc), dev(vc)
+    y = torch.full(q.shape, 9.0, dtype=torch.float16, device=DEV)
+    q4.attention(q4.kv_cache(tk, tv), dev(q), dev(start), dev(lens), dev(table), y=y)
+    assert (y[:spare] == 9.0).all()
+    near(y[spare:], ref[spare:], attention_tol(ref[spare:], absolute[spare:], score[spare:],
+                                               longest, 64, True))
+
+
+def test_attention_long_batch_with_split_parts():
+    """More than 64 conversations whose key axes are split: the joining kernel
+    finds their tokens too."""
+    rng = np.random.default_rng(2)
+    lengths = [(1, int(n)) for n in rng.integers(1, 60, 70)] + [(1, 2600), (0, 0), (1, 1700)]
+    assert q4.q4_0_attention_workspace_size(
+        q4.q4_0_kv_cache(0, 0, 500, 1, 16, 64), 2, q4.F16, 72, 163, 73) > 0
+    check(lengths, 2, 1, 64, 16, 0, 0, True, seed=6)
+    check(lengths, 2, 1, 64, 16, 1500, 33, False, seed=7)
+
+
 @pytest.mark.parametrize("half", [True, False])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_attention_non_finite_values_in_masked_places(dim, half):
@@ -611,3 +644,17 @@ def test_calls_refuse_tensors_on_the_host():
         q4.residual_norm(kv[0], kv[0], torch.ones(64))
     with pytest.raises(ValueError):
         q4.kv_append(c, None, q, kv, kv, None, slots.cpu())
+
+
+def test_first_calls_of_a_process_capture_into_a_graph():
+    import json
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, os.path.join(here, "cold_capture_block.py")],
+                       capture_output=True, text=True, timeout=100)
+    print(r.stdout[-2000:], r.stderr[-2000:], flush=True)
+    assert r.returncode == 0
+    res = json.loads(r.stdout.strip().splitlines()[-1])
+    assert len(res) == 7 and all(res.values()), res
