@@ -218,6 +218,9 @@ PyObject *make_cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const auto s = k->sizes();
         if (s.size() != 4)
             bad_value("k must be [pages, heads, page_size, dim], not " + text(s));
+        // (a call divides by dim before the C entry sees it)
+        for (const int64_t d : s)
+            if (d < 1) bad_value("a cache has no empty dimension: " + text(s));
         void *kp = dense(*k, "k", at::kHalf, s), *vp = dense(*v, "v", at::kHalf, s);
         if (k->device() != v->device()) bad_value("k and v are on different devices");
         Cache *c = (Cache *)g_cache_type->tp_alloc(g_cache_type, 0);
