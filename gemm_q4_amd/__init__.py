@@ -532,7 +532,8 @@ def _new(stream, *args, **kw):
 
 def kv_cache(k, v):
     """Descriptor of a paged cache: k and v float16 [pages, heads, page_size,
-    dim] CUDA tensors, which it keeps alive.  Any call here that takes a
+    dim] CUDA tensors, which it keeps alive and reads anew at every use, so
+    that one whose data was replaced is followed.  Any call here that takes a
     q4_0_kv_cache takes it too."""
     return _bind.kv_cache(k, v)
 
@@ -540,8 +541,8 @@ def kv_cache(k, v):
 def rotary(inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q_norm=None,
            k_norm=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """Descriptor of a rotation (inv_freq: float32 [rot_dim / 2], or None) and of
-    per-head norms (float32 [dim] weights, or None); it keeps the tensors
-    alive."""
+    per-head norms (float32 [dim] weights, or None); it keeps the tensors alive
+    and reads them anew at every use, as kv_cache() does."""
     return _bind.rotary(inv_freq, interleaved, amplitude, q_norm, k_norm, eps, weight_offset)
 
 

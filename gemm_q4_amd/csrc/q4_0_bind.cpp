@@ -146,7 +146,9 @@ void want(Py_ssize_t have, Py_ssize_t need) {
 }
 
 // ---- descriptors ------------------------------------------------------------
-// Objects that hold a descriptor of q4_0.h and the tensors behind it.
+// Objects that hold a descriptor of q4_0.h and the tensors behind it.  What a
+// tensor holds may be replaced at any time (Module.to gives its parameters new
+// memory), so every use forms the descriptor again from the tensors.
 struct Cache {
     PyObject_HEAD
     q4_0_kv_cache c;
@@ -160,6 +162,45 @@ struct Rotary {
     PyObject *inv_freq, *q_norm, *k_norm;
 };
 PyTypeObject *g_cache_type, *g_rotary_type;
+
+q4_0_kv_cache read_cache(PyObject *ko, PyObject *vo) {
+    const at::Tensor *k = tensor(ko, "k"), *v = tensor(vo, "v");
+    const auto s = k->sizes();
+    if (s.size() != 4) bad_value("k must be [pages, heads, page_size, dim], not " + text(s));
+    // (a call divides by dim before the C entry sees it)
+    for (const int64_t d : s)
+        if (d < 1) bad_value("a cache has no empty dimension: " + text(s));
+    void *kp = dense(*k, "k", at::kHalf, s), *vp = dense(*v, "v", at::kHalf, s);
+    if (k->device() != v->device()) bad_value("k and v are on different devices");
+    return {kp, vp, s[0], s[1], s[2], s[3]};
+}
+
+// inv_freq, q_norm and k_norm into `o`'s fields; the rest of it stays.
+void read_rotary(Rotary &o, PyObject *inv_freq, PyObject *q_norm, PyObject *k_norm) {
+    int dev = -1;
+    const auto take = [&](PyObject *t, const char *name, int64_t &length) -> const float * {
+        const at::Tensor *x = tensor(t, name, true);
+        if (!x) return nullptr;
+        if (x->dim() != 1) bad_value(std::string(name) + " must have one dimension");
+        const float *p = (const float *)dense(*x, name, at::kFloat, x->sizes());
+        const int d = x->is_cuda() ? x->get_device() : -2;
+        if (dev != -1 && d != dev) bad_value("the rotation's tensors are on different devices");
+        dev = d;
+        length = x->size(0);
+        return p;
+    };
+    int64_t half = 0, ql = 0, kl = 0;
+    o.r.inv_freq = take(inv_freq, "inv_freq", half);
+    o.r.rot_dim = 2 * half;
+    o.r.q_norm = take(q_norm, "q_norm", ql);
+    o.r.k_norm = take(k_norm, "k_norm", kl);
+    if (ql && kl && ql != kl) bad_value("q_norm and k_norm have different lengths");
+    o.norm_dim = ql ? ql : kl;
+    o.device = dev;
+}
+
+void refresh(Cache &c) { c.c = read_cache(c.k, c.v); }
+void refresh(Rotary &r) { read_rotary(r, r.inv_freq, r.q_norm, r.k_norm); }
 
 template <typename T> void drop(PyObject *self, std::initializer_list<PyObject **> held) {
     for (PyObject **p : held) Py_CLEAR(*p);
@@ -176,12 +217,23 @@ void rotary_free(PyObject *self) {
     drop<Rotary>(self, {&r->inv_freq, &r->q_norm, &r->k_norm});
 }
 
-PyObject *cache_address(PyObject *self, void *) { return PyLong_FromVoidPtr(&((Cache *)self)->c); }
+PyObject *cache_address(PyObject *self, void *) {
+    return guarded([&]() -> PyObject * {
+        refresh(*(Cache *)self);
+        return PyLong_FromVoidPtr(&((Cache *)self)->c);
+    });
+}
 PyObject *cache_field(PyObject *self, void *at) {
-    return PyLong_FromLongLong(*(int64_t *)((char *)&((Cache *)self)->c + (size_t)at));
+    return guarded([&]() -> PyObject * {
+        refresh(*(Cache *)self);
+        return PyLong_FromLongLong(*(int64_t *)((char *)&((Cache *)self)->c + (size_t)at));
+    });
 }
 PyObject *rotary_address(PyObject *self, void *) {
-    return PyLong_FromVoidPtr(&((Rotary *)self)->r);
+    return guarded([&]() -> PyObject * {
+        refresh(*(Rotary *)self);
+        return PyLong_FromVoidPtr(&((Rotary *)self)->r);
+    });
 }
 PyGetSetDef cache_fields[] = {
     {"address", cache_address, nullptr, "address of the descriptor", nullptr},
@@ -214,18 +266,10 @@ PyObject *held(PyObject *o) {
 PyObject *make_cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         want(n, 2);
-        const at::Tensor *k = tensor(a[0], "k"), *v = tensor(a[1], "v");
-        const auto s = k->sizes();
-        if (s.size() != 4)
-            bad_value("k must be [pages, heads, page_size, dim], not " + text(s));
-        // (a call divides by dim before the C entry sees it)
-        for (const int64_t d : s)
-            if (d < 1) bad_value("a cache has no empty dimension: " + text(s));
-        void *kp = dense(*k, "k", at::kHalf, s), *vp = dense(*v, "v", at::kHalf, s);
-        if (k->device() != v->device()) bad_value("k and v are on different devices");
+        const q4_0_kv_cache read = read_cache(a[0], a[1]);
         Cache *c = (Cache *)g_cache_type->tp_alloc(g_cache_type, 0);
         if (!c) throw Raised();
-        c->c = {kp, vp, s[0], s[1], s[2], s[3]};
+        c->c = read;
         c->k = held(a[0]);
         c->v = held(a[1]);
         return (PyObject *)c;
@@ -236,40 +280,19 @@ PyObject *make_cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *make_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         want(n, 7);
-        q4_0_rotary r = {};
-        int64_t dim = 0;
-        int dev = -1;
-        const auto take = [&](PyObject *o, const char *name) -> const float * {
-            const at::Tensor *t = tensor(o, name, true);
-            if (!t) return nullptr;
-            if (t->dim() != 1) bad_value(std::string(name) + " must have one dimension");
-            const float *p = (const float *)dense(*t, name, at::kFloat, t->sizes());
-            const int d = t->is_cuda() ? t->get_device() : -2;
-            if (dev != -1 && d != dev) bad_value("the rotation's tensors are on different devices");
-            dev = d;
-            return p;
-        };
-        r.inv_freq = take(a[0], "inv_freq");
-        if (r.inv_freq) r.rot_dim = 2 * tensor(a[0], "inv_freq")->numel();
+        Rotary read = {};
+        read_rotary(read, a[0], a[3], a[4]);
         const int inter = PyObject_IsTrue(a[1]);
         if (inter < 0) throw Raised();
-        r.interleaved = inter;
-        r.amplitude = number(a[2]);
-        r.q_norm = take(a[3], "q_norm");
-        r.k_norm = take(a[4], "k_norm");
-        r.eps = number(a[5]);
-        r.weight_offset = number(a[6]);
-        for (int i = 3; i < 5; ++i) {
-            if (a[i] == Py_None) continue;
-            const int64_t d = tensor(a[i], "norm")->numel();
-            if (dim && d != dim) bad_value("q_norm and k_norm have different lengths");
-            dim = d;
-        }
+        read.r.interleaved = inter;
+        read.r.amplitude = number(a[2]);
+        read.r.eps = number(a[5]);
+        read.r.weight_offset = number(a[6]);
         Rotary *o = (Rotary *)g_rotary_type->tp_alloc(g_rotary_type, 0);
         if (!o) throw Raised();
-        o->r = r;
-        o->norm_dim = dim;
-        o->device = dev;
+        o->r = read.r;
+        o->norm_dim = read.norm_dim;
+        o->device = read.device;
         o->inv_freq = held(a[0]);
         o->q_norm = held(a[3]);
         o->k_norm = held(a[4]);
@@ -279,6 +302,7 @@ PyObject *make_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 const Cache &cache_of(PyObject *o) {
     if (!PyObject_TypeCheck(o, g_cache_type)) bad_type("cache must come from kv_cache()");
+    refresh(*(Cache *)o);
     return *(const Cache *)o;
 }
 
@@ -291,6 +315,7 @@ PyObject *call_append(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
         const Rotary *rot = nullptr;
         if (a[1] != Py_None) {
             if (!PyObject_TypeCheck(a[1], g_rotary_type)) bad_type("rot must come from rotary()");
+            refresh(*(Rotary *)a[1]);
             rot = (const Rotary *)a[1];
         }
         const at::Tensor *q = tensor(a[2], "q", true), *k = tensor(a[3], "k"),

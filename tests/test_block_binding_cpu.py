@@ -13,3 +13,53 @@ def test_caches_without_elements_are_refused(shape):
     k = torch.zeros(shape, dtype=torch.float16)
     with pytest.raises(ValueError, match="no empty dimension"):
         q4.kv_cache(k, k.clone())
+
+
+def test_descriptors_follow_their_tensors():
+    """A parameter moved or cast holds other memory afterwards: the descriptor
+    gives the new memory, or refuses it, and never the old one's address."""
+    k, v = (torch.zeros(2, 2, 16, 64, dtype=torch.float16) for _ in range(2))
+    cache = q4.kv_cache(k, v)
+    at = lambda: q4.q4_0_kv_cache.from_address(cache.address)
+    assert (at().k, at().v) == (k.data_ptr(), v.data_ptr())
+    k.data = torch.ones(2, 2, 16, 64, dtype=torch.float16)
+    assert (at().k, at().v) == (k.data_ptr(), v.data_ptr())
+    k.data, v.data = (torch.zeros(3, 1, 32, 128, dtype=torch.float16) for _ in range(2))
+    assert (at().k, at().v) == (k.data_ptr(), v.data_ptr())
+    assert (cache.pages, cache.heads, cache.page_size, cache.dim) == (3, 1, 32, 128)
+    v.data = torch.zeros(2, 2, 16, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="v must have shape"):
+        cache.address
+    with pytest.raises(ValueError, match="v must have shape"):
+        cache.dim
+    v.data = torch.zeros(3, 1, 32, 128)
+    with pytest.raises(TypeError, match="v must be Half"):
+        cache.address
+
+    inv, norm = torch.ones(32), torch.nn.Parameter(torch.ones(64), requires_grad=False)
+    rot = q4.rotary(inv, interleaved=True, amplitude=0.5, q_norm=norm, eps=1e-3, weight_offset=1.0)
+    at = lambda: q4.q4_0_rotary.from_address(rot.address)
+    assert (at().inv_freq, at().q_norm, at().k_norm) == (inv.data_ptr(), norm.data_ptr(), None)
+    norm.data = torch.full((128,), 2.0)
+    inv.data = torch.ones(16)
+    assert (at().inv_freq, at().q_norm, at().rot_dim) == (inv.data_ptr(), norm.data_ptr(), 32)
+    assert (at().interleaved, at().amplitude, at().weight_offset) == (1, 0.5, 1.0)
+    assert abs(at().eps - 1e-3) < 1e-9
+    norm.data = norm.data.double()
+    with pytest.raises(TypeError, match="q_norm must be Float"):
+        rot.address
+
+
+def test_calls_read_a_descriptor_whose_tensors_changed():
+    """A call sees the tensors as they are now, before anything else of it."""
+    k, v = (torch.zeros(2, 2, 16, 64, dtype=torch.float16) for _ in range(2))
+    cache, norm = q4.kv_cache(k, v), torch.ones(64)
+    rot = q4.rotary(q_norm=norm)
+    q, kv = torch.zeros(3, 4, 64), torch.zeros(3, 2, 64)
+    slots = torch.zeros(3, dtype=torch.int64)
+    norm.data = torch.ones(32)
+    with pytest.raises(ValueError, match="norm weights of 32 do not fit heads of 64"):
+        q4.kv_append(cache, rot, q, kv, kv, None, slots)
+    v.data = torch.zeros(2, 2, 16, 64)
+    with pytest.raises(TypeError, match="v must be Half"):
+        q4.kv_append(cache, None, q, kv, kv, None, slots, q_out=q.clone())
