@@ -162,8 +162,11 @@ _bind.setup(*(ctypes.cast(getattr(_lib, _name), _vp).value
 def _stream(stream, *tensors):
     if stream is None:
         for t in tensors:
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                return _raw_stream(t.get_device())
+            if isinstance(t, torch.Tensor):
+                if t.is_cuda:
+                    return _raw_stream(t.get_device())
+            elif getattr(t, "is_cuda", False):      # a storage, a wrapper
+                return torch.cuda.current_stream(t.device).cuda_stream
         return None
     if isinstance(stream, int):
         return stream

@@ -63,3 +63,24 @@ def test_calls_read_a_descriptor_whose_tensors_changed():
     v.data = torch.zeros(2, 2, 16, 64)
     with pytest.raises(TypeError, match="v must be Half"):
         q4.kv_append(cache, None, q, kv, kv, None, slots, q_out=q.clone())
+
+
+class Wrapper:
+    """Device memory that is no tensor, as a storage or another library's array is."""
+    is_cuda, device = True, torch.device("cuda", 0)
+
+    def data_ptr(self):
+        return 1 << 36
+
+
+def test_device_memory_that_is_no_tensor_goes_to_the_current_stream(monkeypatch):
+    """Any argument that says it is on a GPU brings torch's current stream of its
+    device, not the null stream."""
+    class Stream:
+        cuda_stream = 0x5150
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: asked.append(d) or Stream)
+    assert q4._stream(None, 1 << 36, Wrapper()) == 0x5150
+    assert asked == [torch.device("cuda", 0)]
+    assert q4._stream(None, 1 << 36, torch.zeros(1), None) is None
+    assert q4._stream(7, Wrapper()) == 7
