@@ -32,11 +32,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # Q4_0_LIBRARY names another build of the same library (a tuning variant)
 LIB_PATH = os.environ.get("Q4_0_LIBRARY") or os.path.join(_HERE, "libq4_0.so")
 
-for _path in (LIB_PATH, os.path.join(_HERE, "_bind.so")):
-    if not os.path.exists(_path):
-        raise ImportError(
-            f"{_path} is missing: build the HIP library first "
-            "(python -c 'import __graft_entry__ as g; g.build()')")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(
+        f"{LIB_PATH} is missing: build the HIP library first "
+        "(python -c 'import __graft_entry__ as g; g.build()')")
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -152,11 +151,37 @@ def _nbytes(ws, workspace_bytes):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
-from . import _bind  # noqa: E402  (torch is loaded; built beside the library)
 
-_bind.setup(*(ctypes.cast(getattr(_lib, _name), _vp).value
-              for _name in ("q4_0_kv_append", "q4_0_attention", "q4_0_residual_norm")),
-            _raw_stream)
+class _Unusable:
+    """Stands for the extension module where it cannot be used: every use of it
+    says why.  The products and the C calls need libq4_0.so alone."""
+
+    def __init__(self, reason):
+        self._reason = reason
+
+    def __getattr__(self, name):
+        raise ImportError(f"the block operators' conveniences need gemm_q4_amd/_bind.so: "
+                          f"{self._reason}; build it again "
+                          "(python -c 'import __graft_entry__ as g; g.build()')")
+
+
+def _load_bind():
+    """The conveniences' extension module.  It is built against one torch, whose
+    C++ interface another does not keep."""
+    try:
+        from . import _bind
+    except ImportError as e:
+        return _Unusable(str(e))
+    if _bind.torch_version != torch.__version__:
+        return _Unusable(f"it was built with torch {_bind.torch_version}, this is torch "
+                         f"{torch.__version__}")
+    _bind.setup(*(ctypes.cast(getattr(_lib, name), _vp).value
+                  for name in ("q4_0_kv_append", "q4_0_attention", "q4_0_residual_norm")),
+                _raw_stream)
+    return _bind
+
+
+_bind = _load_bind()
 
 
 def _stream(stream, *tensors):

@@ -458,5 +458,7 @@ PyMODINIT_FUNC PyInit__bind(void) {
     g_cache_type = (PyTypeObject *)PyType_FromSpec(&cache_spec);
     g_rotary_type = (PyTypeObject *)PyType_FromSpec(&rotary_spec);
     if (!g_cache_type || !g_rotary_type) return nullptr;
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", Q4_0_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
 }

@@ -1,6 +1,11 @@
 """The block operators' conveniences without a GPU: what they refuse and with
 which message, descriptors whose tensors change, and the package where their
 extension module is missing."""
+import os
+import shutil
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -84,3 +89,48 @@ def test_device_memory_that_is_no_tensor_goes_to_the_current_stream(monkeypatch)
     assert asked == [torch.device("cuda", 0)]
     assert q4._stream(None, 1 << 36, torch.zeros(1), None) is None
     assert q4._stream(7, Wrapper()) == 7
+
+
+USE = """
+import ctypes, sys
+sys.path.insert(0, {root!r})
+import torch
+import gemm_q4_amd as q4
+assert q4.__file__.startswith({root!r})
+assert q4.q4_0_blocks_bytes(2, 64) == 72
+assert q4.q4_0_select_kernel(1, 64, 64, q4.F32) > 0
+c = q4.q4_0_kv_cache(0, 0, 500, 1, 16, 64)
+assert q4.q4_0_attention_workspace_size(c, 2, q4.F16, 72, 163, 73) >= 0
+k = torch.zeros(1, 1, 16, 64, dtype=torch.float16)
+h = torch.zeros(1, 64)
+for call in (lambda: q4.kv_cache(k, k.clone()), lambda: q4.rotary(),
+             lambda: q4.residual_norm(h, h, h[0])):
+    try:
+        call()
+    except ImportError as e:
+        print(e)
+    else:
+        raise SystemExit("not refused")
+"""
+
+
+@pytest.mark.parametrize("extension,reason", [
+    (None, "_bind"),
+    ("raise ImportError('undefined symbol: x')", "undefined symbol"),
+    ("torch_version = '0.1'", "built with torch 0.1, this is torch " + torch.__version__),
+])
+def test_products_do_not_need_the_extension_module(tmp_path, extension, reason):
+    """Where the conveniences' module is missing, does not load or was built with
+    another torch, the package imports and its products and C calls are there;
+    the conveniences say what is wrong."""
+    package = tmp_path / "gemm_q4_amd"
+    package.mkdir()
+    shutil.copy(q4.__file__, package / "__init__.py")
+    if extension:
+        (package / "_bind.py").write_text(extension)
+    r = subprocess.run([sys.executable, "-c", USE.format(root=str(tmp_path))], cwd=tmp_path,
+                       env={**os.environ, "Q4_0_LIBRARY": q4.LIB_PATH, "PYTHONPATH": ""},
+                       capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0, r.stderr
+    lines = r.stdout.strip().splitlines()
+    assert len(lines) == 3 and all(reason in line and "build it again" in line for line in lines)
