@@ -25,6 +25,8 @@
 // of the tile sees are read; a row of a group that none sees is taken from a
 // zero block, so whatever a page holds past its conversation's end never meets
 // the arithmetic.
+#include <float.h>
+
 #include "q4_0_device.h"
 #include "q4_0_dma.h"
 #include "q4_0_internal.h"
@@ -79,6 +81,14 @@ __device__ __forceinline__ float halves_sum(float x) {
 // the sum it joins.
 __device__ __forceinline__ float factor_of(float d) {
     return fmaxf(__builtin_amdgcn_exp2f(d), 2e-38f);
+}
+
+// The factor of scores, kept a number other than 0 whatever scale and q are: as 0
+// it would make a masked score (minus infinity) NaN, as infinity a score of 0.
+// Below this range every visible key weighs the same, above it only equal
+// scores do, with the factor or without.
+__device__ __forceinline__ float finite(float c) {
+    return __builtin_amdgcn_fmed3f(c, FLT_MIN, FLT_MAX);
 }
 
 // The conversation whose tiles of R rows include tile `w` of the launch, and
@@ -285,7 +295,7 @@ template <int DIM, bool F32> struct Rows {
         const int token = rr / group;
         p = position(a, position0, token);
         lo = a.window && p >= a.window ? p - a.window + 1 : 0;
-        c = a.scale * kLog2e;
+        c = finite(a.scale * kLog2e);
         const int64_t at = (int64_t)(pl.first + token) * a.q_stride +
                            (int64_t)(hk * group + rr % group) * DIM + 8 * half;
         const u4_t *src = (const u4_t *)((const uint8_t *)a.q + at * (F32 ? 4 : 2));
@@ -307,7 +317,7 @@ template <int DIM, bool F32> struct Rows {
                 top = fmaxf(top, fabsf(__builtin_bit_cast(float, bits)));
             }
             e = __builtin_amdgcn_frexp_expf(halves_max(top));
-            c = __builtin_amdgcn_ldexpf(c, e);
+            c = finite(__builtin_amdgcn_ldexpf(c, e));
         }
 #pragma unroll
         for (int s = 0; s < DIM / 16; ++s) {

@@ -11,7 +11,7 @@ import torch
 
 import gemm_q4_amd as q4
 from oracle import block
-from test_gpu_block import DEV, H16, append_tol, dev, near
+from test_gpu_block import DEV, H16, append_tol, attention_tol, dev, near
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,44 @@ def test_calls_follow_replaced_tensors():
          append_tol(rk[0, :, :n].transpose(1, 0, 2), rows.reshape(n, heads, dim), True, wanted,
                     False))
     near(vc, rv, np.abs(rv) * H16)
+
+
+# ---- attention: scores of any size -------------------------------------------
+def plain(lengths, dim, seed, pages=20):
+    """Caches of `pages` pages of 16 keys and 2 heads, the lengths' tables."""
+    rng = np.random.default_rng(seed)
+    kc, vc = (rng.standard_normal((pages, 2, 16, dim)).astype(np.float16) for _ in range(2))
+    width = max((kv + 15) // 16 for _, kv in lengths)
+    table = rng.integers(0, pages, (len(lengths), width)).astype(np.int32)
+    start = np.concatenate([[0], np.cumsum([new for new, _ in lengths])]).astype(np.int32)
+    return rng, kc, vc, start, np.array([kv for _, kv in lengths], np.int32), table
+
+
+def attend(kc, vc, q, start, lens, table, window=0, sinks=0, scale=1.0):
+    tk, tv = dev(kc), dev(vc)
+    y = q4.attention(q4.kv_cache(tk, tv), dev(q), dev(start), dev(lens), dev(table), window, sinks,
+                     scale)
+    torch.cuda.synchronize()
+    return y
+
+
+LENGTHS = [[(1, 90), (1, 7)], [(40, 90)], [(300, 300)]]
+
+
+@pytest.mark.parametrize("lengths", LENGTHS)
+@pytest.mark.parametrize("half,magnitude,scale,zero_keys", [
+    (False, 1e-25, 1e-21, False), (False, 4e-45, 0.0625, False), (False, 1.0, 1e-45, False),
+    (False, 1e30, 1e30, True), (False, 1.0, 3.2e38, True),
+    (True, 1.0, 1e-45, False), (True, 1.0, 3.2e38, True), (True, 60000.0, 3.4e38, True)])
+def test_attention_factors_beyond_float32(half, magnitude, scale, zero_keys, lengths):
+    """The scale and the query's magnitude leave float32 together: below it every
+    visible key weighs the same; above it equal scores still do."""
+    rng, kc, vc, start, lens, table = plain(lengths, 64, 3)
+    if zero_keys:
+        kc[:] = 0
+    q = rng.standard_normal((start[-1], 4, 64)) * magnitude
+    q = np.clip(q, -65504, 65504).astype(np.float16) if half else q.astype(np.float32)
+    y = attend(kc, vc, q, start, lens, table, scale=scale)
+    ref, absolute, score = block.attend(kc, vc, q, start, lens, table, 0, 0, float(np.float32(scale)))
+    assert score.max() < 1e-30
+    near(y, ref, attention_tol(ref, absolute, score, 300, 64, half))
