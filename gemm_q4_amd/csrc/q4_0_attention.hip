@@ -268,6 +268,7 @@ template <int DIM, bool F32> struct Rows {
     // largest weight; float32 rows rescale more often and keep 2^-39, so that
     // a hundred thousand faint weights beside a strong one keep their sum.
     static constexpr float kShift = F32 ? 14.0f : 7.0f, kLag = F32 ? 1.0f : 8.0f;
+    static constexpr float kFar = 65536.0f;
     h8_t q[kParts][DIM / 16];
     f16x_t o[DIM / 32];
     float m, l;
@@ -379,17 +380,25 @@ template <int DIM, bool F32> struct Rows {
 
     // Scores to weights; maximum, sum and what is accumulated so far brought
     // along.  The sum is of the rounded weights, two at a time.
-    template <int KT>
+    //
+    // The maximum is of scores in powers of two, so that a weight costs one fma
+    // and one exponential.  The larger it is, the coarser are the steps of that
+    // fma's constant: from 2^23 on a weight may pass binary16's range, or the
+    // largest one vanish.  From kFar on (steps of 2^-7) odd() therefore asks for
+    // CAREFUL, which takes the difference of the scores themselves first: its m
+    // is in their units, until close().
+    template <int KT, bool CAREFUL>
     __device__ __forceinline__ void weights(Weights<KT> &out, f16x_t (&s)[KT / 32]) {
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-        top = halves_max(top) * c;
-        if (__any(top > m + kLag)) {
+        top = halves_max(top) * (CAREFUL ? 1.0f : c);
+        if (__any(top > (CAREFUL ? m : m + kLag))) {
             const float mn = fmaxf(m, top);
-            const float f = mn == -INFINITY ? 1.0f : factor_of(m - mn);
+            const float f =
+                mn == -INFINITY ? 1.0f : factor_of(CAREFUL ? (m - mn) * c : m - mn);
             m = mn;
             l *= f;
 #pragma unroll
@@ -397,16 +406,17 @@ template <int DIM, bool F32> struct Rows {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[d][i] *= f;
         }
-        const float base = m == -INFINITY ? 0.0f : kShift - m;
+        const float base = m == -INFINITY ? 0.0f : CAREFUL ? m : kShift - m;
+        const auto power = [&](float x) {
+            return CAREFUL ? fmaf(x - base, c, kShift) : fmaf(x, c, base);
+        };
         const h2_t ones = {(_Float16)1.0f, (_Float16)1.0f};
 #pragma unroll
         for (int b = 0; b < KT / 16; ++b)
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                const float x0 =
-                    __builtin_amdgcn_exp2f(fmaf(s[b / 2][8 * (b % 2) + i], c, base));
-                const float x1 =
-                    __builtin_amdgcn_exp2f(fmaf(s[b / 2][8 * (b % 2) + i + 1], c, base));
+                const float x0 = __builtin_amdgcn_exp2f(power(s[b / 2][8 * (b % 2) + i]));
+                const float x1 = __builtin_amdgcn_exp2f(power(s[b / 2][8 * (b % 2) + i + 1]));
                 const h2_t hi = {(_Float16)x0, (_Float16)x1};
                 out.w[b][0][i] = hi[0];
                 out.w[b][0][i + 1] = hi[1];
@@ -482,12 +492,17 @@ template <int DIM, bool F32> struct Rows {
         f16x_t s[KT / 32];
         scores<KT>(s, kbuf, k0, masked, sinks);
         Weights<KT> ws;
-        weights<KT>(ws, s);
+        weights<KT, CAREFUL>(ws, s);
         mix<KT, CAREFUL>(ws, vbuf, k0, sinks);
     }
 
-    // Whether a product met something that is no number.
+    // After CAREFUL's tiles: the maximum in powers of two, as without.
+    __device__ __forceinline__ void close() { m *= c; }
+
+    // Whether a product met something that is no number, or a maximum lies so far
+    // from 0 that the weights have lost their last bits.
     __device__ __forceinline__ bool odd() const {
+        if (fabsf(m) >= kFar && m != -INFINITY) return true;
         float z = l * 0.0f;
 #pragma unroll
         for (int d = 0; d < DIM / 32; ++d)
@@ -633,6 +648,7 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
         if (__builtin_expect(__syncthreads_or(w.odd()), 0)) {
             w.clear();
             pass_loop<DIM, F32, RW, KW, true>(w, f, r, t0, t1, top_lo, lds);
+            w.close();
         }
     }
     float l = halves_sum(w.l), m = w.m;
@@ -763,7 +779,7 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM, true> &
             counted &= f.fill(r, page1, next + 16, kbuf + kHalf, false);
         }
         typename Rows<DIM, F32>::template Weights<KT> ws;
-        w.template weights<KT>(ws, s);
+        w.template weights<KT, CAREFUL>(ws, s);
         // outstanding: V, then the next K
         if (counted)
             Q4_WAIT_VMCNT(kCopies);
@@ -838,6 +854,7 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Attenti
             look1 = f.look(k + 16);
         }
         step_loop<DIM, F32, true>(w, f, r, t, t1, W, top_lo, mine, look0, look1, false);
+        w.close();
     }
     // join the waves
     w.l = halves_sum(w.l);

@@ -11,7 +11,7 @@ import torch
 
 import gemm_q4_amd as q4
 from oracle import block
-from test_gpu_block import DEV, H16, append_tol, attention_tol, dev, near
+from test_gpu_block import DEV, H16, H32, append_tol, attention_tol, dev, near
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,27 @@ def test_attention_factors_beyond_float32(half, magnitude, scale, zero_keys, len
     ref, absolute, score = block.attend(kc, vc, q, start, lens, table, 0, 0, float(np.float32(scale)))
     assert score.max() < 1e-30
     near(y, ref, attention_tol(ref, absolute, score, 300, 64, half))
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (33, 2)])
+@pytest.mark.parametrize("lengths", LENGTHS + [[(1, 1500)], [(70, 900), (1, 1300)]])
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("power", [10, 20, 22, 23, 24, 26, 28, 31, 60, 100])
+def test_attention_scores_of_any_size(power, half, lengths, window, sinks):
+    """Keys at whole levels, two of the cache's to a level, and queries that make
+    a step of one level a score of 2^power: a row's result is the mean of the
+    values at the highest level it sees.  Every score is exact, so no rounding
+    but that of the weights' sum and of the result is left; the other levels'
+    weights are at most exp(-2^10)."""
+    rng, kc, vc, start, lens, table = plain(lengths, 64, power, pages=100)
+    level = rng.permutation(np.repeat(np.arange(800), 2)).reshape(100, 16) - 400.0
+    kc[:] = 0
+    kc[:, 0, :, 3], kc[:, 1, :, 5] = level, -level
+    table = np.stack([rng.permutation(100)[:table.shape[1]] for _ in lengths]).astype(np.int32)
+    q = np.zeros((start[-1], 4, 64), np.float16 if half else np.float32)
+    shift = min(power, 14) if half else power
+    q[:, :2, 3] = q[:, 2:, 5] = 2.0 ** shift
+    scale = 2.0 ** (power - shift)
+    y = attend(kc, vc, q, start, lens, table, window, sinks, scale)
+    ref, absolute, _ = block.attend(kc, vc, q, start, lens, table, window, sinks, scale)
+    near(y, ref, np.abs(ref) * (H16 if half else H32) + absolute * 8 * H32 + 2.0 ** -25)
