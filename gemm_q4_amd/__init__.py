@@ -112,6 +112,7 @@ _SIGS = {
                               _i64, _i64, _f32, _vp, _sz, _vp]),
     "q4_0_attention_workspace_size": (_int, [_vp, _i64, _int, _i64, _i64, _i64, _i64, _i64,
                                              _szp]),
+    "q4_0_select_attention": (_int, [_vp, _i64, _int, _i64, _i64, _i64, _i64, _i64]),
     "q4_0_residual_norm": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _i64,
                                   _vp, _f32, _f32, _vp, _int, _i64, _i64, _i64, _vp]),
 }
@@ -425,6 +426,12 @@ def q4_0_attention_workspace_size(cache, q_heads: int, x_dtype: int, n: int, tab
                                   batch: int, window: int = 0, sinks: int = 0) -> int:
     return _size(_lib.q4_0_attention_workspace_size, "q4_0_attention_workspace_size",
                  _ref(cache), q_heads, x_dtype, n, table_stride, batch, window, sinks)
+
+
+def q4_0_select_attention(cache, q_heads: int, x_dtype: int, n: int, table_stride: int,
+                          batch: int, window: int = 0, sinks: int = 0) -> int:
+    return _check(_lib.q4_0_select_attention(_ref(cache), q_heads, x_dtype, n, table_stride, batch,
+                                             window, sinks), "q4_0_select_attention")
 
 
 def q4_0_residual_norm(b, b_dtype: int, b_stride: int, post, gate, gate_row: int, gate_col: int,

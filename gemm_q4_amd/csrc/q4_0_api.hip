@@ -746,6 +746,15 @@ int q4_0_attention_workspace_size(const q4_0_kv_cache *cache, int64_t q_heads, i
     return Q4_0_OK;
 }
 
+int q4_0_select_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, int64_t n,
+                          int64_t table_stride, int64_t batch, int64_t window, int64_t sinks) {
+    const int st =
+        check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks, false);
+    if (st != Q4_0_OK) return st;
+    return q4::attention_tile_rows(
+        attention_args(cache, q_heads, n, table_stride, batch, window, sinks));
+}
+
 int q4_0_attention(const q4_0_kv_cache *cache, const void *q, int64_t q_stride, int x_dtype,
                    int64_t q_heads, void *y, int64_t n, const int32_t *q_start,
                    const int32_t *kv_len, const int32_t *table, int64_t table_stride,

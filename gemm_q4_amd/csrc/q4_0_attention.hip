@@ -1093,6 +1093,8 @@ bool attention_supports(int dim) { return dim == 64 || dim == 128 || dim == 256;
 
 size_t attention_workspace_bytes(const AttentionArgs &a, int) { return choose(a).bytes; }
 
+int attention_tile_rows(const AttentionArgs &a) { return choose(a).rows; }
+
 hipError_t launch_attention(const AttentionArgs &a, int x_f16, void *ws, hipStream_t stream) {
     const Choice ch = choose(a);
     const Plan pl = {a.q_heads / a.cache.heads, ch.splits, ch.least, (float *)ws,

@@ -147,6 +147,7 @@ struct AttentionArgs {
 };
 bool attention_supports(int dim);
 size_t attention_workspace_bytes(const AttentionArgs &a, int x_f16);
+int attention_tile_rows(const AttentionArgs &a);
 hipError_t launch_attention(const AttentionArgs &a, int x_f16, void *ws, hipStream_t stream);
 
 struct NormArgs {

@@ -429,6 +429,11 @@ int q4_0_attention(const q4_0_kv_cache *cache, const void *q, int64_t q_stride, 
 int q4_0_attention_workspace_size(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype,
                                   int64_t n, int64_t table_stride, int64_t batch,
                                   int64_t window, int64_t sinks, size_t *bytes);
+/* Rows (tokens times query heads of a key/value head) of a tile in the kernel
+ * that q4_0_attention would run for these sizes: 32, 64 or 128; or a negative
+ * status for an invalid call.  Host only. */
+int q4_0_select_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, int64_t n,
+                          int64_t table_stride, int64_t batch, int64_t window, int64_t sinks);
 
 /* The residual step between two half blocks, with the norm after the one and
  * the norm before the next:

@@ -1,0 +1,34 @@
+"""How attention calls are cut into work, as the host queries show it, without a
+GPU."""
+import pytest
+
+import gemm_q4_amd as q4
+
+
+def cache(heads=8, dim=128):
+    return q4.q4_0_kv_cache(0, 0, 1 << 14, heads, 16, dim)
+
+
+@pytest.mark.parametrize("dtype", [q4.F32, q4.F16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_tiles_by_rows(dim, dtype):
+    """Up to 32 rows to a conversation 32-row tiles; above, 128 rows where that
+    gives every compute unit a tile, else 64."""
+    rows = lambda n, batch, heads=8, group=4: q4.q4_0_select_attention(
+        cache(heads, dim), heads * group, dtype, n, 512, batch)
+    assert rows(1, 1) == rows(8, 1) == rows(64, 64) == rows(512, 64) == 32
+    assert rows(9, 1) == rows(512, 1) == rows(900, 1) == rows(40, 3) == 64
+    assert rows(1100, 1) == rows(65536, 1) == rows(8000, 2) == rows(513, 64) == 128
+    assert rows(512, 1, heads=64, group=1) == 128
+
+
+def test_tile_query_refuses_what_the_call_refuses():
+    def status(*a):
+        with pytest.raises(q4.Q4Error) as e:
+            q4.q4_0_select_attention(*a)
+        return e.value.status
+    assert status(None, 8, q4.F16, 1, 1, 1) == q4.ENULL
+    assert status(cache(dim=96), 8, q4.F16, 1, 1, 1) == q4.EUNSUPPORTED
+    assert status(cache(), 9, q4.F16, 1, 1, 1) == q4.ESHAPE
+    assert status(cache(), 8, q4.F16, 0, 1, 1) == q4.ESHAPE
+    assert status(cache(), 8, 5, 1, 1, 1) == q4.EINVAL

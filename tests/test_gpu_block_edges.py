@@ -11,7 +11,7 @@ import torch
 
 import gemm_q4_amd as q4
 from oracle import block
-from test_gpu_block import DEV, H16, H32, append_tol, attention_tol, dev, near
+from test_gpu_block import DEV, H16, H32, append_tol, attention_tol, batch_inputs, dev, near
 
 pytestmark = pytest.mark.gpu
 
@@ -83,7 +83,8 @@ def test_attention_factors_beyond_float32(half, magnitude, scale, zero_keys, len
     q = rng.standard_normal((start[-1], 4, 64)) * magnitude
     q = np.clip(q, -65504, 65504).astype(np.float16) if half else q.astype(np.float32)
     y = attend(kc, vc, q, start, lens, table, scale=scale)
-    ref, absolute, score = block.attend(kc, vc, q, start, lens, table, 0, 0, float(np.float32(scale)))
+    ref, absolute, score = block.attend(kc, vc, q, start, lens, table, 0, 0,
+                                        float(np.float32(scale)))
     assert score.max() < 1e-30
     near(y, ref, attention_tol(ref, absolute, score, 300, 64, half))
 
@@ -110,3 +111,140 @@ def test_attention_scores_of_any_size(power, half, lengths, window, sinks):
     y = attend(kc, vc, q, start, lens, table, window, sinks, scale)
     ref, absolute, _ = block.attend(kc, vc, q, start, lens, table, window, sinks, scale)
     near(y, ref, np.abs(ref) * (H16 if half else H32) + absolute * 8 * H32 + 2.0 ** -25)
+
+
+# ---- attention: 128-row tiles -------------------------------------------------
+HEADS_128 = 64      # key/value heads, one query head each: a few hundred tokens fill the device
+
+
+def by_128(lengths, dim, half, window=0, sinks=0, seed=0, change=None, q_scale=1.0):
+    """A call on 128-row tiles against the oracle.  change(kc, vc, table, lens)
+    plants what the call has to bear."""
+    kc, vc, q, start, lens, table = batch_inputs(lengths, HEADS_128, HEADS_128, dim, 16, half, seed,
+                                                 window, sinks, q_scale)
+    n, scale = q.shape[0], dim ** -0.5
+    if change:
+        change(kc, vc, table, lens)
+    assert q4.q4_0_select_attention(q4.q4_0_kv_cache(0, 0, len(kc), HEADS_128, 16, dim), HEADS_128,
+                                    q4.F16 if half else q4.F32, n, table.shape[1], len(lengths),
+                                    window, sinks) == 128
+    ref, absolute, score = block.attend(kc, vc, q, start, lens, table, window, sinks, scale)
+    y = attend(kc, vc, q, start, lens, table, window, sinks, scale)
+    keys = max(kv for _, kv in lengths)
+    clean = lambda a: np.where(np.isfinite(a), a, 0.0)
+    near(y, ref, attention_tol(clean(ref), clean(absolute), clean(score), keys, dim, half))
+    assert torch.equal(y.nan_to_num(), attend(kc, vc, q, start, lens, table, window, sinks,
+                                              scale).nan_to_num())
+    return ref
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_128_row_tiles(dim, half):
+    """Long passes: conversations that start and end inside a tile, one of one
+    token, one behind a cache, and rows that see nothing."""
+    by_128([(200, 200), (1, 77), (130, 150), (61, 64), (0, 9), (9, 4)], dim, half, seed=dim)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(70, 5), (17, 130)])
+def test_attention_128_row_tiles_window(window, sinks, dim, half):
+    by_128([(140, 290), (150, 150), (3, 2), (110, 112)], dim, half, window, sinks, seed=window)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_128_row_tiles_bad_pages(dim, half):
+    """A page outside the cache and a table that ends too early: the rows that
+    see such keys are NaN, the others are not touched."""
+    def change(kc, vc, table, lens):
+        kc[np.isnan(kc)], vc[np.isnan(vc)] = 0, 0
+        table[0, 6] = len(kc)                             # keys 96..111
+        table[1] = 0
+        lens[1] = 16 * table.shape[1] + 40
+    ref = by_128([(190, 190), (140, 140), (20, 20)], dim, half, seed=5, change=change)
+    assert np.isfinite(ref[:96]).all() and np.isnan(ref[96:190]).all()
+    assert np.isnan(ref[329]).all() and np.isfinite(ref[330:]).all()
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_128_row_tiles_non_finite(dim, half):
+    """Infinities and NaN of keys and values stay with the rows that see them,
+    though a tile's other rows share the product."""
+    spots = [(1, 150, 3, np.inf), (1, 151, 3, np.inf), (1, 100, 5, -np.inf), (1, 60, 9, np.nan),
+             (0, 170, 1, np.nan), (1, 175, 7, np.inf), (1, 176, 7, -np.inf)]
+
+    def change(kc, vc, table, lens):
+        for which, j, d, x in spots:
+            (kc, vc)[which][table[0, j // 16], 1, j % 16, d] = x
+    ref = by_128([(200, 200), (140, 160), (50, 50)], dim, half, window=60, seed=6, change=change)
+    assert np.isfinite(ref[:, [0, 2]]).all() and not np.isfinite(ref[:200, 1]).all()
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_128_row_tiles_far_scores(dim, half):
+    """Scores around 2^40, one head's: exact ones, so the highest level a row
+    sees decides alone."""
+    lengths = [(200, 200), (140, 160), (50, 50)]
+    rng, kc, vc, start, lens, table = plain(lengths, dim, 9, pages=100)
+    assert q4.q4_0_select_attention(q4.q4_0_kv_cache(0, 0, 100, HEADS_128, 16, dim), HEADS_128,
+                                    q4.F32, start[-1], table.shape[1], 3) == 128
+    level = rng.permutation(1600).reshape(100, 16) - 800.0
+    kc, vc = (np.repeat(c[:, :1], HEADS_128, 1) for c in (kc, vc))
+    kc[:, 5] = 0
+    kc[:, 5, :, 2] = level
+    table = np.stack([rng.permutation(100)[:table.shape[1]] for _ in lengths]).astype(np.int32)
+    q = rng.standard_normal((start[-1], HEADS_128, dim)).astype(np.float16 if half else np.float32)
+    q[:, 5] = 0
+    q[:, 5, 2] = 2.0 ** 14
+    q[:, :5] = q[:, 6:] = 0
+    ref, absolute, _ = block.attend(kc, vc, q, start, lens, table, 0, 0, 2.0 ** 20)
+    y = attend(kc, vc, q, start, lens, table, 0, 0, 2.0 ** 20)
+    # elsewhere equal weights: each rounded alike, and sums of up to 200 terms
+    near(y, ref, np.abs(ref) * (H16 if half else H32) + absolute * 2 * 216 * H32 + 2.0 ** -25)
+
+
+def test_attention_more_tiles_than_one_launch_takes():
+    """More tiles than a grid's third axis: the last ones go in a second launch.
+    Few rows to a conversation (most hold none), and one conversation of very
+    many rows."""
+    batch, width = 65536, 2
+    rng, kc, vc, _, _, _ = plain([(1, 1)], 64, 2, pages=40)
+    news = np.zeros(batch, np.int64)
+    news[[0, 5000, 40000, 65533, 65534, 65535]] = [2, 1, 3, 1, 2, 1]
+    lens = np.where(news > 0, 17 + np.arange(batch) % 14, 0).astype(np.int32)
+    start = np.concatenate([[0], news.cumsum()]).astype(np.int32)
+    table = rng.integers(0, 40, (batch, width)).astype(np.int32)
+    q = rng.standard_normal((start[-1], 4, 64)).astype(np.float16)
+    y = attend(kc, vc, q, start, lens, table, scale=0.125)
+    used = np.flatnonzero(news)
+    ref, absolute, score = block.attend(kc, vc, q, np.concatenate([start[used], start[-1:]]),
+                                        lens[used], table[used], 0, 0, 0.125)
+    near(y, ref, attention_tol(ref, absolute, score, 31, 64, True))
+
+    n, heads, window = 65536, 128, 4
+    assert q4.q4_0_select_attention(q4.q4_0_kv_cache(0, 0, 64, 1, 1024, 64), heads, q4.F16, n, 64,
+                                    1, window, 0) == 128
+    g = torch.Generator(device=DEV).manual_seed(3)
+    tk, tv = (torch.randn(64, 1, 1024, 64, device=DEV, generator=g).half() for _ in range(2))
+    tq = torch.randn(n, heads, 64, device=DEV, generator=g).half()
+    order = torch.randperm(64, device=DEV, generator=g)
+    y = q4.attention(q4.kv_cache(tk, tv), tq, torch.tensor([0, n], dtype=torch.int32, device=DEV),
+                     torch.tensor([n], dtype=torch.int32, device=DEV), order.int()[None], window)
+    pick = torch.cat([torch.tensor([0, 1, 2, 3, n - 2, n - 1]),
+                      torch.from_numpy(rng.integers(4, n, 60))])
+    k, v = (t[order, 0].reshape(n, 64).double().cpu().numpy() for t in (tk, tv))
+    want, absolute, score = (np.zeros((len(pick), heads, 64)), np.zeros((len(pick), heads, 64)),
+                             np.zeros((len(pick), heads)))
+    qs = tq[pick.to(DEV)].double().cpu().numpy()
+    for i, t in enumerate(pick.tolist()):
+        js = np.arange(max(0, t - window + 1), t + 1)
+        z = qs[i] @ k[js].T / 8
+        w = np.exp(z - z.max(1, keepdims=True))
+        w /= w.sum(1, keepdims=True)
+        want[i], absolute[i] = w @ v[js], w @ np.abs(v[js])
+        score[i] = (np.abs(qs[i]) @ np.abs(k[js]).T / 8).max(1)
+    near(y[pick.to(DEV)], want, attention_tol(want, absolute, score, window, 64, True))
