@@ -370,9 +370,9 @@ PyObject *call_attention(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
         const void *lp = dense(*len, "kv_len", at::kInt, {batch});
         const void *tp = dense(*table, "table", at::kInt, {batch, width});
         void *yp = dense(*y, "y", q->scalar_type(), {n, heads, c.c.dim});
+        if (ws && !ws->is_contiguous()) bad_value("ws must be contiguous");
         const at::Tensor *all[] = {q, start, len, table, y, ws, &THPVariable_Unpack(c.k)};
         const int dev = device(all);
-        if (ws && !ws->is_contiguous()) bad_value("ws must be contiguous");
         return PyLong_FromLong(g.attention(
             &c.c, q->data_ptr(), qs, code, heads, yp, n, (const int32_t *)sp,
             (const int32_t *)lp, (const int32_t *)tp, width, batch, integer(a[5]),

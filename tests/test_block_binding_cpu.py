@@ -134,3 +134,114 @@ def test_products_do_not_need_the_extension_module(tmp_path, extension, reason):
     assert r.returncode == 0, r.stderr
     lines = r.stdout.strip().splitlines()
     assert len(lines) == 3 and all(reason in line and "build it again" in line for line in lines)
+
+
+def refused(kind, message, call, *args, **kw):
+    with pytest.raises(kind, match=message):
+        call(*args, **kw)
+
+
+def test_append_says_what_does_not_fit():
+    """Each check by its own message: on the host every call is refused in the
+    end, so the type of the error alone would show nothing."""
+    k = torch.zeros(2, 2, 16, 64, dtype=torch.float16)
+    c = q4.kv_cache(k, k.clone())
+    q, kv = torch.zeros(3, 4, 64), torch.zeros(3, 2, 64)
+    pos, slots = torch.zeros(3, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)
+    call = q4.kv_append
+    refused(ValueError, "every tensor of the call must be on a GPU", call, c, None, q, kv, kv, pos,
+            slots)
+    refused(TypeError, "cache must come from kv_cache", call, k, None, None, kv, kv, pos, slots)
+    refused(TypeError, "rot must come from rotary", call, c, k, q, kv, kv, pos, slots)
+    refused(TypeError, "k must be a tensor", call, c, None, q, None, kv, pos, slots)
+    refused(TypeError, "k must be float32 or float16", call, c, None, q, kv.double(), kv, pos,
+            slots)
+    refused(TypeError, "q, k and v must have one type", call, c, None, q, kv, kv.half(), pos, slots)
+    refused(TypeError, "q, k and v must have one type", call, c, None, q.half(), kv, kv, pos, slots)
+    refused(ValueError, "k has shape .* which does not fit", call, c, None, q, kv[:, :1], kv, pos,
+            slots)
+    refused(ValueError, "v has shape .* which does not fit", call, c, None, q, kv, kv[:2], pos,
+            slots)
+    refused(ValueError, "k must have two or three dimensions", call, c, None, q, kv[0, 0], kv, pos,
+            slots)
+    apart = torch.zeros(3, 2, 128)[..., ::2]
+    refused(ValueError, "k's rows must be dense", call, c, None, q, apart, kv, pos, slots)
+    refused(ValueError, "k's rows must be dense", call, c, None, q,
+            kv.transpose(1, 2).contiguous().transpose(1, 2), kv, pos, slots)
+    refused(ValueError, "q has shape .* which does not fit", call, c, None, q[:2], kv, kv, pos,
+            slots, q_out=q)
+    refused(ValueError, "q_out must have shape", call, c, None, q, kv, kv, pos, slots, q_out=q[:2])
+    refused(TypeError, "q_out must be float32 or float16", call, c, None, q, kv, kv, pos, slots,
+            q_out=q.bfloat16())
+    refused(ValueError, "q_out must be contiguous", call, c, None, q, kv, kv, pos, slots,
+            q_out=torch.zeros(3, 4, 128)[..., :64])
+    refused(TypeError, "positions must be Int", call, c, None, q, kv, kv, pos.long(), slots)
+    refused(ValueError, "positions must have shape", call, c, None, q, kv, kv, pos[:2], slots)
+    refused(TypeError, "slots must be Long", call, c, None, q, kv, kv, pos, slots.int())
+    refused(ValueError, "slots must have shape", call, c, None, q, kv, kv, pos, slots[:2])
+    refused(ValueError, "slots must be contiguous", call, c, None, q, kv, kv, pos,
+            torch.zeros(6, dtype=torch.int64)[::2])
+    refused(ValueError, "norm weights of 32 do not fit heads of 64", call, c,
+            q4.rotary(q_norm=torch.ones(32)), q, kv, kv, pos, slots)
+
+
+def test_descriptors_say_what_does_not_fit():
+    k = torch.zeros(2, 2, 16, 64, dtype=torch.float16)
+    refused(TypeError, "k must be Half", q4.kv_cache, k.float(), k)
+    refused(TypeError, "v must be Half", q4.kv_cache, k, k.float())
+    refused(TypeError, "v must be a tensor", q4.kv_cache, k, None)
+    refused(ValueError, "v must have shape", q4.kv_cache, k, k[:1])
+    refused(ValueError, "k must be .pages, heads, page_size, dim.", q4.kv_cache, k[0], k[0])
+    refused(ValueError, "k must be contiguous", q4.kv_cache, k.transpose(1, 2), k.transpose(1, 2))
+    refused(TypeError, "inv_freq must be Float", q4.rotary, torch.ones(4).double())
+    refused(ValueError, "inv_freq must have one dimension", q4.rotary, torch.ones(2, 4))
+    refused(ValueError, "inv_freq must be contiguous", q4.rotary, torch.ones(8)[::2])
+    refused(TypeError, "k_norm must be a tensor", q4.rotary, k_norm=[1.0])
+    refused(ValueError, "q_norm and k_norm have different lengths", q4.rotary,
+            q_norm=torch.ones(64), k_norm=torch.ones(32))
+
+
+def test_attention_says_what_does_not_fit():
+    k = torch.zeros(2, 2, 16, 64, dtype=torch.float16)
+    c, q = q4.kv_cache(k, k.clone()), torch.zeros(3, 4, 64)
+    start, lens = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    call = q4.attention
+    refused(ValueError, "every tensor of the call must be on a GPU", call, c, q, start, lens, table)
+    refused(ValueError, "q must be .n, heads, 64.", call, c, q[..., :32], start, lens, table)
+    refused(TypeError, "must be float32 or float16", call, c, q.bfloat16(), start, lens, table)
+    refused(ValueError, "q's rows must be dense", call, c, torch.zeros(3, 4, 128)[..., :64], start,
+            lens, table)
+    refused(TypeError, "kv_len must be Int", call, c, q, start, lens.long(), table)
+    refused(TypeError, "q_start must be Int", call, c, q, start.long(), lens, table)
+    refused(ValueError, "q_start must have shape", call, c, q, start[:1], lens, table)
+    refused(TypeError, "table must be Int", call, c, q, start, lens, table.long())
+    refused(ValueError, "table must have shape", call, c, q, start, lens, table.expand(2, 2))
+    refused(ValueError, "table must be contiguous", call, c, q, start, lens,
+            torch.zeros(1, 4, dtype=torch.int32)[:, ::2])
+    refused(TypeError, "y must be Float", call, c, q, start, lens, table, y=q.half())
+    refused(ValueError, "y must have shape", call, c, q, start, lens, table, y=q[:2])
+    refused(ValueError, "ws must be contiguous", call, c, q, start, lens, table,
+            ws=torch.zeros(8, dtype=torch.uint8)[::2])
+
+
+def test_residual_norm_says_what_does_not_fit():
+    h, w, call = torch.zeros(3, 64), torch.ones(64), q4.residual_norm
+    refused(ValueError, "every tensor of the call must be on a GPU", call, h, h.clone(), w, w)
+    refused(TypeError, "h must be float32", call, h.half(), h)
+    refused(ValueError, "h must be .n, dim.", call, h[0], h[0])
+    refused(ValueError, "h's rows must be dense", call, torch.zeros(3, 128)[:, ::2], None, w)
+    refused(ValueError, "b has shape .* which does not fit", call, h, h[:2])
+    refused(TypeError, "b must be float32 or float16", call, h, h.bfloat16())
+    refused(TypeError, "h_out must be float32", call, h, h, h_out=h.half())
+    refused(ValueError, "h_out must have h's row stride", call, h, h,
+            h_out=torch.zeros(3, 128)[:, :64])
+    refused(TypeError, "gate must be float32", call, h, h, gate=h.half())
+    refused(ValueError, "gate must be .n, dim., .n, 1. or .1, dim.", call, h, h,
+            gate=torch.zeros(3, 2))
+    refused(ValueError, "gate must be", call, h, h, gate=w)
+    refused(ValueError, "pre must have shape", call, h, h, pre=w[:63])
+    refused(TypeError, "pre must be Float", call, h, h, pre=w.half())
+    refused(ValueError, "post must have shape", call, h, h, post=w[:63])
+    refused(ValueError, "y has shape .* which does not fit", call, h, h, pre=w, y=h[:2])
+    refused(TypeError, "y must be float32 or float16", call, h, h, pre=w, y=h.double())

@@ -32,3 +32,23 @@ def test_tile_query_refuses_what_the_call_refuses():
     assert status(cache(), 9, q4.F16, 1, 1, 1) == q4.ESHAPE
     assert status(cache(), 8, q4.F16, 0, 1, 1) == q4.ESHAPE
     assert status(cache(), 8, 5, 1, 1, 1) == q4.EINVAL
+
+
+def test_split_calls_refuse_bad_workspaces():
+    """One token over a long axis is split: it needs a workspace, and refuses one
+    that is missing, small, misaligned or overlapping."""
+    at = [(i + 1) << 36 for i in range(8)]
+    c = q4.q4_0_kv_cache(at[0], at[1], 1 << 14, 8, 16, 128)
+    need = q4.q4_0_attention_workspace_size(c, 32, q4.F16, 1, 8192, 1)
+    assert 0 < need <= q4.WORKSPACE_MAX
+
+    def status(*workspace):
+        with pytest.raises(q4.Q4Error) as e:
+            q4.q4_0_attention(c, at[2], 4096, q4.F16, 32, at[3], 1, at[4], at[5], at[6], 8192, 1, 0,
+                              0, 0.125, *workspace)
+        return e.value.status
+    assert status() == q4.EWORKSPACE
+    assert status(at[7], need - 1) == q4.EWORKSPACE
+    assert status(at[7] + 64, need) == q4.EALIGN
+    assert status(at[2], need) == q4.EALIAS
+    assert status(at[3] + 4096 - 256, need) == q4.EALIAS

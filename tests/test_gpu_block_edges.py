@@ -248,3 +248,35 @@ def test_attention_more_tiles_than_one_launch_takes():
         want[i], absolute[i] = w @ v[js], w @ np.abs(v[js])
         score[i] = (np.abs(qs[i]) @ np.abs(k[js]).T / 8).max(1)
     near(y[pick.to(DEV)], want, attention_tol(want, absolute, score, window, 64, True))
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("tokens", [1, 40])
+@pytest.mark.parametrize("gap", [3.0, 14.0, 18.0])
+def test_attention_faint_weights_count(gap, tokens, half):
+    """One strong key and 40000 faint equal ones: a row's result is known from
+    the faint ones' share f of the strong one's weight.  An error of the faint
+    sum, e of it, moves the result (f - 1) / (f + 1) by 2 f e / (f + 1)^2; e is a
+    faint weight's rounding (relative, or half of binary16's last step where a
+    weight of 2^7 (float32: 2^14) exp(-gap) lies that low), float32 sums of
+    40000, and the power's own rounding.  Without the faint keys it would be -1,
+    which has to be out of reach."""
+    n, dim, page, pages = 40001, 64, 256, 160
+    kc, vc = (torch.zeros(pages, 1, page, dim, dtype=torch.float16, device=DEV) for _ in range(2))
+    kc[0, 0, 0, 0] = 8.0
+    vc[:, 0, :, 1] = 1.0
+    vc[0, 0, 0, 1] = -1.0
+    q = torch.zeros(tokens, 2, dim, dtype=torch.float16 if half else torch.float32, device=DEV)
+    q[:, :, 0] = gap
+    i32 = dict(dtype=torch.int32, device=DEV)
+    y = q4.attention(q4.kv_cache(kc, vc), q, torch.tensor([0, tokens], **i32),
+                     torch.tensor([n], **i32), torch.arange(pages, **i32)[None], scale=0.125)
+    f = (n - tokens + np.arange(tokens)) * np.exp(-gap)
+    want = (f - 1) / (f + 1)
+    weight = 2.0 ** (7 if half else 14) * np.exp(-gap)
+    e = max(H16 if half else 2.0 ** -22, 2.0 ** -25 / weight) + 2 * n * H32 + 64 * gap * H32
+    tol = 2 * f * e / (f + 1) ** 2 + np.abs(want) * (H16 if half else 4 * H32)
+    assert (np.abs(want + 1) > 2 * tol).all()
+    got = y[:, :, 1].double().cpu().numpy()
+    assert (np.abs(got - want[:, None]) <= tol[:, None]).all(), np.abs(got - want[:, None]).max()
+    assert (y[:, :, 0] == 0).all() and (y[:, :, 2:] == 0).all()
