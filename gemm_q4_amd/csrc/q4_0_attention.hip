@@ -515,12 +515,8 @@ template <int DIM, bool F32> struct Rows {
 // The rows' results, to y or to this split's share of the workspace.  `o` holds
 // four neighbouring elements of row `row` from element d on.
 template <bool F32>
-__device__ __forceinline__ void put4(const AttentionArgs &a, const Plan &pl, int split,
-                                     int64_t row, int dim, int d, f4_t o, float l, bool sees) {
-    if (pl.splits > 1) {
-        *(f4_t *)(pl.part + ((int64_t)split * a.n * a.q_heads + row) * dim + d) = o;
-        return;
-    }
+__device__ __forceinline__ void put_y4(const AttentionArgs &a, int64_t row, int dim, int d, f4_t o,
+                                       float l, bool sees) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = sees ? o[i] / l : 0.0f;
     if (F32)
@@ -528,6 +524,15 @@ __device__ __forceinline__ void put4(const AttentionArgs &a, const Plan &pl, int
     else
         *(h4_t *)((_Float16 *)a.y + row * dim + d) =
             h4_t{(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]};
+}
+
+template <bool F32>
+__device__ __forceinline__ void put4(const AttentionArgs &a, const Plan &pl, int split,
+                                     int64_t row, int dim, int d, f4_t o, float l, bool sees) {
+    if (pl.splits > 1)
+        *(f4_t *)(pl.part + ((int64_t)split * a.n * a.q_heads + row) * dim + d) = o;
+    else
+        put_y4<F32>(a, row, dim, d, o, l, sees);
 }
 
 __device__ __forceinline__ void put_ml(const AttentionArgs &a, const Plan &pl, int split,
@@ -705,17 +710,14 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
     if (row >= row1) return;
     const int64_t out = (int64_t)(at.first + row / pl.group) * a.q_heads + hk * pl.group +
                         row % pl.group;
-    if (pl.splits > 1) {
-        if (half == 0) put_ml(a, pl, split, out, m, l);
-        if (t0 >= t1) return;
-    }
+    // (one wave group: 128-row tiles, whose key axis is never split)
 #pragma unroll
     for (int d = 0; d < DIM / 32; ++d)
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
-            put4<F32>(a, pl, split, out, DIM, 32 * d + 2 * i + 4 * half,
-                      f4_t{w.o[d][i], w.o[d][i + 1], w.o[d][i + 2], w.o[d][i + 3]}, l,
-                      w.p >= 0);
+            put_y4<F32>(a, out, DIM, 32 * d + 2 * i + 4 * half,
+                        f4_t{w.o[d][i], w.o[d][i + 1], w.o[d][i + 2], w.o[d][i + 3]}, l,
+                        w.p >= 0);
 }
 
 // ---- few rows: every wave streams its own keys for the same 32 rows ---------
@@ -971,9 +973,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] += v[e];
     }
-    Plan whole = pl;
-    whole.splits = 1;
-    put4<F32>(a, whole, 0, row, dim, 4 * x, o, l, sees);
+    put_y4<F32>(a, row, dim, 4 * x, o, l, sees);
 }
 
 // ---- choices on the host ----------------------------------------------------
@@ -1021,7 +1021,7 @@ Choice choose(const AttentionArgs &a) {
     int64_t splits;
     ch.waves = dim > 128 ? 2 : 4;
     if (R > 32) {
-        splits = cus / likely;
+        splits = cus / likely;  // (128-row tiles are taken where that is one at most)
         ch.least = 16;
     } else {
         // workgroups that run at once: two to a compute unit, four of 64-wide heads

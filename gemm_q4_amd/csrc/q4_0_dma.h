@@ -37,14 +37,7 @@ __device__ __forceinline__ void dma16_at(const void *base, uint32_t off, uint8_t
                  : "memory", "m0");
 }
 
-// The same two copies for data that is read once, with the non-temporal hint.
-__device__ __forceinline__ void dma16_once(const void *src, uint8_t *lds) {
-    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt"
-                 :
-                 : "v"(src), "s"(base)
-                 : "memory", "m0");
-}
+// dma16_at for data that is read once, with the non-temporal hint.
 __device__ __forceinline__ void dma16_once_at(const void *base, uint32_t off, uint8_t *lds) {
     const uint32_t lb = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
