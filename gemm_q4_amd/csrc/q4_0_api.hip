@@ -333,7 +333,24 @@ bool outputs_clash(const Span *outs, int nouts, const Span *ins, int nins) {
     return false;
 }
 
-// Shape checks shared by q4_0_attention and its workspace query.
+// Rows `stride` bytes apart, `width` bytes each (stride 0: one run).
+struct RowSpan {
+    const void *p;
+    size_t len;
+    int64_t stride, width;
+};
+
+// Whether rows meet.  Two arguments may be columns of one wider buffer: rows of
+// one stride that lie apart within it lie apart altogether.
+bool rows_meet(const RowSpan &a, const RowSpan &b) {
+    if (!overlaps(a.p, a.len, b.p, b.len)) return false;
+    if (a.stride == 0 || a.stride != b.stride) return true;
+    int64_t from = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % a.stride;
+    if (from < 0) from += a.stride;
+    return from < a.width || from + b.width > a.stride;
+}
+
+// Shape checks shared by q4_0_attention and its queries.
 int check_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, int64_t n,
                     int64_t table_stride, int64_t batch, int64_t window, int64_t sinks,
                     bool pointers) {
@@ -810,18 +827,24 @@ int q4_0_residual_norm(const void *b, int b_dtype, int64_t b_stride, const float
                                  !aligned(gate, 4))) ||
         (y && (!aligned(y, yel) || !aligned(pre, 4))))
         return Q4_0_EALIGN;
-    const size_t hbytes = rows_bytes(n, h_stride, dim, 4), wbytes = (size_t)dim * 4u;
     const bool in_place = b && h_out == h;
-    const Span ins[5] = {
-        {b, b ? rows_bytes(n, b_stride, dim, bel) : 0},
-        {b ? post : nullptr, wbytes},
-        {b ? gate : nullptr,
-         b && gate ? (size_t)((n - 1) * gate_row + (dim - 1) * gate_col + 1) * 4u : 0},
-        {y ? pre : nullptr, wbytes},
-        {in_place ? nullptr : h, hbytes}};
-    const Span outs[2] = {{b ? h_out : nullptr, hbytes},
-                          {y, y ? rows_bytes(n, y_stride, dim, yel) : 0}};
-    if (outputs_clash(outs, 2, ins, 5)) return Q4_0_EALIAS;
+    const auto rows = [&](const void *p, int64_t stride, int64_t width, int64_t bytes) {
+        return RowSpan{p, p ? rows_bytes(n, stride, width, bytes) : 0, stride * bytes,
+                       width * bytes};
+    };
+    const size_t wbytes = (size_t)dim * 4u;
+    const RowSpan ins[5] = {
+        rows(b, b_stride, dim, bel),
+        {b ? post : nullptr, wbytes, 0, 0},
+        rows(b ? gate : nullptr, gate_row, gate_col ? dim : 1, 4),
+        {y ? pre : nullptr, wbytes, 0, 0},
+        rows(in_place ? nullptr : h, h_stride, dim, 4)};
+    const RowSpan outs[2] = {rows(b ? h_out : nullptr, h_stride, dim, 4),
+                             rows(y, y_stride, dim, yel)};
+    for (const RowSpan &out : outs)
+        for (const RowSpan &in : ins)
+            if (rows_meet(out, in)) return Q4_0_EALIAS;
+    if (rows_meet(outs[0], outs[1])) return Q4_0_EALIAS;
     q4::NormArgs a = {};
     a.b = b, a.b_stride = b_stride, a.post = post, a.gate = gate;
     a.gate_row = gate_row, a.gate_col = (int)gate_col, a.alpha = alpha;

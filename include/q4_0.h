@@ -446,7 +446,8 @@ int q4_0_select_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dty
  *   gate : DEVICE float32, g[t][i] = gate[t * gate_row + i * gate_col], or NULL
  *          (1).  gate_col 0 or 1; gate_row >= 0 (0: one row for all tokens).
  *   h, h_out : DEVICE float32 rows, h_stride elements apart; h_out may be h
- *          itself (in place), and overlaps nothing else.
+ *          itself (in place), and overlaps nothing else.  Arguments may be
+ *          columns of one wider buffer (rows of one stride in bytes).
  *   y    : DEVICE rows of dim elements of y_dtype, y_stride apart, with
  *          pre (DEVICE float32 [dim]); or NULL: no second norm, pre ignored.
  * The residual stream and all sums are float32; a binary16 y is rounded once.

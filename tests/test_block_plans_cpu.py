@@ -52,3 +52,20 @@ def test_split_calls_refuse_bad_workspaces():
     assert status(at[7] + 64, need) == q4.EALIGN
     assert status(at[2], need) == q4.EALIAS
     assert status(at[3] + 4096 - 256, need) == q4.EALIAS
+
+
+@pytest.mark.parametrize("moved", [
+    dict(y=63), dict(y=65), dict(y=128), dict(y=300), dict(h_out=1), dict(h_out=129),
+    dict(y=64, y_stride=321), dict(y=64, y_dtype=q4.F16), dict(gate=255, gate_col=0)])
+def test_residual_norm_refuses_columns_that_meet(moved):
+    """Columns of one wide buffer (rows of 320: h from 0 on, b from 128, h_out from
+    192, y from 256) that share an element, or rows of different strides."""
+    f = dict(h=0, b=128, h_out=192, y=256, gate=None, gate_col=1, y_dtype=q4.F32, y_stride=320)
+    f.update(moved)
+    at = {name: 0 if f[name] is None else (1 << 36) + 4 * f[name]
+          for name in ("h", "b", "h_out", "y", "gate")}
+    with pytest.raises(q4.Q4Error) as e:
+        q4.q4_0_residual_norm(at["b"], q4.F32, 320, 0, at["gate"], 320, f["gate_col"], 1.0, at["h"],
+                              at["h_out"], 320, 2 << 36, 0.0, 1e-6, at["y"], f["y_dtype"],
+                              f["y_stride"], 3, 64)
+    assert e.value.status == q4.EALIAS

@@ -280,3 +280,25 @@ def test_attention_faint_weights_count(gap, tokens, half):
     got = y[:, :, 1].double().cpu().numpy()
     assert (np.abs(got - want[:, None]) <= tol[:, None]).all(), np.abs(got - want[:, None]).max()
     assert (y[:, :, 0] == 0).all() and (y[:, :, 2:] == 0).all()
+
+
+# ---- residual norm ------------------------------------------------------------
+@pytest.mark.parametrize("dim", [8, 130])
+def test_residual_norm_columns_of_one_buffer(dim):
+    """h, b, h_out, y and the gate as columns of one buffer: they share its rows
+    and no element."""
+    n, rng = 5, np.random.default_rng(dim)
+    x = rng.standard_normal((n, 5 * dim)).astype(np.float32)
+    wide = dev(x)
+    h, b, gate, out, y = (wide[:, i * dim:(i + 1) * dim] for i in range(5))
+    pre, post = (dev((1 + rng.random(dim)).astype(np.float32)) for _ in range(2))
+    got = q4.residual_norm(h, b, pre, post, gate, 0.5, h_out=out, y=y)
+    torch.cuda.synchronize()
+    rh, ry = block.residual_norm(x[:, :dim], x[:, dim:2 * dim], pre.double().cpu().numpy(),
+                                 post.double().cpu().numpy(), x[:, 2 * dim:3 * dim], 0.5)
+    # norms and sums of dim terms, a few roundings of each element, all below 32
+    tol = (dim + 20) * H32 * 32
+    near(got[0], rh, tol)
+    near(got[1], ry, tol)
+    assert got[0] is out and got[1] is y
+    assert torch.equal(wide[:, :3 * dim], dev(x[:, :3 * dim]))
