@@ -17,7 +17,12 @@
 // running maximum rescales it by a per-lane factor.
 //
 // Float32 rows split q and the weights into binary16 high and low parts (two
-// products each): 22 bits, since K and V are binary16 exactly.
+// products each): 22 bits, since K and V are binary16 exactly.  Few rows (32-row
+// tiles) split the weights of binary16 rows too: bound by the bytes, they pay
+// nothing for it (64 conversations 182 us either way; 131071 keys 83.5 and 82.5),
+// and their results are off by the result's own rounding alone.  Passes round
+// such weights once (2^-11): in two parts two prompts took 431 instead of 318 us,
+// 512 tokens under a window 23.5 instead of 20.6.
 //
 // Keys come through LDS by direct copies, in groups of 16 rows (a group never
 // crosses a page), the 16-byte pieces of row `key` XOR-swizzled by swz(key) so
@@ -259,15 +264,17 @@ template <int DIM, bool ONCE> struct Filler {
 };
 
 // One wave's 32 rows: its queries, running maximum (of scale log2(e) q.k), sum
-// (this lane's half of the keys) and unnormalised result.
-template <int DIM, bool F32> struct Rows {
-    static constexpr int kParts = F32 ? 2 : 1;
+// (this lane's half of the keys) and unnormalised result.  FINE: weights in two
+// parts.
+template <int DIM, bool F32, bool FINE> struct Rows {
+    static constexpr int kParts = F32 ? 2 : 1;       // of q
+    static constexpr int kWeights = FINE ? 2 : 1;    // of a weight
     // Weights are held as 2^kShift exp(s - m), where m may lag behind the true
     // maximum by kLag (in powers of two) before the accumulators are rescaled:
     // 2^15 < 65504 at most.  Binary16's smallest step is then 2^-32 of the
-    // largest weight; float32 rows rescale more often and keep 2^-39, so that
-    // a hundred thousand faint weights beside a strong one keep their sum.
-    static constexpr float kShift = F32 ? 14.0f : 7.0f, kLag = F32 ? 1.0f : 8.0f;
+    // largest weight; weights in two parts rescale more often and keep 2^-39, so
+    // that a hundred thousand faint ones beside a strong one keep their sum.
+    static constexpr float kShift = FINE ? 14.0f : 7.0f, kLag = FINE ? 1.0f : 8.0f;
     static constexpr float kFar = 65536.0f;
     h8_t q[kParts][DIM / 16];
     f16x_t o[DIM / 32];
@@ -375,7 +382,7 @@ template <int DIM, bool F32> struct Rows {
 
     // Weights of KT keys as the second product's B operands, 16 keys each.
     template <int KT> struct Weights {
-        h8_t w[KT / 16][kParts];
+        h8_t w[KT / 16][kWeights];
     };
 
     // Scores to weights; maximum, sum and what is accumulated so far brought
@@ -421,10 +428,10 @@ template <int DIM, bool F32> struct Rows {
                 out.w[b][0][i] = hi[0];
                 out.w[b][0][i + 1] = hi[1];
                 l = __builtin_amdgcn_fdot2(hi, ones, l, false);
-                if (F32) {
+                if (FINE) {
                     const h2_t lo = {(_Float16)(x0 - (float)hi[0]), (_Float16)(x1 - (float)hi[1])};
-                    out.w[b][kParts - 1][i] = lo[0];
-                    out.w[b][kParts - 1][i + 1] = lo[1];
+                    out.w[b][kWeights - 1][i] = lo[0];
+                    out.w[b][kWeights - 1][i + 1] = lo[1];
                     l = __builtin_amdgcn_fdot2(lo, ones, l, false);
                 }
             }
@@ -480,7 +487,7 @@ template <int DIM, bool F32> struct Rows {
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < kParts; ++x)
+                for (int x = 0; x < kWeights; ++x)
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[x], o[d], 0, 0, 0);
             }
         }
@@ -568,7 +575,7 @@ template <int DIM, int RW, int KW> struct Pass {
 };
 
 template <int DIM, bool F32, int RW, int KW, bool CAREFUL>
-__device__ __forceinline__ void pass_loop(Rows<DIM, F32> &w, Filler<DIM, false> &f,
+__device__ __forceinline__ void pass_loop(Rows<DIM, F32, F32> &w, Filler<DIM, false> &f,
                                           const Reach<Pass<DIM, RW, KW>::KT> &r, int t0, int t1,
                                           int top_lo, uint8_t *lds) {
     using P = Pass<DIM, RW, KW>;
@@ -641,9 +648,9 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
     const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int mine = wave % RW * 32 + lane % 32, row = row0 + mine;
-    Rows<DIM, F32> w;
+    Rows<DIM, F32, F32> w;
     {
-        typename Rows<DIM, F32>::Raw raw;
+        typename Rows<DIM, F32, F32>::Raw raw;
         w.request(raw, a, at, pl.group, hk, row, position0);
         w.take(raw);
     }
@@ -733,7 +740,7 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
 constexpr int kStepRows = 32, kStepKeys = 32;
 
 template <int DIM, bool F32, bool CAREFUL>
-__device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM, true> &f,
+__device__ __forceinline__ void step_loop(Rows<DIM, F32, true> &w, Filler<DIM, true> &f,
                                           const Reach<kStepKeys> &r, int t, int t1, int stride,
                                           int top_lo, uint8_t *kbuf, int look0,
                                           int look1, bool started) {
@@ -780,7 +787,7 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32> &w, Filler<DIM, true> &
             counted = f.fill(r, page0, next, kbuf, false);
             counted &= f.fill(r, page1, next + 16, kbuf + kHalf, false);
         }
-        typename Rows<DIM, F32>::template Weights<KT> ws;
+        typename Rows<DIM, F32, true>::template Weights<KT> ws;
         w.template weights<KT, CAREFUL>(ws, s);
         // outstanding: V, then the next K
         if (counted)
@@ -825,11 +832,11 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Attenti
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     uint8_t *mine = lds + wave * kShare;
     Filler<DIM, true> f(a, at.s, hk);
-    Rows<DIM, F32> w;
+    Rows<DIM, F32, true> w;
     const int t = t0 + wave;
     int look0 = -1, look1 = -1;
     {
-        typename Rows<DIM, F32>::Raw raw;
+        typename Rows<DIM, F32, true>::Raw raw;
         if (t < t1) {
             const int k = r.key(min(t + lane * W, t1 - 1));
             look0 = f.look(k);

@@ -411,9 +411,10 @@ int q4_0_kv_append(const q4_0_kv_cache *cache, const q4_0_rotary *rot, const voi
  *             page outside [0, pages), or past the table's end, is NaN.
  *   workspace, workspace_bytes : q4_0_attention_workspace_size gives the need
  *             (partial results of a key axis split across workgroups).
- * Binary16 x: products of binary16 values, each weight rounded to binary16
- * before its product with V.  Float32 x: q and the weights as binary16 high
- * and low parts (22 bits).  Scores, maxima and sums are float32 in both.
+ * Binary16 x: products of binary16 values.  Float32 x: q as binary16 high and
+ * low parts (22 bits).  The weights enter their product with V as such parts
+ * too; on the tiles of binary16 passes (q4_0_select_attention: 64 and 128 rows)
+ * each is rounded to binary16 instead.  Scores, maxima and sums are float32.
  * K or V that a row does not see never change it, infinities and NaN included.
  * dim 64, 128 or 256 (Q4_0_EUNSUPPORTED otherwise); q_heads a multiple of the
  * cache's heads, at most 1024; 1 <= n <= Q4_0_MAX_N, 1 <= batch <= Q4_0_MAX_N;

@@ -302,3 +302,21 @@ def test_residual_norm_columns_of_one_buffer(dim):
     near(got[1], ry, tol)
     assert got[0] is out and got[1] is y
     assert torch.equal(wide[:, :3 * dim], dev(x[:, :3 * dim]))
+
+
+# ---- attention: what a result of few rows is off by ----------------------------
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lengths,window", [([(1, 20), (1, 37), (1, 3)], 0), ([(8, 30)], 0),
+                                            ([(3, 200), (5, 24)], 20)])
+def test_attention_of_few_binary16_rows_is_off_by_its_rounding(lengths, window, dim):
+    """Up to 32 rows to a conversation a binary16 result carries the rounding of
+    its own type, and of float32 weights and sums besides.  (Few keys and small
+    scores keep those far below a binary16 weight's rounding.)"""
+    kc, vc, q, start, lens, table = batch_inputs(lengths, 8, 2, dim, 16, True, dim, window, 4,
+                                                 q_scale=0.25)
+    assert q4.q4_0_select_attention(q4.q4_0_kv_cache(0, 0, len(kc), 2, 16, dim), 8, q4.F16,
+                                    len(q), table.shape[1], len(lengths), window, 4) == 32
+    ref, absolute, score = block.attend(kc, vc, q, start, lens, table, window, 4, dim ** -0.5)
+    y = attend(kc, vc, q, start, lens, table, window, 4, dim ** -0.5)
+    near(y, ref, attention_tol(ref, absolute, score, 40, dim, False) + np.abs(ref) * H16
+         + 2.0 ** -25)
