@@ -350,8 +350,10 @@ template <int DIM, bool F32, bool FINE> struct Rows {
     }
 
     // Scores of KT keys from k0 on, K in LDS.  masked: some row sees not all of
-    // them.
-    template <int KT>
+    // them.  CAREFUL: the high parts of float32 queries alone decide whether a
+    // score is minus infinity: beside an infinite key the low parts, 0 or of
+    // either sign, make NaN.
+    template <int KT, bool CAREFUL>
     __device__ __forceinline__ void scores(f16x_t (&s)[KT / 32], const uint8_t *kbuf, int k0,
                                            bool masked, int sinks) const {
         const int lane = threadIdx.x % 64, half = lane / 32;
@@ -361,12 +363,27 @@ template <int DIM, bool F32, bool FINE> struct Rows {
             for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
             const int key = lane % 32;
             const uint8_t *row = kbuf + (t * 32 + key) * DIM * 2;
+            const auto add = [&](int x0, int x1) {
 #pragma unroll
-            for (int d = 0; d < DIM / 16; ++d) {
-                const h8_t k = *(const h8_t *)(row + (((2 * d + half) ^ swz<DIM>(key)) * 16));
+                for (int d = 0; d < DIM / 16; ++d) {
+                    const h8_t k = *(const h8_t *)(row + (((2 * d + half) ^ swz<DIM>(key)) * 16));
 #pragma unroll
-                for (int x = 0; x < kParts; ++x)
-                    s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[x][d], s[t], 0, 0, 0);
+                    for (int x = 0; x < kParts; ++x) {
+                        if (x < x0 || x >= x1) continue;
+                        s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[x][d], s[t], 0, 0, 0);
+                    }
+                }
+            };
+            add(0, CAREFUL ? 1 : kParts);
+            if (CAREFUL) {
+                uint32_t gone = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) gone |= (s[t][i] == -INFINITY ? 1u : 0u) << i;
+                asm volatile("" ::: "memory");  // K is read again, not held
+                add(1, kParts);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (F32 && (gone >> i & 1)) s[t][i] = -INFINITY;
             }
         }
         if (masked) {
@@ -497,7 +514,7 @@ template <int DIM, bool F32, bool FINE> struct Rows {
     __device__ __forceinline__ void step(const uint8_t *kbuf, const uint8_t *vbuf, int k0,
                                          bool masked, int sinks) {
         f16x_t s[KT / 32];
-        scores<KT>(s, kbuf, k0, masked, sinks);
+        scores<KT, CAREFUL>(s, kbuf, k0, masked, sinks);
         Weights<KT> ws;
         weights<KT, CAREFUL>(ws, s);
         mix<KT, CAREFUL>(ws, vbuf, k0, sinks);
@@ -771,7 +788,7 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32, true> &w, Filler<DIM, t
             Q4_WAIT_VMCNT(0);
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
-        w.template scores<KT>(s, kbuf, k, CAREFUL || !r.all(k, KT, top_lo), r.sinks);
+        w.template scores<KT, CAREFUL>(s, kbuf, k, CAREFUL || !r.all(k, KT, top_lo), r.sinks);
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
         counted = false;

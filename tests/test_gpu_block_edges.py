@@ -320,3 +320,26 @@ def test_attention_of_few_binary16_rows_is_off_by_its_rounding(lengths, window, 
     y = attend(kc, vc, q, start, lens, table, window, 4, dim ** -0.5)
     near(y, ref, attention_tol(ref, absolute, score, 40, dim, False) + np.abs(ref) * H16
          + 2.0 ** -25)
+
+
+def clean(a):
+    return np.where(np.isfinite(a), a, 0.0)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("lengths", LENGTHS)
+def test_attention_infinite_keys(lengths, dim, half):
+    """A key whose score is minus infinity has the weight 0, whatever the type of
+    the queries; a score of plus infinity is NaN throughout."""
+    rng, kc, vc, start, lens, table = plain(lengths, dim, 13)
+    table[:] = np.arange(table.shape[1])
+    kc[0, :, 3, 0], kc[1, 1, 9, 1], kc[2, 0, 5, 1] = np.inf, -np.inf, -np.inf
+    q = rng.standard_normal((start[-1], 4, dim)).astype(np.float16 if half else np.float32)
+    q[:, :, 0], q[:, :, 1] = -np.abs(q[:, :, 0]) - 1, np.abs(q[:, :, 1]) + 1
+    q[::-5, 3, 0] *= -1
+    with np.errstate(invalid="ignore"):
+        ref, absolute, score = block.attend(kc, vc, q, start, lens, table, 0, 0, dim ** -0.5)
+    y = attend(kc, vc, q, start, lens, table, scale=dim ** -0.5)
+    assert np.isfinite(ref[-1, :3]).all() and np.isnan(ref[-1, 3]).all()
+    near(y, ref, attention_tol(clean(ref), clean(absolute), clean(score), 300, dim, half))
