@@ -350,13 +350,14 @@ template <int DIM, bool F32, bool FINE> struct Rows {
     }
 
     // Scores of KT keys from k0 on, K in LDS.  masked: some row sees not all of
-    // them.  CAREFUL: the high parts of float32 queries alone decide whether a
-    // score is minus infinity: beside an infinite key the low parts, 0 or of
-    // either sign, make NaN.
+    // them.  CAREFUL: bit i of `gone` is set where score i is minus infinity.
+    // The high parts of float32 queries alone decide that: beside an infinite
+    // key the low parts, 0 or of either sign, make NaN.
     template <int KT, bool CAREFUL>
-    __device__ __forceinline__ void scores(f16x_t (&s)[KT / 32], const uint8_t *kbuf, int k0,
-                                           bool masked, int sinks) const {
+    __device__ __forceinline__ uint32_t scores(f16x_t (&s)[KT / 32], const uint8_t *kbuf, int k0,
+                                               bool masked, int sinks) const {
         const int lane = threadIdx.x % 64, half = lane / 32;
+        uint32_t gone = 0;
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t) {
 #pragma unroll
@@ -376,14 +377,14 @@ template <int DIM, bool F32, bool FINE> struct Rows {
             };
             add(0, CAREFUL ? 1 : kParts);
             if (CAREFUL) {
-                uint32_t gone = 0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) gone |= (s[t][i] == -INFINITY ? 1u : 0u) << i;
+                for (int i = 0; i < 16; ++i)
+                    gone |= (s[t][i] == -INFINITY ? 1u : 0u) << (16 * t + i);
                 asm volatile("" ::: "memory");  // K is read again, not held
                 add(1, kParts);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (F32 && (gone >> i & 1)) s[t][i] = -INFINITY;
+                    if (F32 && (gone >> (16 * t + i) & 1)) s[t][i] = -INFINITY;
             }
         }
         if (masked) {
@@ -395,6 +396,7 @@ template <int DIM, bool F32, bool FINE> struct Rows {
                     if (!sees(k0 + t * 32 + 8 * (i / 4) + 4 * half + i % 4, sinks))
                         s[t][i] = -INFINITY;
         }
+        return gone;
     }
 
     // Weights of KT keys as the second product's B operands, 16 keys each.
@@ -458,7 +460,7 @@ template <int DIM, bool F32, bool FINE> struct Rows {
     // no numbers touch only the rows that see them.
     template <int KT, bool CAREFUL>
     __device__ __forceinline__ void mix(const Weights<KT> &ws, const uint8_t *vbuf, int k0,
-                                        int sinks) {
+                                        int sinks, uint32_t gone) {
         const int lane = threadIdx.x % 64, half = lane / 32;
 #pragma unroll
         for (int b = 0; b < KT / 16; ++b) {
@@ -477,7 +479,9 @@ template <int DIM, bool F32, bool FINE> struct Rows {
                     h8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
                 if (CAREFUL) {
                     // what is no number leaves the product; rows that see it
-                    // are given it afterwards (both signs: NaN)
+                    // are given it afterwards (both signs: NaN).  One whose
+                    // score is minus infinity has the weight 0, and 0 times an
+                    // infinity is NaN: it counts more than a tile's others.
                     h8_t up, down, see;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -485,9 +489,10 @@ template <int DIM, bool F32, bool FINE> struct Rows {
                         const bool bad = !__builtin_isfinite(x);
                         const bool seen =
                             sees(k0 + 16 * b + 8 * (i / 4) + 4 * half + i % 4, sinks);
+                        const bool none = gone >> (8 * b + i) & 1;
                         up[i] = (_Float16)(bad && !(x < 0.0f) ? 1.0f : 0.0f);
                         down[i] = (_Float16)(bad && !(x > 0.0f) ? 1.0f : 0.0f);
-                        see[i] = (_Float16)(seen ? 1.0f : 0.0f);
+                        see[i] = (_Float16)(seen ? none ? 64.0f : 1.0f : 0.0f);
                         if (bad) v[i] = (_Float16)0.0f;
                     }
                     f16x_t zero;
@@ -501,6 +506,7 @@ template <int DIM, bool F32, bool FINE> struct Rows {
                     for (int i = 0; i < 16; ++i) {
                         if (ups[i] > 0.0f) o[d][i] += INFINITY;
                         if (downs[i] > 0.0f) o[d][i] -= INFINITY;
+                        if (fmaxf(ups[i], downs[i]) >= 64.0f) o[d][i] = NAN;
                     }
                 }
 #pragma unroll
@@ -514,10 +520,10 @@ template <int DIM, bool F32, bool FINE> struct Rows {
     __device__ __forceinline__ void step(const uint8_t *kbuf, const uint8_t *vbuf, int k0,
                                          bool masked, int sinks) {
         f16x_t s[KT / 32];
-        scores<KT, CAREFUL>(s, kbuf, k0, masked, sinks);
+        const uint32_t gone = scores<KT, CAREFUL>(s, kbuf, k0, masked, sinks);
         Weights<KT> ws;
         weights<KT, CAREFUL>(ws, s);
-        mix<KT, CAREFUL>(ws, vbuf, k0, sinks);
+        mix<KT, CAREFUL>(ws, vbuf, k0, sinks, gone);
     }
 
     // After CAREFUL's tiles: the maximum in powers of two, as without.
@@ -788,7 +794,8 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32, true> &w, Filler<DIM, t
             Q4_WAIT_VMCNT(0);
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
-        w.template scores<KT, CAREFUL>(s, kbuf, k, CAREFUL || !r.all(k, KT, top_lo), r.sinks);
+        const uint32_t gone = w.template scores<KT, CAREFUL>(
+            s, kbuf, k, CAREFUL || !r.all(k, KT, top_lo), r.sinks);
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
         counted = false;
@@ -812,7 +819,7 @@ __device__ __forceinline__ void step_loop(Rows<DIM, F32, true> &w, Filler<DIM, t
         else
             Q4_WAIT_VMCNT(0);
         asm volatile("" ::: "memory");
-        w.template mix<KT, CAREFUL>(ws, vbuf, k, r.sinks);
+        w.template mix<KT, CAREFUL>(ws, vbuf, k, r.sinks, gone);
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
         if (more) {

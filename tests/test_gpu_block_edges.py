@@ -343,3 +343,26 @@ def test_attention_infinite_keys(lengths, dim, half):
     y = attend(kc, vc, q, start, lens, table, scale=dim ** -0.5)
     assert np.isfinite(ref[-1, :3]).all() and np.isnan(ref[-1, 3]).all()
     near(y, ref, attention_tol(clean(ref), clean(absolute), clean(score), 300, dim, half))
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("lengths", LENGTHS)
+def test_attention_infinite_keys_with_infinite_values(lengths, dim, half):
+    """A key whose score is minus infinity has the weight 0, and 0 times its
+    value's infinity is NaN in that column; finite values beside it count
+    nothing, and a score of plus infinity is NaN throughout."""
+    rng, kc, vc, start, lens, table = plain(lengths, dim, 12)
+    table[:] = np.arange(table.shape[1])
+    kc[0, :, 3, 0] = np.inf
+    vc[0, :, 3, 7], vc[0, 1, 3, 9] = np.inf, -np.inf
+    kc[2, 0, 5, 1], vc[2, 0, 5, 11] = -np.inf, np.nan
+    q = rng.standard_normal((start[-1], 4, dim)).astype(np.float16 if half else np.float32)
+    q[:, :, 0] = -np.abs(q[:, :, 0]) - np.finfo(q.dtype).tiny
+    q[::-5, 3, 0] *= -1
+    q[:, :, 1] = np.abs(q[:, :, 1]) + np.finfo(q.dtype).tiny
+    with np.errstate(invalid="ignore"):
+        ref, absolute, score = block.attend(kc, vc, q, start, lens, table, 0, 0, dim ** -0.5)
+    y = attend(kc, vc, q, start, lens, table, scale=dim ** -0.5)
+    assert np.isnan(ref[-1, 0, 7]) and np.isfinite(ref[-1, 0, 8]) and np.isnan(ref[-1, 3]).all()
+    near(y, ref, attention_tol(clean(ref), clean(absolute), clean(score), 300, dim, half))
