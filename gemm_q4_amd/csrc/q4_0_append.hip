@@ -145,7 +145,12 @@ hipError_t launch(const AppendArgs &a, hipStream_t stream) {
     const int total = a.q_heads + 2 * a.cache.heads;
     const int all = (total + groups - 1) / groups;
     // few tokens: one head per group, so the step is as short as one row;
-    // enough tokens to fill the device: a workgroup walks its whole token
+    // enough tokens to fill the device: a workgroup walks its whole token, whose
+    // angles it forms once.  Both ways (us; float32, binary16 alike): 32 + 2 x 8
+    // heads of 128, 256 tokens 4.9 and 5.8, 400 tokens 6.5 and 6.5, 512 tokens
+    // 7.4 and 6.7, 2048 tokens 19.6 and 17.4; 16 + 2 x 8 of 256, 256 tokens 5.7
+    // and 6.5, 400 tokens 7.8 and 7.1; 64 + 2 x 8 of 64, 341 tokens 5.3 and 6.0,
+    // 512 tokens 6.8 and 6.5.
     const int chunks = a.n * all <= 1024 ? all : 1;
     hipLaunchKernelGGL((append_kernel<XF16, QF16, LPH>), dim3((uint32_t)(a.n * chunks)),
                        dim3(kThreads), 0, stream, a, chunks);

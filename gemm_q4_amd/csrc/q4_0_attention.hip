@@ -579,11 +579,12 @@ __device__ __forceinline__ void put_ml(const AttentionArgs &a, const Plan &pl, i
 // RW = 4, KW = 1 reads a key least often; RW = 2, KW = 4 (or 2) keeps the
 // device busy when there are few rows.
 //
-// Two prompts of 5001 and 3146 tokens, 32 + 8 heads of 128, binary16: 330 us, 0.87
-// PFLOP/s, where the library's 8192-cubed product reaches 1.19 on this part.
+// Two prompts of 5001 and 3146 tokens, 32 + 8 heads of 128, binary16: 320 to 340 us,
+// 0.84 to 0.89 PFLOP/s, where the library's 8192-cubed product reaches 1.19 on
+// this part (float32: twice the products, 545 us).
 // Matrix, vector and LDS work are about as long as each other (per 64 keys and
-// SIMD 2048, 2000 and 2048 to 2800 cycles of 4800), and the clock falls to
-// about 1.5 GHz under them: eight waves in two groups that take turns at matrix
+// SIMD 2048, 2000 and 2048 to 2800 cycles of 4300), and the clock falls to
+// about 1.7 GHz under them: eight waves in two groups that take turns at matrix
 // and vector work, or fragments requested further ahead, cut the cycles and
 // not the time.
 template <int DIM, int RW, int KW> struct Pass {
@@ -1064,7 +1065,10 @@ Choice choose(const AttentionArgs &a) {
         // 400 to 8192 keys, joining included: 209 us unsplit, 187 us so, 203 us
         // in parts of 512; 32 of 4096 keys of 256: 95 us in three parts, 94 us
         // in four, 105 us in eight; 2 of 1700 keys: 17 us unsplit, 10 us in
-        // parts of 256.
+        // parts of 256.  Parts of 512, 1024 and 2048 keys elsewhere (us): 4 of
+        // 32768 keys 87, 83 and 81; 16 of 1600 to 32768 193, 193 and 198; 32 of
+        // 16384 (heads of 256) 213, 224 and 216; 128 of 100 to 2048 104, 117 and
+        // 100; 128 of 400 to 8192 (heads of 64) 181, 180 and 211.
         splits = ((a.batch == 1 ? 1 : 4) * slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
         const int64_t fair = (most * likely + slots - 1) / slots;
         ch.least = fair > 32 ? 32 : fair < 2 * ch.waves ? 2 * ch.waves : (int)fair;

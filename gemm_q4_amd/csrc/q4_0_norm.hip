@@ -188,9 +188,14 @@ hipError_t run(const NormArgs &a, hipStream_t stream) {
 }
 
 // Waves per row: up to eight, two chunks a lane, so that a row's loads are all
-// in flight at once and one row alone is short; then more chunks (rows of 5120,
-// 16383 of them: 196 us on eight waves, 204 on sixteen, 221 on four), and
-// sixteen waves only for what eight cannot hold.
+// in flight at once and one row alone is short; then more chunks, and sixteen
+// waves only for what eight cannot hold.  16383 binary16 rows (us): of 512 on one
+// wave 19, on four 26; of 1024 on four 34, on eight 42; of 2048 on four 75, on
+// eight 77 to 81; of 4096 on eight 147, on four 152, on sixteen 166; of 4608 on
+// eight 167, on four 187, on sixteen 188; of 8192 on eight 293, on four 316, on
+// sixteen 292.  One row gains by more waves (2048: 3.7 on four, 3.2 on eight;
+// 5120: 4.4 on eight, 4.0 on sixteen), float32 rows of 5120 too (16383: 242 on
+// eight, 230 on sixteen).
 template <bool RAGGED, bool BF16, bool YF16>
 hipError_t by_size(const NormArgs &a, hipStream_t stream) {
     const int lanes = (a.dim + 3) / 4;

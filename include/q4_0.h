@@ -400,6 +400,9 @@ int q4_0_kv_append(const q4_0_kv_cache *cache, const q4_0_rotary *rot, const voi
  * (a sliding window, and the first `sinks` positions that stay visible).  Pages
  * no token of the call sees are never read: their table entries may hold
  * anything.  A decode step is the batch with one token per conversation.
+ * Decode steps over long contexts beside a prompt's tokens run several times
+ * faster as a call of their own (on their rows of q, y, kv_len and table): tiles
+ * and parts are cut for a call as a whole.
  *   q       : DEVICE [n] rows of q_heads * dim elements of x_dtype, q_stride
  *             elements apart; base and row stride a multiple of 16 bytes.
  *   y       : DEVICE [n][q_heads][dim] of x_dtype, dense, 16-byte aligned.
