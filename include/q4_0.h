@@ -378,8 +378,9 @@ typedef struct q4_0_rotary {
  *   positions : DEVICE int32 [n], the rotation's positions.
  *   slots     : DEVICE int64 [n]: page * page_size + offset of each token's
  *               cache row.  A slot outside [0, pages * page_size) writes no
- *               cache row (a padded token: its q is still written).  Two tokens
- *               with one slot leave either's row there.
+ *               cache row (a padded token: its q is still written).  The
+ *               others are distinct: two tokens with one slot leave a mix of
+ *               their rows there, which may differ from run to run.
  * Sums and rotations in float32; K, V and a binary16 q_out are each rounded
  * once.  1 <= n <= Q4_0_MAX_N, 1 <= q_heads <= 1024.  No output overlaps an
  * input or another output (Q4_0_EALIAS).  Needs no workspace. */

@@ -186,8 +186,8 @@ def test_attention_128_row_tiles_non_finite(dim, half):
 @pytest.mark.parametrize("half", [True, False])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_attention_128_row_tiles_far_scores(dim, half):
-    """Scores around 2^40, one head's: exact ones, so the highest level a row
-    sees decides alone."""
+    """One head's scores near 2^40: exact ones, so the highest level a row sees
+    decides alone."""
     lengths = [(200, 200), (140, 160), (50, 50)]
     rng, kc, vc, start, lens, table = plain(lengths, dim, 9, pages=100)
     assert q4.q4_0_select_attention(q4.q4_0_kv_cache(0, 0, 100, HEADS_128, 16, dim), HEADS_128,
