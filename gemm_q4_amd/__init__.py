@@ -113,6 +113,19 @@ _SIGS = {
     "q4_0_attention_workspace_size": (_int, [_vp, _i64, _int, _i64, _i64, _i64, _i64, _i64,
                                              _szp]),
     "q4_0_select_attention": (_int, [_vp, _i64, _int, _i64, _i64, _i64, _i64, _i64]),
+    "q4_0_kv_append8": (_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _int, _i64,
+                               _vp, _vp, _i64, _vp]),
+    "q4_0_kv_read8": (_int, [_vp, _vp, _i64, _vp, _vp, _int, _vp]),
+    "q4_0_attention8": (_int, [_vp, _vp, _i64, _int, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
+                               _i64, _i64, _f32, _vp, _sz, _vp]),
+    "q4_0_attention8_workspace_size": (_int, [_vp, _i64, _int, _i64, _i64, _i64, _i64, _i64,
+                                              _szp]),
+    "q4_0_select_attention8": (_int, [_vp, _i64, _int, _i64, _i64, _i64, _i64, _i64]),
+    "q4_0_embed": (_int, [_vp, _vp, _i64, _i64, _i64, _f32, _vp, _vp, _f32, _f32, _vp, _int,
+                          _vp]),
+    "q4_0_verify": (_int, [_vp, _i64, _vp, _i64, _int, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp,
+                           _vp, _vp, _sz, _vp]),
+    "q4_0_verify_workspace_size": (_int, [_i64, _i64, _i64, _int, _szp]),
     "q4_0_residual_norm": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _i64,
                                   _vp, _f32, _f32, _vp, _int, _i64, _i64, _i64, _vp]),
 }
@@ -177,7 +190,9 @@ def _load_bind():
         return _Unusable(f"it was built with torch {_bind.torch_version}, this is torch "
                          f"{torch.__version__}")
     _bind.setup(*(ctypes.cast(getattr(_lib, name), _vp).value
-                  for name in ("q4_0_kv_append", "q4_0_attention", "q4_0_residual_norm")),
+                  for name in ("q4_0_kv_append", "q4_0_attention", "q4_0_residual_norm",
+                               "q4_0_kv_append8", "q4_0_attention8", "q4_0_kv_read8",
+                               "q4_0_embed", "q4_0_verify")),
                 _raw_stream)
     return _bind
 
@@ -387,6 +402,12 @@ class q4_0_kv_cache(ctypes.Structure):
                 ("dim", _i64)]
 
 
+class q4_0_kv_cache8(ctypes.Structure):
+    """An 8-bit paged cache's descriptor (struct q4_0_kv_cache8 of include/q4_0.h)."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("pages", _i64),
+                ("heads", _i64), ("page_size", _i64), ("dim", _i64)]
+
+
 class q4_0_rotary(ctypes.Structure):
     """Position rotation and per-head norms (struct q4_0_rotary of include/q4_0.h)."""
     _fields_ = [("inv_freq", _vp), ("rot_dim", _i64), ("interleaved", _int),
@@ -395,7 +416,8 @@ class q4_0_rotary(ctypes.Structure):
 
 
 def _ref(struct):
-    """Address of a descriptor: a ctypes structure, or kv_cache()'s or rotary()'s."""
+    """Address of a descriptor: a ctypes structure, or kv_cache()'s, kv_cache8()'s or
+    rotary()'s."""
     if struct is None:
         return None
     return ctypes.addressof(struct) if isinstance(struct, ctypes.Structure) else struct.address
@@ -432,6 +454,67 @@ def q4_0_select_attention(cache, q_heads: int, x_dtype: int, n: int, table_strid
                           batch: int, window: int = 0, sinks: int = 0) -> int:
     return _check(_lib.q4_0_select_attention(_ref(cache), q_heads, x_dtype, n, table_stride, batch,
                                              window, sinks), "q4_0_select_attention")
+
+
+def q4_0_kv_append8(cache, rot, q, q_stride: int, k, k_stride: int, v, v_stride: int,
+                    x_dtype: int, q_out, q_dtype: int, q_heads: int, positions, slots, n: int,
+                    stream=None) -> None:
+    """cache: q4_0_kv_cache8; rot: q4_0_rotary or None."""
+    _check(_lib.q4_0_kv_append8(_ref(cache), _ref(rot), _ptr(q), q_stride, _ptr(k), k_stride,
+                                _ptr(v), v_stride, x_dtype, _ptr(q_out), q_dtype, q_heads,
+                                _ptr(positions), _ptr(slots), n, _stream(stream, k, v)),
+           "q4_0_kv_append8")
+
+
+def q4_0_kv_read8(cache, slots, n: int, k, v, y_dtype: int, stream=None) -> None:
+    """cache: q4_0_kv_cache8."""
+    _check(_lib.q4_0_kv_read8(_ref(cache), _ptr(slots), n, _ptr(k), _ptr(v), y_dtype,
+                              _stream(stream, slots, k, v)), "q4_0_kv_read8")
+
+
+def q4_0_attention8(cache, q, q_stride: int, x_dtype: int, q_heads: int, y, n: int, q_start,
+                    kv_len, table, table_stride: int, batch: int, window: int, sinks: int,
+                    scale: float, workspace=None, workspace_bytes=None, stream=None) -> None:
+    """cache: q4_0_kv_cache8."""
+    _check(_lib.q4_0_attention8(_ref(cache), _ptr(q), q_stride, x_dtype, q_heads, _ptr(y), n,
+                                _ptr(q_start), _ptr(kv_len), _ptr(table), table_stride, batch,
+                                window, sinks, scale, _ptr(workspace),
+                                _nbytes(workspace, workspace_bytes), _stream(stream, q, y)),
+           "q4_0_attention8")
+
+
+def q4_0_attention8_workspace_size(cache, q_heads: int, x_dtype: int, n: int, table_stride: int,
+                                   batch: int, window: int = 0, sinks: int = 0) -> int:
+    return _size(_lib.q4_0_attention8_workspace_size, "q4_0_attention8_workspace_size",
+                 _ref(cache), q_heads, x_dtype, n, table_stride, batch, window, sinks)
+
+
+def q4_0_select_attention8(cache, q_heads: int, x_dtype: int, n: int, table_stride: int,
+                           batch: int, window: int = 0, sinks: int = 0) -> int:
+    return _check(_lib.q4_0_select_attention8(_ref(cache), q_heads, x_dtype, n, table_stride,
+                                              batch, window, sinks), "q4_0_select_attention8")
+
+
+def q4_0_embed(packed, tokens, n: int, out: int, in_: int, scale: float, h, pre,
+               weight_offset: float, eps: float, y, y_dtype: int, stream=None) -> None:
+    _check(_lib.q4_0_embed(_ptr(packed), _ptr(tokens), n, out, in_, scale, _ptr(h), _ptr(pre),
+                           weight_offset, eps, _ptr(y), y_dtype, _stream(stream, h, tokens)),
+           "q4_0_embed")
+
+
+def q4_0_verify(logits, stride: int, drafted, drafted_stride: int, x_dtype: int, vocab: int,
+                tokens, q_start, n: int, batch: int, temperature, uniform, accepted, next_,
+                workspace=None, workspace_bytes=None, stream=None) -> None:
+    _check(_lib.q4_0_verify(_ptr(logits), stride, _ptr(drafted), drafted_stride, x_dtype, vocab,
+                            _ptr(tokens), _ptr(q_start), n, batch, _ptr(temperature),
+                            _ptr(uniform), _ptr(accepted), _ptr(next_), _ptr(workspace),
+                            _nbytes(workspace, workspace_bytes),
+                            _stream(stream, logits, accepted)), "q4_0_verify")
+
+
+def q4_0_verify_workspace_size(n: int, batch: int, vocab: int, drafted: bool = False) -> int:
+    return _size(_lib.q4_0_verify_workspace_size, "q4_0_verify_workspace_size", n, batch, vocab,
+                 int(bool(drafted)))
 
 
 def q4_0_residual_norm(b, b_dtype: int, b_stride: int, post, gate, gate_row: int, gate_col: int,
@@ -573,6 +656,13 @@ def kv_cache(k, v):
     return _bind.kv_cache(k, v)
 
 
+def kv_cache8(k, v, k_scale, v_scale):
+    """Descriptor of an 8-bit paged cache: k and v int8 [pages, heads, page_size, dim]
+    and their scales float32 [pages, heads, page_size], CUDA tensors, held and read
+    anew as by kv_cache().  kv_append, kv_read and attention take it."""
+    return _bind.kv_cache8(k, v, k_scale, v_scale)
+
+
 def rotary(inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q_norm=None,
            k_norm=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """Descriptor of a rotation (inv_freq: float32 [rot_dim / 2], or None) and of
@@ -582,9 +672,9 @@ def rotary(inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q_n
 
 
 def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
-    """Append k and v to `cache` and rotate q: q [n, q_heads * dim] (or None), k
-    and v [n, heads * dim], or the same with the heads as a dimension; rows may
-    be slices of wider ones.  positions int32 [n], slots int64 [n].  Returns the
+    """Append k and v to `cache` (kv_cache()'s; kv_cache8()'s: in 8 bits) and rotate
+    q: q [n, q_heads * dim] (or None), k and v [n, heads * dim], or the same with
+    the heads as a dimension; rows may be slices of wider ones.  positions int32 [n], slots int64 [n].  Returns the
     rotated q [n, q_heads, dim]: q_out, or a new tensor of q's type."""
     if q is not None and q_out is None:
         heads = q.shape[1] if q.dim() == 3 else q.shape[1] // cache.dim
@@ -594,16 +684,33 @@ def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
     return None if q is None else q_out
 
 
+def kv_read(cache, slots, k=None, v=None, dtype=None, stream=None):
+    """(k, v): rows of an 8-bit cache (kv_cache8()'s) as numbers, [n, heads, dim] of
+    `dtype` (float16 unless given): as given, or new tensors.  slots int64 [n]."""
+    shape = (slots.shape[0], cache.heads, cache.dim)
+    if dtype is None:
+        given = k if k is not None else v
+        dtype = torch.float16 if given is None else given.dtype
+    if k is None:
+        k = _new(stream, shape, dtype=dtype, device=slots.device)
+    if v is None:
+        v = _new(stream, shape, dtype=dtype, device=slots.device)
+    _check(_bind.kv_read(cache, slots, k, v, _handle(stream)), "q4_0_kv_read8")
+    return k, v
+
+
 def attention(cache, q, q_start, kv_len, table, window: int = 0, sinks: int = 0, scale=None,
               y=None, stream=None, ws=None):
-    """Attention of q [n, q_heads, dim] over `cache` (q4_0_attention): q_start
-    int32 [batch + 1], kv_len int32 [batch], table int32 [batch, pages of the
+    """Attention of q [n, q_heads, dim] over `cache` (q4_0_attention; kv_cache8()'s:
+    q4_0_attention8): q_start int32 [batch + 1], kv_len int32 [batch], table int32 [batch, pages of the
     longest].  scale: dim ** -0.5 unless given.  Returns y, like q."""
     if y is None:
         y = _new(stream, q.shape, dtype=q.dtype, device=q.device)
     if ws is None:
-        need = q4_0_attention_workspace_size(cache, q.shape[1], dtype_code(q), q.shape[0],
-                                             table.shape[-1], kv_len.shape[0], window, sinks)
+        size = (q4_0_attention8_workspace_size if _bind.is_cache8(cache)
+                else q4_0_attention_workspace_size)
+        need = size(cache, q.shape[1], dtype_code(q), q.shape[0], table.shape[-1],
+                    kv_len.shape[0], window, sinks)
         ws = _new(stream, need, dtype=torch.uint8, device=q.device) if need else None
     if scale is None:
         scale = cache.dim ** -0.5
@@ -637,3 +744,41 @@ def residual_norm(h, b=None, pre=None, post=None, gate=None, alpha: float = 1.0,
     _check(_bind.residual_norm(h, b, pre, post, gate, alpha, eps, weight_offset, h_out, y,
                                _handle(stream)), "q4_0_residual_norm")
     return h_out, y
+
+
+def embed(packed, tokens, out: int, in_: int, scale: float = 1.0, pre=None, eps: float = 1e-6,
+          weight_offset: float = 0.0, h=None, y=None, y_dtype=None, stream=None):
+    """(h, y): h [n, in_] float32 the rows `tokens` (int32 [n]) of a repacked table,
+    times scale, and y = N(h; pre) (q4_0_embed): as given, or new tensors (y of
+    y_dtype, float32 unless given; None without pre)."""
+    shape = (tokens.shape[0], in_)
+    if h is None:
+        h = _new(stream, shape, dtype=torch.float32, device=tokens.device)
+    if pre is None:
+        y = None
+    elif y is None:
+        y = _new(stream, shape, dtype=y_dtype or torch.float32, device=tokens.device)
+    _check(_bind.embed(packed, tokens, out, in_, scale, pre, eps, weight_offset, h, y,
+                       _handle(stream)), "q4_0_embed")
+    return h, y
+
+
+def verify(logits, tokens, q_start, uniform, draft_logits=None, temperature=None, accepted=None,
+           following=None, stream=None, ws=None):
+    """(accepted, following), int32 [batch]: how many of each conversation's drafted
+    tokens the target's logits [n, vocab] take, and the token that follows them
+    (q4_0_verify).  tokens int32 [n] (the step's tokens: row t judges tokens[t + 1]),
+    q_start int32 [batch + 1], uniform float32 [n, 2], draft_logits like logits or
+    None (drafts that were picked), temperature float32 [batch] or None (1)."""
+    batch = q_start.shape[0] - 1
+    if accepted is None:
+        accepted = _new(stream, batch, dtype=torch.int32, device=logits.device)
+    if following is None:
+        following = _new(stream, batch, dtype=torch.int32, device=logits.device)
+    if ws is None:
+        need = q4_0_verify_workspace_size(logits.shape[0], batch, logits.shape[-1],
+                                          draft_logits is not None)
+        ws = _new(stream, need, dtype=torch.uint8, device=logits.device)
+    _check(_bind.verify(logits, tokens, q_start, uniform, draft_logits, temperature, accepted,
+                        following, ws, _handle(stream)), "q4_0_verify")
+    return accepted, following

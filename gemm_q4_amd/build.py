@@ -20,8 +20,8 @@ BIND = os.path.join(HERE, "_bind.so")
 CXX = os.environ.get("CXX", "g++")
 SOURCES = ["q4_0_api.hip", "q4_0_repack.hip", "q4_0_gemv_dpp.hip",
            "q4_0_gemv_mfma.hip", "q4_0_gemv_w4a8.hip", "q4_0_gemm.hip",
-           "q4_0_append.hip", "q4_0_attention.hip", "q4_0_norm.hip",
-           "q4_0_calibrate.hip"]
+           "q4_0_append.hip", "q4_0_attention.hip", "q4_0_attention8.hip", "q4_0_norm.hip",
+           "q4_0_embed.hip", "q4_0_verify.hip", "q4_0_calibrate.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

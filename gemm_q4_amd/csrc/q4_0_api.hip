@@ -282,34 +282,70 @@ size_t routed_workspace(int form, int64_t n, int64_t k, int64_t n_experts, int64
                : q4::gemv_mfma_by_expert_workspace_bytes(n, k, n_experts, out, in);
 }
 
-// Checks of a cache descriptor (host) and the kernels' view of it.
-int check_cache(const q4_0_kv_cache *c, bool pointers) {
-    if (!c) return Q4_0_ENULL;
-    if (c->pages < 1 || c->pages > INT32_MAX || c->heads < 1 || c->heads > 1024)
-        return Q4_0_ESHAPE;
-    if (c->dim < 8 || c->dim > 512 || c->dim % 8 != 0) return Q4_0_ESHAPE;
-    if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0)
+// What a call needs to know of a cache, binary16 or 8-bit.
+struct CacheInfo {
+    q4::KvCache view;
+    int64_t heads, page_size, dim;
+    Span spans[4];  // K, V, and an 8-bit cache's scales
+};
+
+// Checks of a cache's sizes; `el` bytes an element.
+int check_cache_sizes(int64_t pages, int64_t heads, int64_t page_size, int64_t dim, int64_t el) {
+    if (pages < 1 || pages > INT32_MAX || heads < 1 || heads > 1024) return Q4_0_ESHAPE;
+    if (dim < 8 || dim > 512 || dim % 8 != 0) return Q4_0_ESHAPE;
+    if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0)
         return Q4_0_ESHAPE;
     // at most 2^10 heads x 2^16 x 2^9 x 2 bytes a page, so the product below
     // cannot overflow once pages is checked against it
-    const int64_t page = c->heads * c->page_size * c->dim * 2;
-    if (c->pages > (INT64_C(1) << 62) / page) return Q4_0_ESHAPE;
-    if (!pointers) return Q4_0_OK;
-    if (!c->k || !c->v) return Q4_0_ENULL;
-    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return Q4_0_EALIGN;
-    const size_t bytes = (size_t)c->pages * (size_t)page;
-    if (overlaps(c->k, bytes, c->v, bytes)) return Q4_0_EALIAS;
+    if (pages > (INT64_C(1) << 62) / (heads * page_size * dim * el)) return Q4_0_ESHAPE;
     return Q4_0_OK;
 }
 
-size_t cache_bytes(const q4_0_kv_cache *c) {
-    return (size_t)c->pages * (size_t)(c->heads * c->page_size * c->dim * 2);
+q4::KvCache cache_view(void *k, void *v, float *ks, float *vs, int64_t pages, int64_t heads,
+                       int64_t page_size, int64_t dim) {
+    int shift = 0;
+    while ((INT64_C(1) << shift) < page_size) ++shift;
+    return {k, v, ks, vs, pages, (int)heads, shift, (int)dim};
 }
 
-q4::KvCache cache_view(const q4_0_kv_cache *c) {
-    int shift = 0;
-    while ((INT64_C(1) << shift) < c->page_size) ++shift;
-    return {(_Float16 *)c->k, (_Float16 *)c->v, c->pages, (int)c->heads, shift, (int)c->dim};
+bool spans_meet(const Span *s, int count) {
+    for (int i = 0; i < count; ++i)
+        for (int j = i + 1; j < count; ++j)
+            if (overlaps(s[i].p, s[i].len, s[j].p, s[j].len)) return true;
+    return false;
+}
+
+// Checks of a cache descriptor (host) and what the call sees of it.
+int check_cache(const q4_0_kv_cache *c, bool pointers, CacheInfo *info) {
+    if (!c) return Q4_0_ENULL;
+    const int st = check_cache_sizes(c->pages, c->heads, c->page_size, c->dim, 2);
+    if (st != Q4_0_OK) return st;
+    const size_t bytes = (size_t)c->pages * (size_t)(c->heads * c->page_size * c->dim * 2);
+    *info = {cache_view(c->k, c->v, nullptr, nullptr, c->pages, c->heads, c->page_size, c->dim),
+             c->heads, c->page_size, c->dim,
+             {{c->k, bytes}, {c->v, bytes}, {nullptr, 0}, {nullptr, 0}}};
+    if (!pointers) return Q4_0_OK;
+    if (!c->k || !c->v) return Q4_0_ENULL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return Q4_0_EALIGN;
+    return spans_meet(info->spans, 2) ? Q4_0_EALIAS : Q4_0_OK;
+}
+
+int check_cache(const q4_0_kv_cache8 *c, bool pointers, CacheInfo *info) {
+    if (!c) return Q4_0_ENULL;
+    const int st = check_cache_sizes(c->pages, c->heads, c->page_size, c->dim, 1);
+    if (st != Q4_0_OK) return st;
+    const size_t rows = (size_t)c->pages * (size_t)(c->heads * c->page_size);
+    const size_t bytes = rows * (size_t)c->dim;
+    *info = {cache_view(c->k, c->v, c->k_scale, c->v_scale, c->pages, c->heads, c->page_size,
+                        c->dim),
+             c->heads, c->page_size, c->dim,
+             {{c->k, bytes}, {c->v, bytes}, {c->k_scale, rows * 4u}, {c->v_scale, rows * 4u}}};
+    if (!pointers) return Q4_0_OK;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return Q4_0_ENULL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+        !aligned(c->v_scale, 4))
+        return Q4_0_EALIGN;
+    return spans_meet(info->spans, 4) ? Q4_0_EALIAS : Q4_0_OK;
 }
 
 // Largest row stride (elements) accepted: rows, strides and sizes of a call
@@ -351,10 +387,11 @@ bool rows_meet(const RowSpan &a, const RowSpan &b) {
 }
 
 // Shape checks shared by q4_0_attention and its queries.
-int check_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, int64_t n,
+template <typename Cache>
+int check_attention(const Cache *cache, int64_t q_heads, int x_dtype, int64_t n,
                     int64_t table_stride, int64_t batch, int64_t window, int64_t sinks,
-                    bool pointers) {
-    const int st = check_cache(cache, pointers);
+                    bool pointers, CacheInfo *info) {
+    const int st = check_cache(cache, pointers, info);
     if (st != Q4_0_OK) return st;
     if (n < 1 || n > Q4_0_MAX_N || batch < 1 || batch > Q4_0_MAX_N) return Q4_0_ESHAPE;
     if (q_heads < 1 || q_heads > 1024 || q_heads % cache->heads != 0) return Q4_0_ESHAPE;
@@ -365,11 +402,11 @@ int check_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, in
     return Q4_0_OK;
 }
 
-q4::AttentionArgs attention_args(const q4_0_kv_cache *cache, int64_t q_heads, int64_t n,
+q4::AttentionArgs attention_args(const CacheInfo &info, int64_t q_heads, int64_t n,
                                  int64_t table_stride, int64_t batch, int64_t window,
                                  int64_t sinks) {
     q4::AttentionArgs a = {};
-    a.cache = cache_view(cache);
+    a.cache = info.view;
     a.q_heads = (int)q_heads;
     a.n = (int)n;
     a.batch = (int)batch;
@@ -377,6 +414,117 @@ q4::AttentionArgs attention_args(const q4_0_kv_cache *cache, int64_t q_heads, in
     a.window = (int)window;
     a.sinks = window ? (int)sinks : 0;
     return a;
+}
+
+template <typename Cache>
+int kv_append(const Cache *cache, const q4_0_rotary *rot, const void *q, int64_t q_stride,
+              const void *k, int64_t k_stride, const void *v, int64_t v_stride, int x_dtype,
+              void *q_out, int q_dtype, int64_t q_heads, const int32_t *positions,
+              const int64_t *slots, int64_t n, void *stream) {
+    CacheInfo info;
+    const int st = check_cache(cache, true, &info);
+    if (st != Q4_0_OK) return st;
+    const int64_t dim = cache->dim;
+    if (n < 1 || n > Q4_0_MAX_N) return Q4_0_ESHAPE;
+    if (!valid_dtype(x_dtype)) return Q4_0_EINVAL;
+    if (q && (q_heads < 1 || q_heads > 1024)) return Q4_0_ESHAPE;
+    if (q && !valid_dtype(q_dtype)) return Q4_0_EINVAL;
+    if (rot && (rot->rot_dim < 0 || rot->rot_dim > dim || rot->rot_dim % 8 != 0))
+        return Q4_0_ESHAPE;
+    const int64_t kw = cache->heads * dim, qw = q ? q_heads * dim : 0;
+    if (k_stride < kw || v_stride < kw || k_stride > kMaxStride || v_stride > kMaxStride ||
+        (q && (q_stride < qw || q_stride > kMaxStride)))
+        return Q4_0_ESHAPE;
+    if (!k || !v || !slots || (q && !q_out)) return Q4_0_ENULL;
+    const bool rotates = rot && rot->rot_dim > 0;
+    if (rotates && (!rot->inv_freq || !positions)) return Q4_0_ENULL;
+    const int64_t el = elem_bytes(x_dtype);
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride * el % 16 || v_stride * el % 16 ||
+        !aligned(slots, 8) || !aligned(positions, 4))
+        return Q4_0_EALIGN;
+    if (q && (!aligned(q, 16) || q_stride * el % 16 || !aligned(q_out, 16))) return Q4_0_EALIGN;
+    if (rot && (!aligned(rot->inv_freq, 4) || !aligned(rot->q_norm, 16) ||
+                !aligned(rot->k_norm, 16)))
+        return Q4_0_EALIGN;
+    const size_t norm_bytes = (size_t)dim * 4u;
+    const Span ins[8] = {
+        {k, rows_bytes(n, k_stride, kw, el)},
+        {v, rows_bytes(n, v_stride, kw, el)},
+        {q, q ? rows_bytes(n, q_stride, qw, el) : 0},
+        {rotates ? positions : nullptr, (size_t)n * 4u},
+        {slots, (size_t)n * 8u},
+        {rotates ? rot->inv_freq : nullptr, rotates ? (size_t)rot->rot_dim * 2u : 0},
+        {rot ? rot->q_norm : nullptr, norm_bytes},
+        {rot ? rot->k_norm : nullptr, norm_bytes}};
+    const Span outs[5] = {{q ? q_out : nullptr,
+                           q ? (size_t)(n * qw) * (size_t)elem_bytes(q_dtype) : 0},
+                          info.spans[0], info.spans[1], info.spans[2], info.spans[3]};
+    if (outputs_clash(outs, 5, ins, 8)) return Q4_0_EALIAS;
+    q4::AppendArgs a = {};
+    a.cache = info.view;
+    a.q = q, a.k = k, a.v = v;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.q_out = q_out;
+    a.q_heads = q ? (int)q_heads : 0;
+    a.positions = positions, a.slots = slots, a.n = n;
+    if (rot) {
+        a.inv_freq = rot->inv_freq, a.q_norm = rot->q_norm, a.k_norm = rot->k_norm;
+        a.rot_dim = (int)rot->rot_dim, a.interleaved = rot->interleaved != 0;
+        a.amplitude = rot->amplitude, a.eps = rot->eps, a.weight_offset = rot->weight_offset;
+    }
+    return map_hip(q4::launch_kv_append(a, x_dtype == Q4_0_F16, q && q_dtype == Q4_0_F16,
+                                        (hipStream_t)stream));
+}
+
+// The kernels for a cache of either kind.
+size_t attention_workspace(const q4::AttentionArgs &a, int f16) {
+    return a.cache.k_scale ? q4::attention8_workspace_bytes(a)
+                           : q4::attention_workspace_bytes(a, f16);
+}
+
+template <typename Cache>
+int attention(const Cache *cache, const void *q, int64_t q_stride, int x_dtype, int64_t q_heads,
+              void *y, int64_t n, const int32_t *q_start, const int32_t *kv_len,
+              const int32_t *table, int64_t table_stride, int64_t batch, int64_t window,
+              int64_t sinks, float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    CacheInfo info;
+    const int st = check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks,
+                                   true, &info);
+    if (st != Q4_0_OK) return st;
+    if (!(scale > 0.0f) || !isfinite(scale)) return Q4_0_EINVAL;
+    const int64_t qw = q_heads * cache->dim, el = elem_bytes(x_dtype);
+    if (q_stride < qw || q_stride > kMaxStride) return Q4_0_ESHAPE;
+    if (!q || !y || !q_start || !kv_len || !table) return Q4_0_ENULL;
+    if (!aligned(q, 16) || q_stride * el % 16 || !aligned(y, 16) || !aligned(q_start, 4) ||
+        !aligned(kv_len, 4) || !aligned(table, 4))
+        return Q4_0_EALIGN;
+    const Span spans[9] = {info.spans[0], info.spans[1], info.spans[2], info.spans[3],
+                           {q, rows_bytes(n, q_stride, qw, el)},
+                           {q_start, (size_t)(batch + 1) * 4u},
+                           {kv_len, (size_t)batch * 4u},
+                           {table, (size_t)(batch * table_stride) * 4u},
+                           {y, (size_t)(n * qw) * (size_t)el}};
+    if (outputs_clash(spans + 8, 1, spans, 8)) return Q4_0_EALIAS;
+    q4::AttentionArgs a = attention_args(info, q_heads, n, table_stride, batch, window, sinks);
+    a.q = q, a.q_stride = q_stride, a.y = y;
+    a.q_start = q_start, a.kv_len = kv_len, a.table = table;
+    a.scale = scale;
+    const int f16 = x_dtype == Q4_0_F16;
+    const int wst = check_workspace(workspace, workspace_bytes, attention_workspace(a, f16), spans,
+                                    9);
+    if (wst != Q4_0_OK) return wst;
+    return map_hip(a.cache.k_scale
+                       ? q4::launch_attention8(a, f16, workspace, (hipStream_t)stream)
+                       : q4::launch_attention(a, f16, workspace, (hipStream_t)stream));
+}
+
+// Shape checks shared by q4_0_verify and its query.
+int check_verify(int64_t n, int64_t batch, int64_t vocab, bool drafted) {
+    if (n < 1 || n > Q4_0_MAX_N || batch < 1 || batch > Q4_0_MAX_N) return Q4_0_ESHAPE;
+    if (vocab < 1 || vocab > Q4_0_MAX_OUT) return Q4_0_ESHAPE;
+    if (q4::verify_workspace_bytes(n, batch, vocab, drafted) > q4::kWorkspaceBytes)
+        return Q4_0_EUNSUPPORTED;
+    return Q4_0_OK;
 }
 
 }  // namespace
@@ -695,81 +843,58 @@ int q4_0_kv_append(const q4_0_kv_cache *cache, const q4_0_rotary *rot, const voi
                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                    int64_t v_stride, int x_dtype, void *q_out, int q_dtype, int64_t q_heads,
                    const int32_t *positions, const int64_t *slots, int64_t n, void *stream) {
-    const int st = check_cache(cache, true);
+    return kv_append(cache, rot, q, q_stride, k, k_stride, v, v_stride, x_dtype, q_out, q_dtype,
+                     q_heads, positions, slots, n, stream);
+}
+
+int q4_0_kv_append8(const q4_0_kv_cache8 *cache, const q4_0_rotary *rot, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, int x_dtype, void *q_out, int q_dtype, int64_t q_heads,
+                    const int32_t *positions, const int64_t *slots, int64_t n, void *stream) {
+    return kv_append(cache, rot, q, q_stride, k, k_stride, v, v_stride, x_dtype, q_out, q_dtype,
+                     q_heads, positions, slots, n, stream);
+}
+
+int q4_0_kv_read8(const q4_0_kv_cache8 *cache, const int64_t *slots, int64_t n, void *k, void *v,
+                  int y_dtype, void *stream) {
+    CacheInfo info;
+    const int st = check_cache(cache, true, &info);
     if (st != Q4_0_OK) return st;
-    const int64_t dim = cache->dim;
     if (n < 1 || n > Q4_0_MAX_N) return Q4_0_ESHAPE;
-    if (!valid_dtype(x_dtype)) return Q4_0_EINVAL;
-    if (q && (q_heads < 1 || q_heads > 1024)) return Q4_0_ESHAPE;
-    if (q && !valid_dtype(q_dtype)) return Q4_0_EINVAL;
-    if (rot && (rot->rot_dim < 0 || rot->rot_dim > dim || rot->rot_dim % 8 != 0))
-        return Q4_0_ESHAPE;
-    const int64_t kw = cache->heads * dim, qw = q ? q_heads * dim : 0;
-    if (k_stride < kw || v_stride < kw || k_stride > kMaxStride || v_stride > kMaxStride ||
-        (q && (q_stride < qw || q_stride > kMaxStride)))
-        return Q4_0_ESHAPE;
-    if (!k || !v || !slots || (q && !q_out)) return Q4_0_ENULL;
-    const bool rotates = rot && rot->rot_dim > 0;
-    if (rotates && (!rot->inv_freq || !positions)) return Q4_0_ENULL;
-    const int64_t el = elem_bytes(x_dtype);
-    if (!aligned(k, 16) || !aligned(v, 16) || k_stride * el % 16 || v_stride * el % 16 ||
-        !aligned(slots, 8) || !aligned(positions, 4))
-        return Q4_0_EALIGN;
-    if (q && (!aligned(q, 16) || q_stride * el % 16 || !aligned(q_out, 16))) return Q4_0_EALIGN;
-    if (rot && (!aligned(rot->inv_freq, 4) || !aligned(rot->q_norm, 16) ||
-                !aligned(rot->k_norm, 16)))
-        return Q4_0_EALIGN;
-    const size_t norm_bytes = (size_t)dim * 4u;
-    const Span ins[8] = {
-        {k, rows_bytes(n, k_stride, kw, el)},
-        {v, rows_bytes(n, v_stride, kw, el)},
-        {q, q ? rows_bytes(n, q_stride, qw, el) : 0},
-        {rotates ? positions : nullptr, (size_t)n * 4u},
-        {slots, (size_t)n * 8u},
-        {rotates ? rot->inv_freq : nullptr, rotates ? (size_t)rot->rot_dim * 2u : 0},
-        {rot ? rot->q_norm : nullptr, norm_bytes},
-        {rot ? rot->k_norm : nullptr, norm_bytes}};
-    const Span outs[3] = {{cache->k, cache_bytes(cache)},
-                          {cache->v, cache_bytes(cache)},
-                          {q ? q_out : nullptr,
-                           q ? (size_t)(n * qw) * (size_t)elem_bytes(q_dtype) : 0}};
-    if (outputs_clash(outs, 3, ins, 8)) return Q4_0_EALIAS;
-    q4::AppendArgs a = {};
-    a.cache = cache_view(cache);
-    a.q = q, a.k = k, a.v = v;
-    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
-    a.q_out = q_out;
-    a.q_heads = q ? (int)q_heads : 0;
-    a.positions = positions, a.slots = slots, a.n = n;
-    if (rot) {
-        a.inv_freq = rot->inv_freq, a.q_norm = rot->q_norm, a.k_norm = rot->k_norm;
-        a.rot_dim = (int)rot->rot_dim, a.interleaved = rot->interleaved != 0;
-        a.amplitude = rot->amplitude, a.eps = rot->eps, a.weight_offset = rot->weight_offset;
-    }
-    return map_hip(q4::launch_kv_append(a, x_dtype == Q4_0_F16, q && q_dtype == Q4_0_F16,
-                                        (hipStream_t)stream));
+    if (!valid_dtype(y_dtype)) return Q4_0_EINVAL;
+    if (!slots || (!k && !v)) return Q4_0_ENULL;
+    if (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return Q4_0_EALIGN;
+    const size_t bytes = (size_t)(n * info.heads * info.dim) * (size_t)elem_bytes(y_dtype);
+    const Span ins[5] = {info.spans[0], info.spans[1], info.spans[2], info.spans[3],
+                         {slots, (size_t)n * 8u}};
+    const Span outs[2] = {{k, bytes}, {v, bytes}};
+    if (outputs_clash(outs, 2, ins, 5)) return Q4_0_EALIAS;
+    const q4::ReadArgs a = {info.view, slots, n, k, v};
+    return map_hip(q4::launch_kv_read8(a, y_dtype == Q4_0_F16, (hipStream_t)stream));
 }
 
 int q4_0_attention_workspace_size(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype,
                                   int64_t n, int64_t table_stride, int64_t batch,
                                   int64_t window, int64_t sinks, size_t *bytes) {
     if (!bytes) return Q4_0_ENULL;
-    const int st =
-        check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks, false);
+    CacheInfo info;
+    const int st = check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks,
+                                   false, &info);
     if (st != Q4_0_OK) return st;
-    *bytes = q4::attention_workspace_bytes(
-        attention_args(cache, q_heads, n, table_stride, batch, window, sinks),
-        x_dtype == Q4_0_F16);
+    const q4::AttentionArgs a =
+        attention_args(info, q_heads, n, table_stride, batch, window, sinks);
+    *bytes = q4::attention_workspace_bytes(a, x_dtype == Q4_0_F16);
     return Q4_0_OK;
 }
 
 int q4_0_select_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, int64_t n,
                           int64_t table_stride, int64_t batch, int64_t window, int64_t sinks) {
-    const int st =
-        check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks, false);
+    CacheInfo info;
+    const int st = check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks,
+                                   false, &info);
     if (st != Q4_0_OK) return st;
     return q4::attention_tile_rows(
-        attention_args(cache, q_heads, n, table_stride, batch, window, sinks));
+        attention_args(info, q_heads, n, table_stride, batch, window, sinks));
 }
 
 int q4_0_attention(const q4_0_kv_cache *cache, const void *q, int64_t q_stride, int x_dtype,
@@ -777,33 +902,109 @@ int q4_0_attention(const q4_0_kv_cache *cache, const void *q, int64_t q_stride, 
                    const int32_t *kv_len, const int32_t *table, int64_t table_stride,
                    int64_t batch, int64_t window, int64_t sinks, float scale, void *workspace,
                    size_t workspace_bytes, void *stream) {
-    const int st =
-        check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks, true);
+    return attention(cache, q, q_stride, x_dtype, q_heads, y, n, q_start, kv_len, table,
+                     table_stride, batch, window, sinks, scale, workspace, workspace_bytes,
+                     stream);
+}
+
+int q4_0_attention8_workspace_size(const q4_0_kv_cache8 *cache, int64_t q_heads, int x_dtype,
+                                  int64_t n, int64_t table_stride, int64_t batch,
+                                  int64_t window, int64_t sinks, size_t *bytes) {
+    if (!bytes) return Q4_0_ENULL;
+    CacheInfo info;
+    const int st = check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks,
+                                   false, &info);
     if (st != Q4_0_OK) return st;
-    if (!(scale > 0.0f) || !isfinite(scale)) return Q4_0_EINVAL;
-    const int64_t qw = q_heads * cache->dim, el = elem_bytes(x_dtype);
-    if (q_stride < qw || q_stride > kMaxStride) return Q4_0_ESHAPE;
-    if (!q || !y || !q_start || !kv_len || !table) return Q4_0_ENULL;
-    if (!aligned(q, 16) || q_stride * el % 16 || !aligned(y, 16) || !aligned(q_start, 4) ||
-        !aligned(kv_len, 4) || !aligned(table, 4))
+    const q4::AttentionArgs a =
+        attention_args(info, q_heads, n, table_stride, batch, window, sinks);
+    *bytes = q4::attention8_workspace_bytes(a);
+    return Q4_0_OK;
+}
+
+int q4_0_select_attention8(const q4_0_kv_cache8 *cache, int64_t q_heads, int x_dtype, int64_t n,
+                          int64_t table_stride, int64_t batch, int64_t window, int64_t sinks) {
+    CacheInfo info;
+    const int st = check_attention(cache, q_heads, x_dtype, n, table_stride, batch, window, sinks,
+                                   false, &info);
+    if (st != Q4_0_OK) return st;
+    return q4::attention8_tile_rows(
+        attention_args(info, q_heads, n, table_stride, batch, window, sinks));
+}
+
+int q4_0_attention8(const q4_0_kv_cache8 *cache, const void *q, int64_t q_stride, int x_dtype,
+                   int64_t q_heads, void *y, int64_t n, const int32_t *q_start,
+                   const int32_t *kv_len, const int32_t *table, int64_t table_stride,
+                   int64_t batch, int64_t window, int64_t sinks, float scale, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    return attention(cache, q, q_stride, x_dtype, q_heads, y, n, q_start, kv_len, table,
+                     table_stride, batch, window, sinks, scale, workspace, workspace_bytes,
+                     stream);
+}
+
+int q4_0_embed(const void *packed, const int32_t *tokens, int64_t n, int64_t out, int64_t in,
+               float scale, float *h, const float *pre, float weight_offset, float eps, void *y,
+               int y_dtype, void *stream) {
+    const int st = check_shape(n, out, in);
+    if (st != Q4_0_OK) return st;
+    if (in > q4::kEmbedMaxDim) return Q4_0_EUNSUPPORTED;
+    if (!isfinite(scale) || (y && !valid_dtype(y_dtype))) return Q4_0_EINVAL;
+    if (!packed || !tokens || !h || (y && !pre)) return Q4_0_ENULL;
+    if (!aligned(packed, 16) || !aligned(tokens, 4) || !aligned(h, 16) ||
+        (y && (!aligned(y, 16) || !aligned(pre, 16))))
         return Q4_0_EALIGN;
-    const Span spans[7] = {{cache->k, cache_bytes(cache)},
-                           {cache->v, cache_bytes(cache)},
-                           {q, rows_bytes(n, q_stride, qw, el)},
+    const Span ins[3] = {{packed, q4_0_packed_bytes(out, in)},
+                         {tokens, (size_t)n * 4u},
+                         {y ? pre : nullptr, (size_t)in * 4u}};
+    const Span outs[2] = {{h, (size_t)(n * in) * 4u},
+                          {y, y ? (size_t)(n * in) * (size_t)elem_bytes(y_dtype) : 0}};
+    if (outputs_clash(outs, 2, ins, 3)) return Q4_0_EALIAS;
+    const q4::EmbedArgs a = {packed, tokens, n, out, in, scale, h, y ? pre : nullptr,
+                             weight_offset, eps, y};
+    return map_hip(q4::launch_embed(a, y && y_dtype == Q4_0_F16, (hipStream_t)stream));
+}
+
+int q4_0_verify_workspace_size(int64_t n, int64_t batch, int64_t vocab, int drafted,
+                               size_t *bytes) {
+    if (!bytes) return Q4_0_ENULL;
+    const int st = check_verify(n, batch, vocab, drafted != 0);
+    if (st != Q4_0_OK) return st;
+    *bytes = q4::verify_workspace_bytes(n, batch, vocab, drafted != 0);
+    return Q4_0_OK;
+}
+
+int q4_0_verify(const void *logits, int64_t stride, const void *drafted, int64_t drafted_stride,
+                int x_dtype, int64_t vocab, const int32_t *tokens, const int32_t *q_start,
+                int64_t n, int64_t batch, const float *temperature, const float *uniform,
+                int32_t *accepted, int32_t *next, void *workspace, size_t workspace_bytes,
+                void *stream) {
+    const int st = check_verify(n, batch, vocab, drafted != nullptr);
+    if (st != Q4_0_OK) return st;
+    if (!valid_dtype(x_dtype)) return Q4_0_EINVAL;
+    if (stride < vocab || stride > kMaxStride ||
+        (drafted && (drafted_stride < vocab || drafted_stride > kMaxStride)))
+        return Q4_0_ESHAPE;
+    if (!logits || !tokens || !q_start || !uniform || !accepted || !next) return Q4_0_ENULL;
+    const int64_t el = elem_bytes(x_dtype);
+    if (!aligned(logits, el) || !aligned(drafted, el) || !aligned(tokens, 4) ||
+        !aligned(q_start, 4) || !aligned(temperature, 4) || !aligned(uniform, 4) ||
+        !aligned(accepted, 4) || !aligned(next, 4))
+        return Q4_0_EALIGN;
+    const Span spans[8] = {{logits, rows_bytes(n, stride, vocab, el)},
+                           {drafted, drafted ? rows_bytes(n, drafted_stride, vocab, el) : 0},
+                           {tokens, (size_t)n * 4u},
                            {q_start, (size_t)(batch + 1) * 4u},
-                           {kv_len, (size_t)batch * 4u},
-                           {table, (size_t)(batch * table_stride) * 4u},
-                           {y, (size_t)(n * qw) * (size_t)el}};
-    if (outputs_clash(spans + 6, 1, spans, 6)) return Q4_0_EALIAS;
-    q4::AttentionArgs a = attention_args(cache, q_heads, n, table_stride, batch, window, sinks);
-    a.q = q, a.q_stride = q_stride, a.y = y;
-    a.q_start = q_start, a.kv_len = kv_len, a.table = table;
-    a.scale = scale;
-    const int f16 = x_dtype == Q4_0_F16;
-    const int wst = check_workspace(workspace, workspace_bytes,
-                                    q4::attention_workspace_bytes(a, f16), spans, 7);
+                           {temperature, (size_t)batch * 4u},
+                           {uniform, (size_t)n * 8u},
+                           {accepted, (size_t)batch * 4u},
+                           {next, (size_t)batch * 4u}};
+    if (outputs_clash(spans + 6, 2, spans, 6)) return Q4_0_EALIAS;
+    const int wst =
+        check_workspace(workspace, workspace_bytes,
+                        q4::verify_workspace_bytes(n, batch, vocab, drafted != nullptr), spans, 8);
     if (wst != Q4_0_OK) return wst;
-    return map_hip(q4::launch_attention(a, f16, workspace, (hipStream_t)stream));
+    const q4::VerifyArgs a = {logits, drafted, stride, drafted_stride, (int)vocab, (int)n,
+                              (int)batch, tokens, q_start, temperature, uniform, accepted, next};
+    return map_hip(q4::launch_verify(a, x_dtype == Q4_0_F16, workspace, (hipStream_t)stream));
 }
 
 int q4_0_residual_norm(const void *b, int b_dtype, int64_t b_stride, const float *post,

@@ -11,6 +11,8 @@
 // Bound by the bytes: 8191 tokens of 16 + 2 x 8 heads of 256, binary16, in
 // 56.5 us: 4.8 TB/s, where a copy of as many bytes reaches 4.8 to 5.4.  A single
 // token (32 + 2 x 8 heads of 128) takes 3.3 us, one launch.
+#include <float.h>
+
 #include "q4_0_device.h"
 #include "q4_0_internal.h"
 
@@ -47,7 +49,19 @@ __device__ __forceinline__ void turn(int position, float inv_freq, float *s, flo
     sincosf((float)r, s, c);
 }
 
-template <bool XF16, bool QF16, int LPH>
+// Four elements as codes of scale `s` (0: codes 0), one word.  The division is
+// rounded correctly, so a code is the nearest whole number of x / s in float32.
+__device__ __forceinline__ uint32_t codes_of(f4_t x, float s) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = s > 0.0f ? (int)rintf(x[i] / s) : 0;
+        w |= (uint32_t)(c & 255) << (8 * i);
+    }
+    return w;
+}
+
+template <bool XF16, bool QF16, bool CODES, int LPH>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int chunks) {
     constexpr int kGroups = kThreads / LPH;
     const int dim = a.cache.dim;
@@ -125,21 +139,45 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int chun
                 }
             }
         }
+        float step = 0.0f;
+        if (CODES && !is_q) {
+            // the row's largest magnitude, as bits: what is no number is larger
+            // than every number
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = x0[i], v = x1[i];
+                top = max(top, max(__builtin_bit_cast(uint32_t, u) & 0x7FFFFFFFu,
+                                   __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu));
+            }
+#pragma unroll
+            for (int m = 1; m < LPH; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+            step = __builtin_bit_cast(float, top) / 127.0f;
+            if (step < FLT_MIN) step = 0.0f;  // its codes would need smaller steps than float32's
+            if (top >= 0x7F800000u) step = NAN;
+        }
         if (!active) continue;
         if (is_q) {
             const int64_t o = (t * a.q_heads + hh) * dim;
             store4<QF16>(a.q_out, o + e0, x0);
             store4<QF16>(a.q_out, o + e1, x1);
+        } else if (CODES) {
+            if (!kept) continue;
+            const int64_t row = ((page * heads + hh) << shift) + off;
+            uint8_t *dst = (uint8_t *)(is_v ? a.cache.v : a.cache.k) + row * dim;
+            *(uint32_t *)(dst + e0) = codes_of(x0, step);
+            *(uint32_t *)(dst + e1) = codes_of(x1, step);
+            if (j == 0) (is_v ? a.cache.v_scale : a.cache.k_scale)[row] = step;
         } else if (kept) {
             const int64_t o = (((page * heads + hh) << shift) + off) * dim;
-            _Float16 *dst = is_v ? a.cache.v : a.cache.k;
+            void *dst = is_v ? a.cache.v : a.cache.k;
             store4<true>(dst, o + e0, x0);
             store4<true>(dst, o + e1, x1);
         }
     }
 }
 
-template <bool XF16, bool QF16, int LPH>
+template <bool XF16, bool QF16, bool CODES, int LPH>
 hipError_t launch(const AppendArgs &a, hipStream_t stream) {
     const int groups = kThreads / LPH;
     const int total = a.q_heads + 2 * a.cache.heads;
@@ -152,23 +190,82 @@ hipError_t launch(const AppendArgs &a, hipStream_t stream) {
     // and 6.5, 400 tokens 7.8 and 7.1; 64 + 2 x 8 of 64, 341 tokens 5.3 and 6.0,
     // 512 tokens 6.8 and 6.5.
     const int chunks = a.n * all <= 1024 ? all : 1;
-    hipLaunchKernelGGL((append_kernel<XF16, QF16, LPH>), dim3((uint32_t)(a.n * chunks)),
+    hipLaunchKernelGGL((append_kernel<XF16, QF16, CODES, LPH>), dim3((uint32_t)(a.n * chunks)),
                        dim3(kThreads), 0, stream, a, chunks);
     return hipGetLastError();
 }
 
-template <bool XF16, bool QF16> hipError_t by_dim(const AppendArgs &a, hipStream_t stream) {
-    if (a.cache.dim <= 64) return launch<XF16, QF16, 8>(a, stream);
-    if (a.cache.dim <= 128) return launch<XF16, QF16, 16>(a, stream);
-    if (a.cache.dim <= 256) return launch<XF16, QF16, 32>(a, stream);
-    return launch<XF16, QF16, 64>(a, stream);
+template <bool XF16, bool QF16, bool CODES>
+hipError_t by_dim(const AppendArgs &a, hipStream_t stream) {
+    if (a.cache.dim <= 64) return launch<XF16, QF16, CODES, 8>(a, stream);
+    if (a.cache.dim <= 128) return launch<XF16, QF16, CODES, 16>(a, stream);
+    if (a.cache.dim <= 256) return launch<XF16, QF16, CODES, 32>(a, stream);
+    return launch<XF16, QF16, CODES, 64>(a, stream);
+}
+
+template <bool CODES>
+hipError_t by_type(const AppendArgs &a, int x_f16, int q_f16, hipStream_t stream) {
+    if (x_f16)
+        return q_f16 ? by_dim<true, true, CODES>(a, stream) : by_dim<true, false, CODES>(a, stream);
+    return q_f16 ? by_dim<false, true, CODES>(a, stream) : by_dim<false, false, CODES>(a, stream);
+}
+
+// Rows of an 8-bit cache as numbers: a group of LPH lanes to a row, 8 codes to a
+// lane; K in one half of the grid's second dimension, V in the other.
+template <bool YF16, int LPH>
+__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
+    constexpr int kGroups = kThreads / LPH;
+    const int dim = a.cache.dim, heads = a.cache.heads, shift = a.cache.page_shift;
+    const bool is_v = blockIdx.y ? true : !a.k;
+    const int j = threadIdx.x % LPH;
+    if (8 * j >= dim) return;
+    const float *scales = is_v ? a.cache.v_scale : a.cache.k_scale;
+    const uint8_t *codes = (const uint8_t *)(is_v ? a.cache.v : a.cache.k) + 8 * j;
+    void *y = is_v ? a.v : a.k;
+    const int64_t total = a.n * heads, stride = (int64_t)gridDim.x * kGroups;
+    for (int64_t at = (int64_t)blockIdx.x * kGroups + threadIdx.x / LPH; at < total; at += stride) {
+        const int64_t slot = a.slots[at / heads];
+        f4_t x0 = {0.0f, 0.0f, 0.0f, 0.0f}, x1 = x0;
+        if (slot >= 0 && slot < (a.cache.pages << shift)) {
+            const int64_t row = (((slot >> shift) * heads + at % heads) << shift) +
+                                (slot & ((INT64_C(1) << shift) - 1));
+            const float step = scales[row];
+            const u2_t w = load_u2(codes + row * dim);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x0[i] = step * (float)(int8_t)(w[0] >> (8 * i));
+                x1[i] = step * (float)(int8_t)(w[1] >> (8 * i));
+            }
+        }
+        store4<YF16>(y, at * dim + 8 * j, x0);
+        store4<YF16>(y, at * dim + 8 * j + 4, x1);
+    }
+}
+
+template <bool YF16, int LPH> hipError_t read(const ReadArgs &a, hipStream_t stream) {
+    const int64_t total = a.n * a.cache.heads;
+    hipLaunchKernelGGL((read_kernel<YF16, LPH>),
+                       dim3((uint32_t)grid_for(total, kThreads / LPH), a.k && a.v ? 2u : 1u),
+                       dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool YF16> hipError_t read_by_dim(const ReadArgs &a, hipStream_t stream) {
+    if (a.cache.dim <= 64) return read<YF16, 8>(a, stream);
+    if (a.cache.dim <= 128) return read<YF16, 16>(a, stream);
+    if (a.cache.dim <= 256) return read<YF16, 32>(a, stream);
+    return read<YF16, 64>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const AppendArgs &a, int x_f16, int q_f16, hipStream_t stream) {
-    if (x_f16) return q_f16 ? by_dim<true, true>(a, stream) : by_dim<true, false>(a, stream);
-    return q_f16 ? by_dim<false, true>(a, stream) : by_dim<false, false>(a, stream);
+    return a.cache.k_scale ? by_type<true>(a, x_f16, q_f16, stream)
+                           : by_type<false>(a, x_f16, q_f16, stream);
+}
+
+hipError_t launch_kv_read8(const ReadArgs &a, int y_f16, hipStream_t stream) {
+    return y_f16 ? read_by_dim<true>(a, stream) : read_by_dim<false>(a, stream);
 }
 
 }  // namespace q4

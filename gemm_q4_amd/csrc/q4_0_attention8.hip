@@ -1,0 +1,1047 @@
+// Attention of a ragged batch over a paged cache of 8-bit codes.
+//
+//     y = sum_j softmax_j(scale q . s_j c_j) t_j e_j
+//
+// with codes c, e of K and V (integers from -128 to 127) and one float32 scale
+// s, t to a row of either.  The codes are binary16 numbers exactly, so both
+// products run on the binary16 matrix cores without a rounding of K or V; a
+// key's scale multiplies its score, and a value's scale its weight, in float32.
+//
+// Codes to binary16: with the sign bit flipped a code c is the byte c + 128, which
+// under the exponent byte 0x64 reads as 1024 + 128 + c; one packed subtraction
+// leaves c.  Five instructions for four codes.
+//
+// A value's weight is p t with p = exp(x - m) in float32, t brought to the
+// largest scale met so far (a power of two, so without rounding) before it is
+// multiplied; that running exponent is lifted, and what is accumulated rescaled,
+// like the maximum of the softmax.  The scales of keys that no row of a tile sees
+// are taken as 0 and their codes are finite whatever they are, so what a page
+// holds past its conversation's end never meets the arithmetic.
+//
+// Scores keep their own units: a weight is exp2((x - m) c), the difference first,
+// so that scores of any size lose nothing.
+#include "q4_0_attention.h"
+#include "q4_0_dma.h"
+
+namespace q4 {
+
+namespace {
+
+typedef int i2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i2_t *lds_i2_t;
+
+// Four codes as two pairs of binary16.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t &h0, uint32_t &h1) {
+    const uint32_t top = 0x64646464u, b = w ^ 0x80808080u;
+    const h2_t off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+    h0 = as_u32(as_h2(__builtin_amdgcn_perm(top, b, 0x04010400u)) + off);
+    h1 = as_u32(as_h2(__builtin_amdgcn_perm(top, b, 0x04030402u)) + off);
+}
+__device__ __forceinline__ h8_t codes8(uint32_t w0, uint32_t w1) {
+    uint32_t h[4];
+    codes4(w0, h[0], h[1]);
+    codes4(w1, h[2], h[3]);
+    return pack_h8(h);
+}
+
+// Direct copy of 4 bytes per lane into LDS: lane i's at lds + 4 i.
+__device__ __forceinline__ void dma4(const void *src, uint8_t *lds) {
+    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+                 :
+                 : "v"(src), "s"(base)
+                 : "memory", "m0");
+}
+
+static __device__ const uint32_t kNanWord = 0x7FC00000u;
+
+// x of the four lanes l, l + 16, l + 32, l + 48 joined.
+template <typename F> __device__ __forceinline__ float quads(float x, F f) {
+    uint32_t u = __builtin_bit_cast(uint32_t, x);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    x = f(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+    u = __builtin_bit_cast(uint32_t, x);
+    r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return f(__builtin_bit_cast(float, (uint32_t)r[0]),
+             __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float quads_max(float x) {
+    return quads(x, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float quads_sum(float x) {
+    return quads(x, [](float a, float b) { return a + b; });
+}
+
+// The exponent that brings a scale into [1/2, 1); far below any for 0 and for
+// what is no number.
+constexpr int kNoExponent = -1000;
+__device__ __forceinline__ int exponent(float t) {
+    const float a = fabsf(t);
+    return a > 0.0f && a <= FLT_MAX ? __builtin_amdgcn_frexp_expf(a) : kNoExponent;
+}
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) x = max(x, __shfl_xor(x, i));
+    return uniform(x);
+}
+// A value's scale relative to 2^top; one that is infinite is no number either.
+__device__ __forceinline__ float relative(float t, int top, int shift) {
+    return fabsf(t) <= FLT_MAX ? __builtin_amdgcn_ldexpf(t, shift - top) : NAN;
+}
+
+// The cache as a tile's loads see it: head hk of the pages of conversation s.
+struct Source {
+    const uint8_t *k, *v;  // codes of this head on page 0
+    const float *ks, *vs;  // scales, likewise
+    const int32_t *table;
+    int64_t page_rows;  // rows of all heads of a page
+    int pages, table_stride, shift;
+    __device__ __forceinline__ Source(const AttentionArgs &a, int s, int hk)
+        : table(a.table + (int64_t)s * a.table_stride),
+          page_rows((int64_t)a.cache.heads << a.cache.page_shift), pages((int)a.cache.pages),
+          table_stride(a.table_stride), shift(a.cache.page_shift) {
+        const int64_t row = (int64_t)hk << shift;
+        k = (const uint8_t *)a.cache.k + row * a.cache.dim;
+        v = (const uint8_t *)a.cache.v + row * a.cache.dim;
+        ks = a.cache.k_scale + row;
+        vs = a.cache.v_scale + row;
+    }
+    // The page of key `key` (of the lane's own choice), -1 if it has none.
+    __device__ __forceinline__ int look(int key) const {
+        const int slot = key >> shift;
+        const int page = slot < table_stride ? table[slot] : -1;
+        return page < pages ? max(page, -1) : -1;
+    }
+    // Row of `key` on `page`.  A key without a page is given a row of page 0,
+    // whose codes do no harm: its scales say what it is.
+    __device__ __forceinline__ int64_t row(int page, int key) const {
+        return max(page, 0) * page_rows + (key & ((1 << shift) - 1));
+    }
+    // Where the scale of `key` is read: 0 for one that no row of the tile sees;
+    // without a page K's is NaN.
+    template <int KT>
+    __device__ __forceinline__ const void *scale(const Reach<KT> &r, int page, int key,
+                                                 bool is_v) const {
+        const void *p = (is_v ? vs : ks) + row(page, key);
+        if (page < 0) p = is_v ? (const void *)&kZeroPiece : (const void *)&kNanWord;
+        return r.any(key) ? p : (const void *)&kZeroPiece;
+    }
+};
+
+// ---- few rows: every wave streams its own keys ------------------------------
+// A wave works on tiles of 64 keys and one or two blocks of 16 rows, with
+// v_mfma_f32_16x16x32_f16: S^T = K Q^T leaves row l % 16's scores of the keys
+// 16 b + 4 (l / 16) + 0..3 in lane l, and the weights of two such blocks are as they
+// lie the B operand of O^T = V^T P^T, whose A operand (eight keys of one column
+// to a lane) the transposing 8-bit LDS read delivers from row-major V.
+constexpr int kStepRows = 32, kStepKeys = 64;
+
+// Codes in LDS are rows of DIM bytes, their 16-byte pieces XOR-swizzled: sixteen
+// neighbouring keys at one piece, and keys 8 h + 0..7 with 16 + 8 h + 0..7 at one
+// piece, fall on distinct banks.
+template <int DIM> __device__ __forceinline__ int swz8(int key) {
+    constexpr int kLow = DIM == 256 ? 0 : DIM == 128 ? 1 : 2;  // rows of 256 bytes, as a power
+    return ((key >> kLow) & ((1 << (3 - kLow)) - 1)) |
+           ((((key >> 3) ^ (key >> 4)) & 1) << (3 - kLow));
+}
+
+// Copies of a tile into a wave's share of LDS: codes of K, of V, then scales of
+// K, of V.  Always as many of them, whatever the keys are.
+template <int DIM> struct StepFiller : Source {
+    static constexpr int kCopies = DIM / 64;  // of 16 rows, 1 KB each
+    static constexpr int kAll = kStepKeys / 16 * kCopies + 1;  // a tile's, of K or of V
+    static constexpr int kCodes = kStepKeys * DIM;
+    uint32_t off[2][kCopies];
+    __device__ __forceinline__ StepFiller(const AttentionArgs &a, int s, int hk)
+        : Source(a, s, hk) {
+        const int lane = threadIdx.x % 64;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j) {
+                const int row = j * (1024 / DIM) + lane / (DIM / 16);
+                off[g][j] = row * DIM + ((lane % (DIM / 16)) ^ swz8<DIM>(16 * g + row)) * 16;
+            }
+    }
+    __device__ __forceinline__ void fill(const Reach<kStepKeys> &r, const int (&page)[4], int key,
+                                         uint8_t *lds, bool is_v) const {
+        const int lane = threadIdx.x % 64;
+        uint8_t *dst = lds + (is_v ? kCodes : 0);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint8_t *src = (is_v ? v : k) + row(page[g], key + 16 * g) * DIM;
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j)
+                dma16_once_at(src, off[g & 1][j], dst + g * 16 * DIM + j * 1024);
+        }
+        // the lane's own page, chosen among copies (an identity move): the pages
+        // themselves stay in scalar registers, as the copies' bases have to
+        const auto copy = [](int x) { return __builtin_amdgcn_mov_dpp(x, 0xE4, 0xF, 0xF, true); };
+        const int p0 = copy(page[0]), p1 = copy(page[1]), p2 = copy(page[2]), p3 = copy(page[3]);
+        const int mine = lane < 32 ? (lane < 16 ? p0 : p1) : (lane < 48 ? p2 : p3);
+        dma4(scale(r, mine, key + lane, is_v),
+             lds + 2 * kCodes + (is_v ? kStepKeys * 4 : 0));
+    }
+};
+
+// A block of 16 rows: queries, running maximum (of scores without `c`), sum (this
+// lane's keys) and unnormalised result.  Weights are held in two binary16 parts,
+// as 2^kShift of the largest.
+template <int DIM, bool F32> struct Block {
+    static constexpr int kParts = F32 ? 2 : 1;
+    static constexpr float kLag = 1.0f;
+    static constexpr int kShift = 14;
+    h8_t q[kParts][DIM / 32];
+    f4_t o[DIM / 16];
+    float m, l, c;
+    int p, lo;
+
+    struct Raw {
+        u4_t x[kParts * DIM / 32];
+    };
+    // Row r (of the conversation's `rows`); rows past the end repeat the last.
+    // Lane l holds elements 64 j + 16 (l / 16) + 0..15 of row l % 16.
+    __device__ __forceinline__ void request(Raw &raw, const AttentionArgs &a, const Place &pl,
+                                            int group, int hk, int r, int position0) {
+        const int g = threadIdx.x % 64 / 16;
+        const int rr = min(r, pl.rows - 1);
+        const int token = rr / group;
+        p = position(a, position0, token);
+        lo = a.window && p >= a.window ? p - a.window + 1 : 0;
+        c = finite(a.scale * kLog2e);
+        const int64_t at = (int64_t)(pl.first + token) * a.q_stride +
+                           (int64_t)(hk * group + rr % group) * DIM + 16 * g;
+        const u4_t *src = (const u4_t *)((const uint8_t *)a.q + at * (F32 ? 4 : 2));
+#pragma unroll
+        for (int j = 0; j < DIM / 64; ++j)
+#pragma unroll
+            for (int x = 0; x < 2 * kParts; ++x)
+                raw.x[j * 2 * kParts + x] = src[j * (F32 ? 16 : 8) + x];
+    }
+    __device__ __forceinline__ void clear() {
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DIM / 16; ++d) o[d] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __device__ __forceinline__ void take(const Raw &raw) {
+        if (!F32) {
+#pragma unroll
+            for (int d = 0; d < DIM / 32; ++d) q[0][d] = __builtin_bit_cast(h8_t, raw.x[d]);
+            return;
+        }
+        // the row's largest element brought into [1/2, 1), so that its parts are
+        // neither infinite nor faint whatever q's magnitude
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kParts * DIM / 8; ++i) {
+            const uint32_t bits = raw.x[i / 4][i % 4];
+            top = fmaxf(top, fabsf(__builtin_bit_cast(float, bits)));
+        }
+        const int e = __builtin_amdgcn_frexp_expf(quads_max(top));
+        c = finite(__builtin_amdgcn_ldexpf(c, e));
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = raw.x[(d * kParts + i / 4) % (kParts * DIM / 32)][i % 4];
+                const float v = __builtin_amdgcn_ldexpf(__builtin_bit_cast(float, bits), -e);
+                const _Float16 hi = (_Float16)v;
+                q[0][d][i] = hi;
+                q[kParts - 1][d][i] = (_Float16)(v - (float)hi);
+            }
+    }
+    __device__ __forceinline__ bool sees(int key, int sinks) const {
+        return key <= p && (key >= lo || key < sinks);
+    }
+    __device__ __forceinline__ void rescale(float f) {
+#pragma unroll
+        for (int d = 0; d < DIM / 16; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][i] *= f;
+    }
+    // Scores of 64 keys to exp(x - m), the maximum brought along; a set bit of
+    // `hidden` is a score whose key the row does not see.
+    __device__ __forceinline__ void soften(f4_t (&s)[4]) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
+        top = quads_max(top);
+        if (__any((top - m) * c > kLag)) {
+            const float mn = fmaxf(m, top);
+            const float f = mn == -INFINITY ? 1.0f : factor_of((m - mn) * c);
+            m = mn;
+            l *= f;
+            rescale(f);
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[b][i] = __builtin_amdgcn_exp2f((s[b][i] - base) * c);
+                l += s[b][i];
+            }
+    }
+};
+
+template <int DIM, bool F32, int NR>
+__device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFiller<DIM> &f,
+                                          const Reach<kStepKeys> &r, int t, int t1, int stride,
+                                          int top_lo, uint8_t *lds, int (&look)[4], int &top) {
+    using B = Block<DIM, F32>;
+    constexpr int kAll = StepFiller<DIM>::kAll, kCodes = StepFiller<DIM>::kCodes;
+    const int lane = threadIdx.x % 64, g = lane / 16;
+    const uint8_t *vbuf = lds + kCodes;
+    const float *ksc = (const float *)(lds + 2 * kCodes);
+    float *vsc = (float *)(lds + 2 * kCodes) + kStepKeys;
+    // lane i of 16 names the address of half a piece of the (i / 2)-th of its
+    // eight keys and receives column i of all eight
+    const int i2 = lane % 16 / 2;
+    const int vkey = (i2 < 4 ? 4 * g + i2 : 12 + 4 * g + i2);
+    const uint8_t *vrow = vbuf + vkey * DIM + 8 * (lane % 2);
+    int i = 0;  // the tile's lane in look
+    for (; t < t1; t += stride) {
+        const int k0 = r.key(t), next = r.key(t + stride);
+        const bool more = t + stride < t1, masked = !r.all(k0, kStepKeys, top_lo);
+        f4_t s[NR][4];
+        // outstanding: K, then V
+        Q4_WAIT_VMCNT(kAll);
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) s[n][b] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            const int key = 16 * b + lane % 16;
+#pragma unroll
+            for (int j = 0; j < DIM / 64; ++j) {
+                const u4_t x =
+                    *(const u4_t *)(lds + key * DIM + (((4 * j + g) ^ swz8<DIM>(key)) * 16));
+                const h8_t a0 = codes8(x[0], x[1]), a1 = codes8(x[2], x[3]);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int y = 0; y < B::kParts; ++y) {
+                        s[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, w[n].q[y][2 * j],
+                                                                         s[n][b], 0, 0, 0);
+                        s[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            a1, w[n].q[y][2 * j + 1], s[n][b], 0, 0, 0);
+                    }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const f4_t x = *(const f4_t *)(ksc + 16 * b + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float none = x[e] * 0.0f;  // an infinite scale is no number either
+#pragma unroll
+                for (int n = 0; n < NR; ++n) s[n][b][e] = fmaf(s[n][b][e], x[e], none);
+            }
+        }
+        uint32_t hidden[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) hidden[n] = 0;
+        if (masked) {
+            asm volatile("; masked tile");  // a branch, not a select in every tile
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!w[n].sees(k0 + 16 * b + 4 * g + e, r.sinks)) {
+                            s[n][b][e] = -INFINITY;
+                            hidden[n] |= 1u << (4 * b + e);
+                        }
+        }
+        Q4_WAIT_LGKM0();
+        asm volatile("" ::: "memory");
+        int page[4];
+        if (more) {
+            i = (i + 1) % 64;
+            if (__builtin_expect(i == 0, 0)) {
+                const int mine = r.key(min(t + stride + lane * stride, t1 - 1));
+#pragma unroll
+                for (int x = 0; x < 4; ++x) look[x] = f.look(mine + 16 * x);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) page[x] = __builtin_amdgcn_readlane(look[x], i);
+            f.fill(r, page, next, lds, false);
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) w[n].soften(s[n]);
+        // outstanding: V, then the next K
+        if (more)
+            Q4_WAIT_VMCNT(kAll);
+        else
+            Q4_WAIT_VMCNT(0);
+        asm volatile("" ::: "memory");
+        // V's scales against the largest so far
+        {
+            const float t4 = vsc[lane];
+            const int e = exponent(t4);
+            if (__any(e > top)) {
+                const int up = max(wave_max(e), top);
+                const float fall = __builtin_amdgcn_ldexpf(1.0f, top - up);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) w[n].rescale(fall);
+                top = up;
+            }
+            vsc[lane] = relative(t4, top, B::kShift);
+        }
+        Q4_WAIT_LGKM0();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const f4_t x = *(const f4_t *)(vsc + 16 * b + 4 * g);
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][b][e] *= x[e];
+        }
+        if (masked) {
+            asm volatile("; masked tile");
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (hidden[n] >> (4 * b + e) & 1) s[n][b][e] = 0.0f;
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            h8_t p[NR][2];
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = s[n][2 * b + e / 4][e % 4];
+                    const _Float16 hi = (_Float16)y;
+                    p[n][0][e] = hi;
+                    p[n][1][e] = (_Float16)(y - (float)hi);
+                }
+#pragma unroll
+            for (int d = 0; d < DIM / 16; ++d) {
+                const i2_t x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                    (lds_i2_t)(vrow + b * 32 * DIM + ((d ^ swz8<DIM>(vkey)) * 16)));
+                const h8_t a = codes8((uint32_t)x[0], (uint32_t)x[1]);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        w[n].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, p[n][y], w[n].o[d],
+                                                                           0, 0, 0);
+            }
+        }
+        Q4_WAIT_LGKM0();
+        asm volatile("" ::: "memory");
+        if (more) f.fill(r, page, next, lds, true);
+    }
+}
+
+// One tile of up to 16 NR rows by a workgroup of W waves.
+template <int DIM, bool F32, int W, int NR>
+__device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl, const Place &at,
+                                          int hk, int split, int row0, int row1, uint8_t *lds,
+                                          float (*ml)[W][kStepRows]) {
+    constexpr int kPitch = DIM + 4, kShare = 32 * kPitch * 4;
+    static_assert(2 * StepFiller<DIM>::kCodes + 2 * kStepKeys * 4 <= kShare && kShare % 256 == 0,
+                  "a wave's tile, later its rows");
+    const int position0 = at.kv - at.rows / pl.group;
+    const int p0 = position(a, position0, row0 / pl.group);
+    const int p1 = position(a, position0, (row1 - 1) / pl.group);
+    const Reach<kStepKeys> r(a, p0, p1);
+    const int top_lo = a.window && p1 >= a.window ? p1 - a.window + 1 : 0;
+    const int per = max((r.tiles + pl.splits - 1) / pl.splits, pl.least);
+    const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
+    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), g = lane / 16;
+    uint8_t *mine = lds + wave * kShare;
+    const StepFiller<DIM> f(a, at.s, hk);
+    Block<DIM, F32> w[NR];
+    const int t = t0 + wave;
+    int look[4] = {-1, -1, -1, -1};
+    {
+        typename Block<DIM, F32>::Raw raw[NR];
+        if (t < t1) {
+            const int k = r.key(min(t + lane * W, t1 - 1));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) look[x] = f.look(k + 16 * x);
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+            w[n].request(raw[n], a, at, pl.group, hk, row0 + 16 * n + lane % 16, position0);
+        if (t < t1) {
+            int page[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) page[x] = __builtin_amdgcn_readlane(look[x], 0);
+            f.fill(r, page, r.key(t), mine, false);
+            f.fill(r, page, r.key(t), mine, true);
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) w[n].take(raw[n]);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) w[n].clear();
+    }
+    int top = kNoExponent;
+    step_loop<DIM, F32, NR>(w, f, r, t, t1, W, top_lo, mine, look, top);
+    // join the waves
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        w[n].l = quads_sum(w[n].l);
+        w[n].m = w[n].m * w[n].c;  // in powers of two
+        if (g == 0) {
+            ml[0][wave][16 * n + lane] = w[n].m;
+            ml[1][wave][16 * n + lane] = w[n].l;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int rr = 16 * n + lane % 16;
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < W; ++i) m = fmaxf(m, ml[0][i][rr]);
+        const float fs = factor_of(w[n].m - (m == -INFINITY ? 0.0f : m));
+        if (rr < row1 - row0) {
+            float *row = (float *)mine + rr * kPitch + 4 * g;
+#pragma unroll
+            for (int d = 0; d < DIM / 16; ++d) {
+                f4_t v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = __builtin_amdgcn_ldexpf(w[n].o[d][e], top - w[n].kShift) * fs;
+                *(f4_t *)(row + 16 * d) = v;
+            }
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < (row1 - row0) * (DIM / 4); e += 64 * W) {
+        const int rr = e / (DIM / 4), d = e % (DIM / 4) * 4;
+        f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) m = fmaxf(m, ml[0][i][rr]);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const f4_t v = *(const f4_t *)((const float *)(lds + i * kShare) + rr * kPitch + d);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[x] += v[x];
+            l += ml[1][i][rr] * factor_of(ml[0][i][rr] - (m == -INFINITY ? 0.0f : m));
+        }
+        const int token = (row0 + rr) / pl.group;
+        const int64_t out = (int64_t)(at.first + token) * a.q_heads + hk * pl.group +
+                            (row0 + rr) % pl.group;
+        if (pl.splits > 1 && d == 0) put_ml(a, pl, split, out, m, l);
+        if (pl.splits > 1 && t0 >= t1) continue;
+        put4<F32>(a, pl, split, out, DIM, d, o, l, position0 + token >= 0);
+    }
+}
+
+template <int DIM, bool F32, int W>
+__global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(AttentionArgs a, Plan pl,
+                                                                         int base) {
+    __shared__ __align__(1024) uint8_t lds[W * 32 * (DIM + 4) * 4];
+    __shared__ float ml[2][W][kStepRows];
+    const int hk = blockIdx.x, split = blockIdx.y;
+    const Place at = find_tile<kStepRows>(a, pl.group, base + blockIdx.z);
+    const int row0 = at.tile * kStepRows;
+    if (row0 < 0 || row0 >= at.rows) return;
+    const int row1 = min(row0 + kStepRows, at.rows);
+    if (row1 - row0 <= 16)
+        step_tile<DIM, F32, W, 1>(a, pl, at, hk, split, row0, row1, lds, ml);
+    else
+        step_tile<DIM, F32, W, 2>(a, pl, at, hk, split, row0, row1, lds, ml);
+}
+
+// ---- many rows: waves of 32 rows share each key tile ------------------------
+// RW waves of 32 rows work on one key tile; KW such groups take every KW-th tile
+// each and are joined through LDS at the end.  A tile is brought to binary16 once,
+// on its way into LDS: its codes are loaded to registers a tile ahead, written to
+// the other of two stages while this one is worked on, and read there by all RW
+// waves.  Both products are v_mfma_f32_32x32x16_f16 on transposed scores; weights of
+// binary16 rows are rounded once, of float32 rows held in two parts.
+template <int DIM, int RW, int KW> struct Pass {
+    static constexpr int KT = 16 * RW;
+    static constexpr int kTile = KT * DIM * 2;
+    static constexpr int kPitch = DIM + 4, kShare = 32 * kPitch * 4;
+    static constexpr int kStages = KW * 4 * kTile;
+    static constexpr int kLds = KW > 1 && RW * KW * kShare > kStages ? RW * KW * kShare : kStages;
+    static constexpr int kThreads = 64 * RW * KW;
+    static constexpr int kWavesPerSimd = DIM > 128 ? 1 : 2;
+};
+
+// Scales of a stage: of K, of V (against 2^top), and top.
+template <int KT> struct Scales {
+    float k[KT], v[KT];
+    int top;
+};
+
+// One wave's 32 rows.
+template <int DIM, bool F32> struct Rows {
+    static constexpr int kParts = F32 ? 2 : 1;
+    // weights as 2^kShift of the largest, which may lag behind by kLag (powers of two)
+    static constexpr float kLag = F32 ? 1.0f : 8.0f;
+    static constexpr int kShift = F32 ? 14 : 7;
+    h8_t q[kParts][DIM / 16];
+    f16x_t o[DIM / 32];
+    float m, l, c;
+    int p, lo;
+
+    struct Raw {
+        u4_t x[kParts * DIM / 16];
+    };
+    __device__ __forceinline__ void request(Raw &raw, const AttentionArgs &a, const Place &pl,
+                                            int group, int hk, int r, int position0) {
+        const int half = threadIdx.x % 64 / 32;
+        const int rr = min(r, pl.rows - 1);
+        const int token = rr / group;
+        p = position(a, position0, token);
+        lo = a.window && p >= a.window ? p - a.window + 1 : 0;
+        c = finite(a.scale * kLog2e);
+        const int64_t at = (int64_t)(pl.first + token) * a.q_stride +
+                           (int64_t)(hk * group + rr % group) * DIM + 8 * half;
+        const u4_t *src = (const u4_t *)((const uint8_t *)a.q + at * (F32 ? 4 : 2));
+#pragma unroll
+        for (int s = 0; s < DIM / 16; ++s)
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) raw.x[s * kParts + x] = src[s * (F32 ? 4 : 2) + x];
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+    }
+    __device__ __forceinline__ void take(const Raw &raw) {
+        int e = 0;
+        if (F32) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kParts * DIM / 4; ++i) {
+                const uint32_t bits = raw.x[i / 4][i % 4];
+                top = fmaxf(top, fabsf(__builtin_bit_cast(float, bits)));
+            }
+            e = __builtin_amdgcn_frexp_expf(halves_max(top));
+            c = finite(__builtin_amdgcn_ldexpf(c, e));
+        }
+#pragma unroll
+        for (int s = 0; s < DIM / 16; ++s) {
+            if (!F32) {
+                q[0][s] = __builtin_bit_cast(h8_t, raw.x[s]);
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = raw.x[s * kParts + (i / 4) % kParts][i % 4];
+                const float v = __builtin_amdgcn_ldexpf(__builtin_bit_cast(float, bits), -e);
+                const _Float16 hi = (_Float16)v;
+                q[0][s][i] = hi;
+                q[kParts - 1][s][i] = (_Float16)(v - (float)hi);
+            }
+        }
+    }
+    __device__ __forceinline__ bool sees(int key, int sinks) const {
+        return key <= p && (key >= lo || key < sinks);
+    }
+    __device__ __forceinline__ void rescale(float f) {
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] *= f;
+    }
+    // One tile: binary16 codes of K and V in LDS, and its scales.
+    template <int KT>
+    __device__ __forceinline__ void step(const uint8_t *kbuf, const uint8_t *vbuf,
+                                         const Scales<KT> &sc, int k0, bool masked, int sinks) {
+        const int lane = threadIdx.x % 64, half = lane / 32;
+        f16x_t s[KT / 32];
+#pragma unroll
+        for (int t = 0; t < KT / 32; ++t) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
+            const int key = lane % 32;
+            const uint8_t *row = kbuf + (t * 32 + key) * DIM * 2;
+#pragma unroll
+            for (int d = 0; d < DIM / 16; ++d) {
+                const h8_t k = *(const h8_t *)(row + (((2 * d + half) ^ swz<DIM>(key)) * 16));
+#pragma unroll
+                for (int x = 0; x < kParts; ++x)
+                    s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[x][d], s[t], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const f4_t x = *(const f4_t *)(sc.k + t * 32 + 2 * i + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][i + e] *= x[e];
+            }
+        uint32_t hidden = 0;
+        if (masked) {
+            asm volatile("; masked tile");
+#pragma unroll
+            for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!sees(k0 + t * 32 + 8 * (i / 4) + 4 * half + i % 4, sinks)) {
+                        s[t][i] = -INFINITY;
+                        hidden |= 1u << (16 * t + i);
+                    }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+        top = halves_max(top);
+        if (__any((top - m) * c > kLag)) {
+            const float mn = fmaxf(m, top);
+            const float f = mn == -INFINITY ? 1.0f : factor_of((m - mn) * c);
+            m = mn;
+            l *= f;
+            rescale(f);
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        h8_t w[KT / 16][kParts];
+#pragma unroll
+        for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const f4_t x = *(const f4_t *)(sc.v + t * 32 + 2 * i + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y = __builtin_amdgcn_exp2f((s[t][i + e] - base) * c);
+                    l += y;
+                    s[t][i + e] = y * x[e];
+                }
+            }
+        if (masked) {
+            asm volatile("; masked tile");
+#pragma unroll
+            for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (hidden >> (16 * t + i) & 1) s[t][i] = 0.0f;
+        }
+#pragma unroll
+        for (int b = 0; b < KT / 16; ++b)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = s[b / 2][8 * (b % 2) + i];
+                const _Float16 hi = (_Float16)y;
+                w[b][0][i] = hi;
+                if (F32) w[b][kParts - 1][i] = (_Float16)(y - (float)hi);
+            }
+#pragma unroll
+        for (int b = 0; b < KT / 16; ++b) {
+            const int key = 16 * b + 4 * half + lane % 16 / 4;
+            const int piece = 2 * (lane / 16 % 2) + lane % 4 / 2;
+            const uint8_t *r0 = vbuf + key * DIM * 2 + 8 * (lane % 2);
+            const uint8_t *r1 = r0 + 8 * DIM * 2;
+#pragma unroll
+            for (int d = 0; d < DIM / 32; ++d) {
+                const s4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s4_t)(r0 + ((4 * d + piece) ^ swz<DIM>(key)) * 16));
+                const s4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s4_t)(r1 + ((4 * d + piece) ^ swz<DIM>(key + 8)) * 16));
+                const h8_t v = __builtin_bit_cast(
+                    h8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int x = 0; x < kParts; ++x)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[b][x], o[d], 0, 0, 0);
+            }
+        }
+    }
+};
+
+template <int DIM, bool F32, int RW, int KW>
+__global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
+                             (Pass<DIM, RW, KW>::kWavesPerSimd)) void pass_kernel(AttentionArgs a,
+                                                                                  Plan pl,
+                                                                                  int base) {
+    using P = Pass<DIM, RW, KW>;
+    using W = Rows<DIM, F32>;
+    constexpr int KT = P::KT, kTile = P::kTile, R = 32 * RW, kLoads = DIM / 64;
+    __shared__ __align__(1024) uint8_t lds[P::kLds];
+    __shared__ __align__(16) Scales<KT> scales[2][KW];
+    __shared__ float ml[2][KW][R];
+    const int hk = blockIdx.x, split = blockIdx.y;
+    Place at = find_tile<R>(a, pl.group, base + blockIdx.z);
+    const int count = (at.rows + R - 1) / R;
+    if (at.tile < 0 || at.tile >= count) return;
+    at.tile = count - 1 - at.tile;  // the tiles with the most keys first
+    const int position0 = at.kv - at.rows / pl.group;
+    const int row0 = at.tile * R, row1 = min(row0 + R, at.rows);
+    const int p0 = position(a, position0, row0 / pl.group);
+    const int p1 = position(a, position0, (row1 - 1) / pl.group);
+    const Reach<KT> r(a, p0, p1);
+    const int top_lo = a.window && p1 >= a.window ? p1 - a.window + 1 : 0;
+    const int per = max((r.tiles + pl.splits - 1) / pl.splits, pl.least);
+    const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
+    const int lane = threadIdx.x % 64, half = lane / 32, wave = uniform(threadIdx.x / 64);
+    const int rw = wave % RW, kw = wave / RW;
+    const int mine = rw * 32 + lane % 32, row = row0 + mine;
+    W w;
+    {
+        typename W::Raw raw;
+        w.request(raw, a, at, pl.group, hk, row, position0);
+        w.take(raw);
+    }
+    int top = kNoExponent;  // of the values in o
+    const int tiles = max((t1 - t0 - kw + KW - 1) / KW, 0);  // this group's
+    const int rounds = uniform((t1 - t0 + KW - 1) / KW);     // the first group's
+    const Source f(a, at.s, hk);
+    uint8_t *stages = lds + kw * 4 * kTile;
+    const auto key_of = [&](int i) { return r.key(t0 + kw + i * KW); };
+    // a tile's loads: this wave's 16 rows of K and V, and the scales of V (first
+    // wave) or K (second), a key to a lane
+    u4_t kx[kLoads], vx[kLoads];
+    float sx = 0.0f;
+    const auto look = [&](int i) { return f.look(key_of(min(i, tiles - 1)) + lane % KT); };
+    const auto load = [&](int i, int pages) {
+        const int k0 = key_of(i), k = k0 + 16 * rw;
+        const int64_t at16 = f.row(__builtin_amdgcn_readlane(pages, 16 * rw), k) * DIM + lane * 16;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            kx[j] = *(const u4_t *)(f.k + at16 + j * 1024);
+            vx[j] = *(const u4_t *)(f.v + at16 + j * 1024);
+        }
+        if (rw < 2) sx = *(const float *)f.scale(r, pages, k0 + lane % KT, rw == 0);
+    };
+    int lifted = kNoExponent;  // the running exponent, of the wave that stages V's scales
+    const auto stage = [&](int i) {
+        uint8_t *dst = stages + (i & 1) * 2 * kTile;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int key = 16 * rw + j * (1024 / DIM) + lane / (DIM / 16);
+            const int piece = lane % (DIM / 16) * 2;
+            uint8_t *to = dst + key * DIM * 2;
+            *(h8_t *)(to + ((piece ^ swz<DIM>(key)) * 16)) = codes8(kx[j][0], kx[j][1]);
+            *(h8_t *)(to + (((piece + 1) ^ swz<DIM>(key)) * 16)) = codes8(kx[j][2], kx[j][3]);
+            to += kTile;
+            *(h8_t *)(to + ((piece ^ swz<DIM>(key)) * 16)) = codes8(vx[j][0], vx[j][1]);
+            *(h8_t *)(to + (((piece + 1) ^ swz<DIM>(key)) * 16)) = codes8(vx[j][2], vx[j][3]);
+        }
+        Scales<KT> &sc = scales[i & 1][kw];
+        if (rw == 0) {
+            const int e = exponent(sx);
+            if (__any(e > lifted)) lifted = max(wave_max(e), lifted);
+            if (lane < KT) sc.v[lane] = relative(sx, lifted, W::kShift);
+            if (lane == 0) sc.top = lifted;
+        } else if (rw == 1 && lane < KT) {
+            sc.k[lane] = fabsf(sx) <= FLT_MAX ? sx : NAN;
+        }
+    };
+    int pages = -1;
+    if (tiles > 0) {
+        load(0, look(0));
+        pages = look(1);
+        stage(0);
+        if (tiles > 1) load(1, pages);
+        pages = look(2);
+    }
+    for (int i = 0; i < rounds; ++i) {
+        __syncthreads();
+        if (i + 1 < tiles) {
+            stage(i + 1);
+            if (i + 2 < tiles) {
+                load(i + 2, pages);
+                pages = look(i + 3);
+            }
+        }
+        if (i >= tiles) continue;
+        __builtin_amdgcn_sched_barrier(0);
+        const Scales<KT> &sc = scales[i & 1][kw];
+        const int now = uniform(sc.top);
+        if (now != top) {
+            w.rescale(__builtin_amdgcn_ldexpf(1.0f, top - now));
+            top = now;
+        }
+        const int k0 = key_of(i);
+        const uint8_t *kbuf = stages + (i & 1) * 2 * kTile;
+        w.template step<KT>(kbuf, kbuf + kTile, sc, k0, !r.all(k0, KT, top_lo), r.sinks);
+    }
+    // the values' own magnitude again, the maximum in powers of two
+#pragma unroll
+    for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w.o[d][i] = __builtin_amdgcn_ldexpf(w.o[d][i], top - W::kShift);
+    float l = halves_sum(w.l), m = w.m * w.c;
+    if (KW > 1) {
+        // join the groups: the first takes over its rows' sum
+        if (lane < 32) ml[0][kw][mine] = m, ml[1][kw][mine] = l;
+        __syncthreads();
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) most = fmaxf(most, ml[0][i][mine]);
+        const float zero = most == -INFINITY ? 0.0f : most;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) l += ml[1][i][mine] * factor_of(ml[0][i][mine] - zero);
+        const float fs = factor_of(m - zero);
+        m = most;
+        float *share = (float *)(lds + wave * P::kShare) + (lane % 32) * P::kPitch + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                f4_t v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = w.o[d][i + e] * fs;
+                *(f4_t *)(share + 32 * d + 2 * i) = v;
+            }
+        __syncthreads();
+        if (pl.splits > 1 && wave < RW && lane < 32 && row < row1) {
+            const int64_t out = (int64_t)(at.first + row / pl.group) * a.q_heads +
+                                hk * pl.group + row % pl.group;
+            put_ml(a, pl, split, out, m, l);
+        }
+        if (wave < RW && lane < 32) ml[1][0][mine] = l;
+        __syncthreads();
+        if (pl.splits > 1 && t0 >= t1) return;
+        for (int e = threadIdx.x; e < (row1 - row0) * (DIM / 4); e += P::kThreads) {
+            const int rr = e / (DIM / 4), d = e % (DIM / 4) * 4;
+            const float *src = (const float *)(lds + rr / 32 * P::kShare) + rr % 32 * P::kPitch + d;
+            f4_t o = *(const f4_t *)src;
+#pragma unroll
+            for (int i = 1; i < KW; ++i) {
+                const f4_t v = *(const f4_t *)(src + i * RW * P::kShare / 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[x] += v[x];
+            }
+            const int token = (row0 + rr) / pl.group;
+            const int64_t out = (int64_t)(at.first + token) * a.q_heads + hk * pl.group +
+                                (row0 + rr) % pl.group;
+            put4<F32>(a, pl, split, out, DIM, d, o, ml[1][0][rr], position0 + token >= 0);
+        }
+        return;
+    }
+    if (row >= row1) return;
+    const int64_t out = (int64_t)(at.first + row / pl.group) * a.q_heads + hk * pl.group +
+                        row % pl.group;
+    // (one wave group: 128-row tiles, whose key axis is never split)
+#pragma unroll
+    for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            put_y4<F32>(a, out, DIM, 32 * d + 2 * i + 4 * half,
+                        f4_t{w.o[d][i], w.o[d][i + 1], w.o[d][i + 2], w.o[d][i + 3]}, l,
+                        w.p >= 0);
+}
+
+// ---- choices on the host ----------------------------------------------------
+struct Choice {
+    int rows;   // of a tile: 32 (every wave on its own keys), 64 or 128 (waves share them)
+    int waves;  // of a 32-row workgroup
+    int64_t tiles;
+    int splits;
+    int least;  // key tiles of a part, at least
+    size_t part, bytes;  // workspace: bytes of the partial rows, and in all
+};
+
+// How a call is cut into work items.  The host knows the sizes, not the
+// conversations' lengths: those may change between replays of a graph.
+Choice choose(const AttentionArgs &a) {
+    Choice ch;
+    const int dim = a.cache.dim, heads = a.cache.heads;
+    const int64_t rows = (int64_t)a.n * (a.q_heads / heads);
+    const int64_t cus = device_shape().cus;
+    if (rows <= (int64_t)kStepRows * a.batch)
+        ch.rows = 32;
+    else
+        ch.rows = (rows / 128 + (a.batch + 1) / 2) * heads >= cus ? 128 : 64;
+    const int R = ch.rows;
+    ch.tiles = rows / R + a.batch;
+    // the items that are likely to have work: not all tiles do
+    const int64_t likely = (R > 32 ? rows / R + (a.batch + 1) / 2
+                                   : (rows / R > a.batch ? rows / R : a.batch)) *
+                           heads;
+    // the key tiles a row tile can have at most
+    const int KT = R == 64 ? 32 : 64;
+    int64_t keys = (int64_t)a.table_stride << a.cache.page_shift;
+    if (a.window) {
+        const int64_t near = (int64_t)a.window + a.sinks + 2 * R + 2 * KT;
+        if (near < keys) keys = near;
+    }
+    const int64_t most = (keys + KT - 1) / KT;
+    int64_t splits;
+    ch.waves = dim > 128 ? 2 : 4;
+    if (R > 32) {
+        splits = cus / likely;  // (128-row tiles are taken where that is one at most)
+        ch.least = 16;
+    } else {
+        // workgroups that run at once: two to a compute unit, four of 64-wide heads
+        const int64_t slots = cus * (dim > 64 ? 2 : 4);
+        splits = ((a.batch == 1 ? 1 : 4) * slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
+        const int64_t fair = (most * likely + slots - 1) / slots;
+        ch.least = fair > 16 ? 16 : fair < ch.waves ? ch.waves : (int)fair;
+        // too few keys to split: the workgroup's own waves take them, eight
+        // (four) instead of four (two) while there are units to spare
+        if (most / ch.least < 2 && likely <= cus) ch.waves *= 2;
+    }
+    if (splits > most / ch.least) splits = most / ch.least;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    const int64_t out = (int64_t)a.n * a.q_heads;
+    const int64_t room = (int64_t)kWorkspaceBytes / (out * (dim + 2) * 4);
+    if (splits > room) splits = room;
+    ch.splits = splits < 2 ? 1 : (int)splits;
+    if (ch.splits == 1) ch.least = 1;
+    ch.part = ch.splits > 1 ? (size_t)ch.splits * (size_t)out * (size_t)dim * 4u : 0;
+    ch.bytes = ch.splits > 1 ? ch.part + (size_t)ch.splits * (size_t)out * 8u : 0;
+    return ch;
+}
+
+template <int DIM, bool F32>
+hipError_t run(const AttentionArgs &a, const Choice &ch, const Plan &pl, hipStream_t stream) {
+    constexpr int W = DIM > 128 ? 2 : 4;
+    // heads fastest: the tiles of one head of a conversation come to the same
+    // die, eight heads to eight dies, and share its L2
+    for (int64_t base = 0; base < ch.tiles; base += 65535) {
+        const int64_t tiles = ch.tiles - base < 65535 ? ch.tiles - base : 65535;
+        const dim3 grid((uint32_t)a.cache.heads, (uint32_t)ch.splits, (uint32_t)tiles);
+        if (ch.rows == 128)
+            hipLaunchKernelGGL((pass_kernel<DIM, F32, 4, 1>), grid, dim3(256), 0, stream, a, pl,
+                               (int)base);
+        else if (ch.rows == 64)
+            hipLaunchKernelGGL((pass_kernel<DIM, F32, 2, W>), grid, dim3(128 * W), 0, stream, a,
+                               pl, (int)base);
+        else if (ch.waves == W)
+            hipLaunchKernelGGL((step_kernel<DIM, F32, W>), grid, dim3(64 * W), 0, stream, a, pl,
+                               (int)base);
+        else
+            hipLaunchKernelGGL((step_kernel<DIM, F32, 2 * W>), grid, dim3(128 * W), 0, stream, a,
+                               pl, (int)base);
+    }
+    if (ch.splits > 1)
+        hipLaunchKernelGGL((join_kernel<F32>), dim3((uint32_t)(a.n * a.q_heads)), dim3(256), 0,
+                           stream, a, pl);
+    return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t by_dim(const AttentionArgs &a, const Choice &ch, const Plan &pl, hipStream_t stream) {
+    if (a.cache.dim == 64) return run<64, F32>(a, ch, pl, stream);
+    if (a.cache.dim == 128) return run<128, F32>(a, ch, pl, stream);
+    return run<256, F32>(a, ch, pl, stream);
+}
+
+}  // namespace
+
+size_t attention8_workspace_bytes(const AttentionArgs &a) { return choose(a).bytes; }
+
+int attention8_tile_rows(const AttentionArgs &a) { return choose(a).rows; }
+
+hipError_t launch_attention8(const AttentionArgs &a, int x_f16, void *ws, hipStream_t stream) {
+    const Choice ch = choose(a);
+    const Plan pl = {a.q_heads / a.cache.heads, ch.splits, ch.least, (float *)ws,
+                     (float *)((uint8_t *)ws + ch.part)};
+    return x_f16 ? by_dim<false>(a, ch, pl, stream) : by_dim<true>(a, ch, pl, stream);
+}
+
+}  // namespace q4

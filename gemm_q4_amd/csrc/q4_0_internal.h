@@ -116,7 +116,8 @@ hipError_t launch_gemm(const void *packed, const void *x, int x_f16, float *y,
 
 // Operators between the products (include/q4_0.h documents the formulas).
 struct KvCache {
-    _Float16 *k, *v;
+    void *k, *v;               // binary16, or int8 codes with
+    float *k_scale, *v_scale;  // a scale for each row (null: binary16)
     int64_t pages;
     int heads, page_shift, dim;  // page_size == 1 << page_shift
 };
@@ -149,6 +150,46 @@ bool attention_supports(int dim);
 size_t attention_workspace_bytes(const AttentionArgs &a, int x_f16);
 int attention_tile_rows(const AttentionArgs &a);
 hipError_t launch_attention(const AttentionArgs &a, int x_f16, void *ws, hipStream_t stream);
+// the same over a cache of 8-bit codes
+size_t attention8_workspace_bytes(const AttentionArgs &a);
+int attention8_tile_rows(const AttentionArgs &a);
+hipError_t launch_attention8(const AttentionArgs &a, int x_f16, void *ws, hipStream_t stream);
+
+// Rows of an 8-bit cache as numbers.
+struct ReadArgs {
+    KvCache cache;
+    const int64_t *slots;
+    int64_t n;
+    void *k, *v;  // either may be null
+};
+hipError_t launch_kv_read8(const ReadArgs &a, int y_f16, hipStream_t stream);
+
+// Rows of the repacked table, scaled, and their norm.
+struct EmbedArgs {
+    const void *packed;
+    const int32_t *tokens;
+    int64_t n, vocab, in;
+    float scale;
+    float *h;
+    const float *pre;  // null: no norm
+    float weight_offset, eps;
+    void *y;
+};
+constexpr int64_t kEmbedMaxDim = 32768;
+hipError_t launch_embed(const EmbedArgs &a, int y_f16, hipStream_t stream);
+
+// Drafted tokens judged by the target's logits.
+struct VerifyArgs {
+    const void *logits, *drafted;  // drafted null: the drafts are picks
+    int64_t stride, drafted_stride;
+    int vocab, n, batch;
+    const int32_t *tokens, *q_start;
+    const float *heat;  // null: 1
+    const float *uniform;
+    int32_t *accepted, *next;
+};
+size_t verify_workspace_bytes(int64_t n, int64_t batch, int64_t vocab, bool drafted);
+hipError_t launch_verify(const VerifyArgs &a, int x_f16, void *ws, hipStream_t stream);
 
 struct NormArgs {
     const void *b;  // null: no block output

@@ -440,6 +440,123 @@ int q4_0_attention_workspace_size(const q4_0_kv_cache *cache, int64_t q_heads, i
 int q4_0_select_attention(const q4_0_kv_cache *cache, int64_t q_heads, int x_dtype, int64_t n,
                           int64_t table_stride, int64_t batch, int64_t window, int64_t sinks);
 
+/* ---- the cache in 8 bits ---------------------------------------------------
+ * The same paged cache with int8 codes and one float32 scale to each row (a token's
+ * dim elements of one head, of K or of V): an element is scale * code.  It takes
+ * dim + 4 bytes a row where binary16 takes 2 dim, and attention reads as many. */
+
+/* K and V codes each int8 [pages][heads][page_size][dim], dense, 16-byte aligned;
+ * their scales each float32 [pages][heads][page_size], dense.  Nothing overlaps.  A
+ * descriptor on the HOST; the caller owns the memory.  Sizes as of q4_0_kv_cache.
+ * Codes are whole numbers from -128 to 127 (the library writes none below -127);
+ * a scale that is no finite number makes what sees its row NaN. */
+typedef struct q4_0_kv_cache8 {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    int64_t pages, heads, page_size, dim;
+} q4_0_kv_cache8;
+
+/* q4_0_kv_append into such a cache: the same arguments and checks.  Each row x of K
+ * (normed and rotated) and of V is quantized as it is written:
+ *     scale = max_i |x[i]| / 127          (float32 division)
+ *     code[i] = x[i] / scale, rounded to nearest, ties to even (float32 division)
+ * A scale below 2^-126 becomes 0, with codes 0.  A row that holds an infinity or a
+ * NaN gets a NaN scale: it reads as NaN altogether. */
+int q4_0_kv_append8(const q4_0_kv_cache8 *cache, const q4_0_rotary *rot, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, int x_dtype, void *q_out, int q_dtype, int64_t q_heads,
+                    const int32_t *positions, const int64_t *slots, int64_t n, void *stream);
+
+/* Rows of an 8-bit cache as numbers: scale * code, rounded once to y_dtype.
+ *   slots : DEVICE int64 [n], page * page_size + offset, in any order and as often as
+ *           wanted.  A slot outside [0, pages * page_size) gives rows of 0.
+ *   k, v  : DEVICE [n][heads][dim] of y_dtype, dense, 16-byte aligned; one of them
+ *           may be NULL.
+ * 1 <= n <= Q4_0_MAX_N.  Needs no workspace. */
+int q4_0_kv_read8(const q4_0_kv_cache8 *cache, const int64_t *slots, int64_t n, void *k, void *v,
+                  int y_dtype, void *stream);
+
+/* q4_0_attention over an 8-bit cache: the same formula on the elements scale * code,
+ * the same arguments, checks and limits.  Codes enter both products exactly; scales
+ * multiply scores and weights in float32.  Binary16 x: the weights of passes
+ * (q4_0_select_attention8: 64 and 128 rows) are rounded to binary16, else held in
+ * two parts, as with float32 x.  Codes and scales that a row does not see never
+ * change it. */
+int q4_0_attention8(const q4_0_kv_cache8 *cache, const void *q, int64_t q_stride, int x_dtype,
+                    int64_t q_heads, void *y, int64_t n, const int32_t *q_start,
+                    const int32_t *kv_len, const int32_t *table, int64_t table_stride,
+                    int64_t batch, int64_t window, int64_t sinks, float scale, void *workspace,
+                    size_t workspace_bytes, void *stream);
+int q4_0_attention8_workspace_size(const q4_0_kv_cache8 *cache, int64_t q_heads, int x_dtype,
+                                   int64_t n, int64_t table_stride, int64_t batch,
+                                   int64_t window, int64_t sinks, size_t *bytes);
+int q4_0_select_attention8(const q4_0_kv_cache8 *cache, int64_t q_heads, int x_dtype, int64_t n,
+                           int64_t table_stride, int64_t batch, int64_t window, int64_t sinks);
+
+/* ---- the ends of a step: token ids in, token ids out -----------------------
+ * A step may carry, after a conversation's last token, tokens that a draft proposed
+ * (golem README, "Multi-token prediction": they ride in the pass that reads the
+ * weights anyway): its rows are that token's and the drafts', and the logits of each
+ * row judge the draft that follows it. */
+
+/* Rows of a repacked table, scaled, and their norm:
+ *     h[t] = scale * W[tokens[t]],   y[t] = N(h[t]; pre)   (N as in q4_0_residual_norm)
+ *   packed : DEVICE, q4_0_repack's layout of W[out x in] (so the logit head's own
+ *            matrix serves, where a model ties them), 16-byte aligned.
+ *   tokens : DEVICE int32 [n].  One outside [0, out) gives a row of 0.
+ *   h      : DEVICE float32 [n][in], dense, 16-byte aligned.
+ *   y      : DEVICE [n][in] of y_dtype, dense, 16-byte aligned, with pre (DEVICE
+ *            float32 [in], 16-byte aligned); or NULL: no norm, pre ignored.
+ * d * (q - 8) is exact in float32, the scale rounds it once; sums are float32, a
+ * binary16 y is rounded once.  Any finite scale (Q4_0_EINVAL); 1 <= n <= Q4_0_MAX_N,
+ * in <= 32768 (Q4_0_EUNSUPPORTED above).  Needs no workspace. */
+int q4_0_embed(const void *packed, const int32_t *tokens, int64_t n, int64_t out, int64_t in,
+               float scale, float *h, const float *pre, float weight_offset, float eps, void *y,
+               int y_dtype, void *stream);
+
+/* Drafted tokens verified against the target's probabilities, and the next token.
+ * Conversation s holds rows q_start[s] .. q_start[s+1] - 1 of `logits` (as of
+ * q4_0_attention's q).  Row t, but for the last, judges the draft d = tokens[t+1]:
+ *     p = softmax(logits[t] / T),  q = softmax(drafted[t] / T),  T = temperature[s]
+ *     d is taken when  uniform[t][0] * q(d) < p(d)
+ * where without `drafted` all of q lies on d (a draft that was picked, not drawn).
+ * accepted[s] is the number of drafts taken before the first that is not, and r the
+ * row that judged that one, or the last row if all were.  next[s] is then the lowest
+ * token whose cumulative weight exceeds uniform[r][1] times the total, the weights
+ *     max(p - q, 0)   after a refused draft (p, where that leaves nothing),
+ *     p               after all of them
+ * of row r; the highest token with a weight if none does (a number from 1 on).  So
+ * the drawn tokens are distributed as the target alone would draw them, if uniform
+ * is uniform on [0, 1) and the drafts were drawn from q.  With T not above 0 (or
+ * T no number) the target is its greatest logit, the lowest token where several
+ * are: drafts equal to it are taken and next is the first that would have been.
+ *   logits  : DEVICE [n] rows of vocab elements of x_dtype, `stride` apart.
+ *   drafted : DEVICE rows likewise, or NULL.  Rows that judge nothing are not read.
+ *   tokens  : DEVICE int32 [n], the step's own tokens (q4_0_embed's).  A draft outside
+ *             [0, vocab) is refused, and nothing is taken from p for it.
+ *   q_start : DEVICE int32 [batch + 1], 0 <= q_start[s] <= q_start[s+1] <= n.  A
+ *             conversation without rows gets accepted 0 and next -1.
+ *   temperature : DEVICE float32 [batch], finite; or NULL: 1.
+ *   uniform : DEVICE float32 [n][2].
+ *   accepted, next : DEVICE int32 [batch].
+ * A logit of minus infinity excludes its token.  A row that holds NaN or plus infinity,
+ * or nothing else than minus infinities, is no distribution: reached, it (or its
+ * row of `drafted`) ends the step there with next -1.
+ * Weights and their sums are float64, so that the order of summation decides no
+ * token.  1 <= n, batch <= Q4_0_MAX_N, 1 <= vocab <= Q4_0_MAX_OUT; sizes whose
+ * workspace would pass Q4_0_WORKSPACE_MAX: Q4_0_EUNSUPPORTED.  */
+int q4_0_verify(const void *logits, int64_t stride, const void *drafted, int64_t drafted_stride,
+                int x_dtype, int64_t vocab, const int32_t *tokens, const int32_t *q_start,
+                int64_t n, int64_t batch, const float *temperature, const float *uniform,
+                int32_t *accepted, int32_t *next, void *workspace, size_t workspace_bytes,
+                void *stream);
+/* Workspace bytes of q4_0_verify into *bytes (drafted: not 0 if the call has them).
+ * Host only. */
+int q4_0_verify_workspace_size(int64_t n, int64_t batch, int64_t vocab, int drafted,
+                               size_t *bytes);
+
 /* The residual step between two half blocks, with the norm after the one and
  * the norm before the next:
  *     h_out[t] = h[t] + alpha * g[t] * N(b[t]; post),   y[t] = N(h_out[t]; pre)
