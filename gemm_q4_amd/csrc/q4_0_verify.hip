@@ -7,12 +7,18 @@
 //
 // A draw is a border among up to 10^5 shares, so weights and sums are 64-bit: the
 // same token comes out whatever the order of the sums.  A weight 2^x is a table's
-// entry (256 of them) times a polynomial of the third degree, off by 2e-13.
+// entry (256 of them) times a polynomial of the third degree, off by 2e-13; weights
+// below 2^-980 of a row's largest count as none.
 //
-// Three launches.  stats: maximum and sum of every part of every row, one read.
-// rest (with the draft's logits): each conversation's refused draft, and the sums of
-// max(p - q, 0) over the parts of its row.  pick: the part, then the token.
+// stats: every part of every row, one read: its largest logit and the sum of its
+// weights (without draft logits: of all but the judged draft's, so that taking it
+// out costs no digits).  judge: each conversation's first refused draft.  rest (with
+// draft logits): sums of max(p - q, 0) over the parts of that row.  pick: the part
+// that the number falls into, then the token.  Without draft logits pick judges, and
+// two launches are all.
 #include <float.h>
+
+#include <type_traits>
 
 #include "q4_0_device.h"
 #include "q4_0_internal.h"
@@ -25,43 +31,102 @@ typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
 typedef f4_t f4_any_t __attribute__((aligned(4)));
 typedef h4_t h4_any_t __attribute__((aligned(2)));
 
-constexpr int kThreads = 256;
-constexpr int kPart = 8192;               // tokens of a part
-constexpr int kPickThreads = 1024;
-constexpr int kMaxParts = (1 << 24) / kPart;
-constexpr double kLog2e = 1.4426950408889634;
+constexpr int kPart = 2048;        // tokens of a part, one wave's
+constexpr int kLoads = kPart / 256;
+constexpr int kThreads = 256;      // of stats: four parts
+constexpr int kWaves = kThreads / 64;
+constexpr int kPickThreads = 512;  // of the others: eight parts, or eight rows judged at once
+constexpr int kPickWaves = kPickThreads / 64;
+constexpr int kHeld = 2;           // parts that a lane keeps: rows of 262144 tokens need no more
+constexpr double kFaint = 0x1p-980;
 
-// A part of a row: its largest logit, the first token that has it, and the sum of
-// its weights relative to that logit.  A sum that is no number: the part holds a
-// logit that is NaN or plus infinity.
+// A part of a row: its largest logit, the sum of its weights relative to that
+// logit, and `at`: of a greedy row the first token that has the largest, else (as
+// bits) the judged draft's logit, where it is in this part.  A sum that is no
+// number: the part holds a logit that is NaN or plus infinity.
 struct Stat {
     double sum;
     float top;
     int32_t at;
 };
 
-// 2^x for the weights, from a table of 2^(i / 256) in LDS.
-struct Power {
-    const double *table;
-    double c, least;  // 256 log2(e) / T, and where weights are 0
-    __device__ __forceinline__ Power(const double *t, double heat)
-        : table(t), c(256.0 * kLog2e / heat), least(-256.0 * 1100.0 / (256.0 * kLog2e / heat)) {}
-    // exp(d / T) of a difference d <= 0
-    __device__ __forceinline__ double operator()(double d) const {
-        const double magic = 6755399441055744.0;  // 1.5 2^52: the sum's low bits are the integer
-        d = fmax(d, least);
-        const double k = fma(d, c, magic);
-        const double r = fma(d, c, -(k - magic));
-        const int i = (int)(uint32_t)__builtin_bit_cast(uint64_t, k);
-        // e^z, z = r ln(2) / 256, |z| < 0.00136
-        const double z = fma(fma(fma(3.3083026805413713e-09, r, 3.6655655969101062e-06), r,
-                                 0.0027076061740622863), r, 1.0);
-        return __builtin_amdgcn_ldexp(table[i & 255] * z, i >> 8);
+// How the next token is found.
+enum { kNone, kGreedy, kPlain, kWithout, kRest };
+// A conversation's judgement: the row that ends it and what follows, its largest
+// logits and the reciprocals of its total weights (of p, of q), the number to draw
+// with, its first best token.
+struct Verdict {
+    double p_share, q_share;
+    float p_top, q_top, u;
+    int row, how, draft, at;
+};
+
+// 2^(i / 256), computed by the compiler: square roots by Newton's method, and each
+// entry a product of at most eight of them.
+struct Table {
+    double v[256];
+    constexpr Table() : v() {
+        double roots[8] = {};  // 2^(1/2), 2^(1/4), ..
+        double of = 2.0;
+        for (int k = 0; k < 8; ++k) {
+            double x = of;
+            for (int n = 0; n < 12; ++n) x = 0.5 * (x + of / x);
+            roots[k] = of = x;
+        }
+        for (int i = 0; i < 256; ++i) {
+            v[i] = 1.0;
+            for (int k = 0; k < 8; ++k)
+                if (i >> (7 - k) & 1) v[i] *= roots[k];
+        }
     }
 };
+static __device__ const Table kTable = Table();
+
 __device__ __forceinline__ void fill_table(double *table) {
-    if (threadIdx.x < 256) table[threadIdx.x] = exp2((double)threadIdx.x / 256.0);
+    if (threadIdx.x < 256) table[threadIdx.x] = kTable.v[threadIdx.x];
 }
+
+// Weights exp(d / T) of differences d <= 0, from the table in LDS.
+struct Power {
+    const double *table;
+    double c, least;  // 256 log2(e) / T, and the difference that stands for all below
+    __device__ __forceinline__ Power(const double *t, double heat)
+        : table(t), c(369.3299304675746 / heat), least(-1010.0 * 0.6931471805599453 * heat) {}
+    // Sum of the weights of N differences, side by side: a single one is a chain of
+    // ten operations and an LDS read.  None is below about 2^-1010, so that the
+    // exponent is a plain addition.
+    template <int N> __device__ __forceinline__ void of(const double (&d)[N], double (&w)[N]) const {
+        const double magic = 6755399441055744.0;  // 1.5 2^52: the sum's low bits are the integer
+        double r[N], z[N];
+        uint32_t k[N];
+        uint64_t t[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const double x = fmax(d[i], least), y = fma(x, c, magic);
+            r[i] = fma(x, c, -(y - magic));
+            k[i] = (uint32_t)__builtin_bit_cast(uint64_t, y);
+            t[i] = __builtin_bit_cast(uint64_t, table[k[i] & 255]);
+        }
+        // e^z, z = r ln(2) / 256, |z| < 0.00136
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = fma(3.3083026805413713e-09, r[i], 3.6655655969101062e-06);
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = fma(z[i], r[i], 0.0027076061740622863);
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = fma(z[i], r[i], 1.0);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            w[i] = z[i] * __builtin_bit_cast(double, t[i] + ((uint64_t)((k[i] << 12) & 0xFFF00000u)
+                                                             << 32));
+    }
+    // One, 0 below that.
+    __device__ __forceinline__ double exact(double d) const {
+        const double one[1] = {d};
+        double w[1];
+        of(one, w);
+        return d > least ? w[0] : 0.0;
+    }
+};
 
 // Four neighbouring logits of a row from element i on; minus infinity past its end.
 template <bool F16> __device__ __forceinline__ f4_t load4(const void *row, int i, int vocab) {
@@ -83,14 +148,74 @@ template <bool F16> __device__ __forceinline__ f4_t load4(const void *row, int i
 template <bool F16> __device__ __forceinline__ float load1(const void *row, int i) {
     return F16 ? (float)((const _Float16 *)row)[i] : ((const float *)row)[i];
 }
+// A lane's logits of a part: runs of four, 256 tokens apart.
+template <bool F16>
+__device__ __forceinline__ void load_part(f4_t (&l)[kLoads], const void *row, int part, int vocab) {
+    const int base = part * kPart + threadIdx.x % 64 * 4;
+    if ((part + 1) * kPart <= vocab) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) l[i] = load4<F16>(row, base + i * 256, INT32_MAX);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) l[i] = load4<F16>(row, base + i * 256, vocab);
+    }
+}
 template <bool F16>
 __device__ __forceinline__ const void *row_of(const void *p, int64_t row, int64_t stride) {
     return (const uint8_t *)p + row * stride * (F16 ? 2 : 4);
 }
 
-template <typename T, typename F> __device__ __forceinline__ T over_wave(T x, F f) {
+// Sums over a wave by lane moves: no LDS in between.
+template <int CTRL, int ROWS> __device__ __forceinline__ double moved(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF,
+                                                              false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL,
+                                                              ROWS, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// x of this lane and all before it.
+__device__ __forceinline__ double up_to(double x) {
+    x += moved<0x111, 0xF>(x);  // one lane on within 16, two, four, eight
+    x += moved<0x112, 0xF>(x);
+    x += moved<0x114, 0xF>(x);
+    x += moved<0x118, 0xF>(x);
+    x += moved<0x142, 0xA>(x);  // the last of 16 to the next 16, of 32 to the next 32
+    x += moved<0x143, 0xC>(x);
+    return x;
+}
+__device__ __forceinline__ double lane_of(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double x) { return lane_of(up_to(x), 63); }
+
+// The larger number; NaN if either is.
+__device__ __forceinline__ float larger(float x, float y) {
+    return __builtin_elementwise_maximum(x, y);
+}
+template <int CTRL> __device__ __forceinline__ float turned(float x) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float wave_max(float x) {
+    x = larger(x, turned<0x121>(x));
+    x = larger(x, turned<0x122>(x));
+    x = larger(x, turned<0x124>(x));
+    x = larger(x, turned<0x128>(x));
+    uint32_t u = __builtin_bit_cast(uint32_t, x);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    x = larger(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+    u = __builtin_bit_cast(uint32_t, x);
+    r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return larger(__builtin_bit_cast(float, (uint32_t)r[0]),
+                  __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ int wave_min(int x) {
 #pragma unroll
-    for (int i = 1; i < 64; i <<= 1) x = f(x, __shfl_xor(x, i));
+    for (int i = 1; i < 64; i <<= 1) x = min(x, __shfl_xor(x, i));
     return x;
 }
 
@@ -122,361 +247,473 @@ __device__ __forceinline__ float heat_of(const VerifyArgs &a, int s) {
 }
 
 // ---- every part of every row ------------------------------------------------
-template <bool F16>
-__global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a, Stat *stats, int parts) {
-    constexpr int kLoads = kPart / (4 * kThreads);
+// EAGER: few workgroups.  Every row is requested before the conversation that holds
+// it is known; otherwise the draft's rows only then, since of those one in each
+// conversation is not needed, and none of the greedy ones.
+template <bool F16, bool EAGER>
+__global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *stats, int parts) {
     __shared__ double table[256];
-    __shared__ float tops[kThreads / 64];
-    __shared__ double sums[kThreads / 64];
-    __shared__ int firsts[kThreads / 64];
-    const int part = blockIdx.x % parts;
-    const bool drafted = blockIdx.x / parts >= (uint32_t)a.n;
-    const int row = blockIdx.x / parts - (drafted ? a.n : 0);
+    const int groups = (parts + kWaves - 1) / kWaves, lane = threadIdx.x % 64;
+    const int part =
+        __builtin_amdgcn_readfirstlane(blockIdx.x % groups * kWaves + threadIdx.x / 64);
+    const bool drafted = blockIdx.x / groups >= (uint32_t)a.n;
+    const int row = blockIdx.x / groups - (drafted ? a.n : 0);
+    f4_t l[kLoads];
+    const void *x = drafted ? row_of<F16>(a.drafted, row, a.drafted_stride)
+                            : row_of<F16>(a.logits, row, a.stride);
+    if (EAGER || !drafted) load_part<F16>(l, x, part, a.vocab);
+    fill_table(table);
     Span sp;
     if (!span_of(a, holder(a, row), sp) || row < sp.first || row > sp.last) return;
     const float heat = heat_of(a, sp.s);
     const bool cold = !(heat > 0.0f);
     if (drafted && (row == sp.last || cold)) return;
-    const void *x = drafted ? row_of<F16>(a.drafted, row, a.drafted_stride)
-                            : row_of<F16>(a.logits, row, a.stride);
-    const int base = part * kPart + threadIdx.x * 4;
-    f4_t l[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) l[i] = load4<F16>(x, base + i * 4 * kThreads, a.vocab);
-    fill_table(table);
+    if (!EAGER && drafted) load_part<F16>(l, x, part, a.vocab);
+    const int draft = row < sp.last ? a.tokens[row + 1] : -1;
+    __syncthreads();
+    if (part >= parts) return;
+    const int base = part * kPart + lane * 4;
     float top = -INFINITY;
-    bool bad = false;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            top = fmaxf(top, l[i][e]);
-            bad |= !(l[i][e] <= FLT_MAX);
-        }
-    top = over_wave(top, [](float p, float q) { return fmaxf(p, q); });
-    const int wave = threadIdx.x / 64;
-    if (threadIdx.x % 64 == 0) tops[wave] = top;
-    bad = __syncthreads_or(bad);
-#pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) top = fmaxf(top, tops[i]);
-    double sum = 0.0;
-    int first = INT32_MAX;
-    if (cold) {
-#pragma unroll
-        for (int i = kLoads; i-- > 0;)
+        for (int e = 0; e < 4; ++e) top = larger(top, l[i][e]);
+    top = wave_max(top);
+    Stat st = {0.0, top, INT32_MAX};
+    if (!(top <= FLT_MAX)) {
+        st.sum = NAN;
+    } else if (top == -INFINITY) {
+    } else if (cold) {
+        // (read again: a loop that is not unrolled, beside the one that is)
+        int first = INT32_MAX;
+#pragma nounroll
+        for (int i = kLoads; i-- > 0;) {
+            const f4_t again = load4<F16>(x, base + i * 256, a.vocab);
 #pragma unroll
             for (int e = 4; e-- > 0;)
-                if (l[i][e] == top) first = base + i * 4 * kThreads + e;
-        first = over_wave(first, [](int p, int q) { return min(p, q); });
-    } else if (top != -INFINITY) {
+                if (again[e] == top) first = base + i * 256 + e;
+        }
+        st.at = wave_min(first);
+    } else {
         const Power power(table, heat);
         const double m = top;
+        double sum = 0.0;
+        const bool judged = draft >= part * kPart && draft < min(part * kPart + kPart, a.vocab);
+        if (judged) st.at = __builtin_bit_cast(int, load1<F16>(x, draft));
+        if (judged && !a.drafted) {
+            // the judged draft's weight stays out
+#pragma nounroll
+            for (int i = 0; i < kLoads; ++i) {
+                const f4_t again = load4<F16>(x, base + i * 256, a.vocab);
+                double d[4], w[4];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
+                for (int e = 0; e < 4; ++e) d[e] = (double)again[e] - m;
+                power.of(d, w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum += power((double)l[i][e] - m);
-        sum = over_wave(sum, [](double p, double q) { return p + q; });
+                for (int e = 0; e < 4; ++e) sum += base + i * 256 + e == draft ? 0.0 : w[e];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * kLoads; i += 2) {
+                const double d[2] = {(double)l[i / 4][i % 4] - m, (double)l[i / 4][i % 4 + 1] - m};
+                double w[2];
+                power.of(d, w);
+                sum += w[0];
+                sum += w[1];
+                __builtin_amdgcn_sched_barrier(0);  // else all are formed side by side
+            }
+        }
+        sum = wave_sum(sum);
+        st.sum = sum < kFaint ? 0.0 : sum;
     }
-    if (threadIdx.x % 64 == 0) sums[wave] = sum, firsts[wave] = first;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-#pragma unroll
-    for (int i = 1; i < kThreads / 64; ++i) {
-        sum += sums[i];
-        first = min(first, firsts[i]);
-    }
-    stats[(int64_t)blockIdx.x] = {bad ? (double)NAN : sum, top, first};
+    if (lane == 0) stats[(row + (drafted ? (int64_t)a.n : 0)) * parts + part] = st;
 }
 
 // ---- the refused draft ------------------------------------------------------
-// A row's distribution: largest logit, its first token, total weight; `fine` if it
-// is one.
+// A row's distribution: largest logit, its first token, total weight (without the
+// judged draft's where stats left it out); `fine` if it is one.
 struct Whole {
     double sum;
     float top;
     int at;
     bool fine;
 };
+struct Parts {
+    Stat of[kHeld];  // lane's parts: lane, lane + 64
+    __device__ __forceinline__ void load(const Stat *stats, int parts) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int part = 64 * i + (int)(threadIdx.x % 64);
+            of[i] = {0.0, -INFINITY, INT32_MAX};
+            if (part < parts) of[i] = stats[part];
+        }
+    }
+};
 // By all lanes of a wave.
-__device__ __forceinline__ Whole whole_of(const Stat *stats, int parts, double c) {
+__device__ __forceinline__ Whole whole_of(const Stat *stats, const Parts &held, int parts,
+                                          bool cold, const Power &power) {
     const int lane = threadIdx.x % 64;
     Whole w = {0.0, -INFINITY, INT32_MAX, true};
-    for (int i = lane; i < parts; i += 64) w.top = fmaxf(w.top, stats[i].top);
-    w.top = over_wave(w.top, [](float p, float q) { return fmaxf(p, q); });
-    for (int i = lane; i < parts; i += 64) {
-        const Stat st = stats[i];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) w.top = larger(w.top, held.of[i].top);
+    for (int i = lane + 64 * kHeld; i < parts; i += 64) w.top = larger(w.top, stats[i].top);
+    w.top = wave_max(w.top);
+    const auto add = [&](const Stat &st) {
         if (st.sum != st.sum) w.fine = false;
         if (st.top == w.top) w.at = min(w.at, st.at);
-        if (st.sum > 0.0) w.sum += st.sum * exp2(((double)st.top - (double)w.top) * c);
-    }
-    w.sum = over_wave(w.sum, [](double p, double q) { return p + q; });
-    w.at = over_wave(w.at, [](int p, int q) { return min(p, q); });
+        if (!cold) w.sum += st.sum * power.exact((double)st.top - (double)w.top);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) add(held.of[i]);
+    for (int i = lane + 64 * kHeld; i < parts; i += 64) add(stats[i]);
+    if (cold)
+        w.at = wave_min(w.at);
+    else
+        w.sum = wave_sum(w.sum);
     w.fine = __all(w.fine) && w.top != -INFINITY;
     return w;
 }
-
-// How the next token is found.
-enum { kNone, kGreedy, kPlain, kWithout, kRest };
-struct Verdict {
-    int row, how, draft;
-    Whole p, q;
-};
+// The judged draft's logit, minus infinity for a token outside the vocabulary.
+__device__ __forceinline__ float drafted_logit(const Stat *stats, const Parts &held, int draft,
+                                               bool real) {
+    if (!real) return -INFINITY;
+    const int part = draft / kPart;
+    Stat st;
+    if (part < 64 * kHeld) {
+        const Stat &mine = held.of[0];
+        st.top = __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(
+                       __builtin_bit_cast(int, part < 64 ? mine.top : held.of[1].top), part % 64));
+        st.at = __builtin_amdgcn_readlane(part < 64 ? mine.at : held.of[1].at, part % 64);
+    } else {
+        st = stats[part];
+    }
+    // (a part of minus infinities alone has noted none)
+    return st.top == -INFINITY ? st.top : __builtin_bit_cast(float, st.at);
+}
 
 // The first row of the conversation whose draft is refused (its last row, if none
 // is), and what follows.  Each of the workgroup's waves takes a row.
-template <bool F16, int WAVES>
 __device__ __forceinline__ Verdict judge(const VerifyArgs &a, const Stat *stats, int parts,
-                                         const Span &sp, float heat, Verdict (&seen)[WAVES]) {
-    const int wave = threadIdx.x / 64;
+                                         const Span &sp, float heat, const Power &power,
+                                         Verdict (&seen)[kPickWaves]) {
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const bool cold = !(heat > 0.0f);
-    const double c = kLog2e / (double)heat;
-    for (int row0 = sp.first;; row0 += WAVES) {
+    for (int row0 = sp.first;; row0 += kPickWaves) {
         const int row = row0 + wave;
-        Verdict v = {row, -1, -1, {}, {}};
+        Verdict v = {0.0, 0.0, 0.0f, 0.0f, 0.0f, row, -1, -1, 0};
+        Parts of_p, of_q;
+        const Stat *ps = stats + (int64_t)row * parts;
+        const Stat *qs = stats + ((int64_t)a.n + row) * parts;
+        const bool last = row == sp.last, drafted = a.drafted && !last && !cold;
+        float u = 0.0f;
         if (row <= sp.last) {
-            v.p = whole_of(stats + (int64_t)row * parts, parts, c);
-            v.draft = row < sp.last ? a.tokens[row + 1] : -1;
+            of_p.load(ps, parts);
+            if (drafted) of_q.load(qs, parts);
+            u = a.uniform[2 * (int64_t)row];
+            v.u = a.uniform[2 * (int64_t)row + 1];
+            if (!last) v.draft = __builtin_amdgcn_readfirstlane(a.tokens[row + 1]);
+        }
+        __syncthreads();  // (the table, in the first round)
+        if (row <= sp.last) {
             const bool real = v.draft >= 0 && v.draft < a.vocab;
-            if (!v.p.fine) {
+            const Whole p = whole_of(ps, of_p, parts, cold, power);
+            v.p_top = p.top;
+            v.at = p.at;
+            if (!p.fine) {
                 v.how = kNone;
             } else if (cold) {
-                if (row == sp.last || v.draft != v.p.at) v.how = kGreedy;
-            } else if (row == sp.last) {
-                v.how = kPlain;
+                if (last || v.draft != p.at) v.how = kGreedy;
             } else {
-                const double u = a.uniform[2 * (int64_t)row];
-                const double pd =
-                    !real ? 0.0
-                          : exp2(((double)load1<F16>(row_of<F16>(a.logits, row, a.stride), v.draft) -
-                                  (double)v.p.top) * c) / v.p.sum;
-                double qd = 1.0;
-                if (a.drafted) {
-                    v.q = whole_of(stats + ((int64_t)a.n + row) * parts, parts, c);
-                    qd = !real ? 0.0
-                               : exp2(((double)load1<F16>(
-                                           row_of<F16>(a.drafted, row, a.drafted_stride), v.draft) -
-                                       (double)v.q.top) * c) / v.q.sum;
+                const double wd =
+                    power.exact((double)drafted_logit(ps, of_p, v.draft, real) - (double)p.top);
+                v.p_share = 1.0 / (p.sum + (a.drafted ? 0.0 : wd));
+                if (last) {
+                    v.how = kPlain;
+                } else if (!drafted) {
+                    if (!((double)u < wd * v.p_share)) v.how = real ? kWithout : kPlain;
+                } else {
+                    const Whole q = whole_of(qs, of_q, parts, false, power);
+                    v.q_top = q.top;
+                    v.q_share = 1.0 / q.sum;
+                    const double qd = power.exact((double)drafted_logit(qs, of_q, v.draft, real) -
+                                                  (double)q.top) * v.q_share;
+                    if (!q.fine)
+                        v.how = kNone;
+                    else if (!((double)u * qd < wd * v.p_share))
+                        v.how = kRest;
                 }
-                if (a.drafted && !v.q.fine)
-                    v.how = kNone;
-                else if (!(u * qd < pd))
-                    v.how = a.drafted ? kRest : real ? kWithout : kPlain;
             }
         }
-        if (threadIdx.x % 64 == 0) seen[wave] = v;
+        if (lane == 0) seen[wave] = v;
         __syncthreads();
         int found = -1;
 #pragma unroll
-        for (int i = WAVES; i-- > 0;)
+        for (int i = kPickWaves; i-- > 0;)
             if (row0 + i <= sp.last && seen[i].how >= 0) found = i;
         if (found >= 0) return seen[found];
-        __syncthreads();
     }
 }
 
-// max(p - q, 0) of a token
-__device__ __forceinline__ double rest_of(const Power &power, const Verdict &v, float l, float g) {
-    const double p = power((double)l - (double)v.p.top) / v.p.sum;
-    const double q = power((double)g - (double)v.q.top) / v.q.sum;
-    return fmax(p - q, 0.0);
+__global__ __launch_bounds__(kPickThreads) void judge_kernel(VerifyArgs a, const Stat *stats,
+                                                             Verdict *verdicts, int parts) {
+    __shared__ double table[256];
+    __shared__ Verdict seen[kPickWaves];
+    const float heat = heat_of(a, blockIdx.x);
+    Span sp;
+    if (!span_of(a, blockIdx.x, sp)) return;
+    fill_table(table);
+    const Verdict v = judge(a, stats, parts, sp, heat, Power(table, heat), seen);
+    if (threadIdx.x == 0) verdicts[sp.s] = v;
 }
 
+// max(p - q, 0) of a token.  Two products, each rounded, then the difference: as one
+// fused operation equal p and q would leave the rounding of one of them.
+__device__ __forceinline__ double above(double p, double p_share, double q, double q_share) {
+#pragma clang fp contract(off)
+    return fmax(p * p_share - q * q_share, 0.0);
+}
+
+// Sums of max(p - q, 0), a part to a wave.
 template <bool F16>
-__global__ __launch_bounds__(kThreads, 4) void rest_kernel(VerifyArgs a, const Stat *stats,
-                                                        double *rests, int parts) {
-    constexpr int kLoads = kPart / (4 * kThreads);
+__global__ __launch_bounds__(kPickThreads) void rest_kernel(VerifyArgs a, const Verdict *verdicts,
+                                                            double *rests, int parts) {
     __shared__ double table[256];
-    __shared__ double sums[kThreads / 64];
-    __shared__ Verdict seen[kThreads / 64];
-    const int part = blockIdx.x % parts, s = blockIdx.x / parts;
-    Span sp;
-    if (!span_of(a, s, sp)) return;
+    const int groups = (parts + kPickWaves - 1) / kPickWaves, s = blockIdx.x / groups;
+    const int part = __builtin_amdgcn_readfirstlane(blockIdx.x % groups * kPickWaves +
+                                                    threadIdx.x / 64);
+    const Verdict v = verdicts[s];  // (of an empty conversation: whatever is there)
     const float heat = heat_of(a, s);
-    if (!(heat > 0.0f)) return;
-    fill_table(table);
-    const Verdict v = judge<F16>(a, stats, parts, sp, heat, seen);
-    if (v.how != kRest) return;
-    const void *x = row_of<F16>(a.logits, v.row, a.stride);
-    const void *y = row_of<F16>(a.drafted, v.row, a.drafted_stride);
     const Power power(table, heat);
+    Span sp;
+    const bool some = span_of(a, s, sp);
+    fill_table(table);
+    if (!some) return;
+    if (v.how != kRest) return;
+    f4_t l[kLoads], g[kLoads];
+    load_part<F16>(l, row_of<F16>(a.logits, v.row, a.stride), part, a.vocab);
+    load_part<F16>(g, row_of<F16>(a.drafted, v.row, a.drafted_stride), part, a.vocab);
+    __syncthreads();
+    if (part >= parts) return;
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int at = part * kPart + (i * kThreads + threadIdx.x) * 4;
-        const f4_t l = load4<F16>(x, at, a.vocab), g = load4<F16>(y, at, a.vocab);
+        double d[8], w[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += rest_of(power, v, l[e], g[e]);
+        for (int e = 0; e < 4; ++e) {
+            d[e] = (double)l[i][e] - (double)v.p_top;
+            d[4 + e] = (double)g[i][e] - (double)v.q_top;
+        }
+        power.of(d, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += above(w[e], v.p_share, w[4 + e], v.q_share);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    sum = over_wave(sum, [](double p, double q) { return p + q; });
-    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = sum;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-#pragma unroll
-    for (int i = 1; i < kThreads / 64; ++i) sum += sums[i];
-    rests[blockIdx.x] = sum;
+    sum = wave_sum(sum);
+    if (threadIdx.x % 64 == 0) rests[(int64_t)s * parts + part] = sum < kFaint ? 0.0 : sum;
 }
 
 // ---- the next token ---------------------------------------------------------
-// Sum of x over the workgroup before this thread; the total in `total`.
-__device__ __forceinline__ double before(double x, double (&sums)[kPickThreads / 64],
-                                         double &total) {
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    double run = x;
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) {
-        const double y = __shfl_up(run, i);
-        if (lane >= i) run += y;
-    }
-    __syncthreads();
-    if (lane == 63) sums[wave] = run;
-    __syncthreads();
-    double base = 0.0;
-    total = 0.0;
-#pragma unroll
-    for (int i = 0; i < kPickThreads / 64; ++i) {
-        if (i < wave) base += sums[i];
-        total += sums[i];
-    }
-    return base + run - x;
-}
-
-template <bool F16>
+// JUDGED: verdicts and rests are there.
+template <bool F16, bool JUDGED>
 __global__ __launch_bounds__(kPickThreads) void pick_kernel(VerifyArgs a, const Stat *stats,
+                                                            const Verdict *verdicts,
                                                             const double *rests, int parts) {
     constexpr int kEach = kPart / kPickThreads;
+    static_assert(kEach == 4, "one load to a thread");
     __shared__ double table[256];
-    __shared__ double share[kMaxParts];
-    __shared__ double sums[kPickThreads / 64];
-    __shared__ Verdict seen[kPickThreads / 64];
-    __shared__ int found, highest;
-    const int s = blockIdx.x;
+    __shared__ double sums[kPickWaves];
+    __shared__ Verdict seen[kPickWaves];
+    __shared__ struct {
+        double target, below;
+        int part;  // -1: the draft is all there is
+    } goal;
+    __shared__ int highest;
+    const int s = blockIdx.x, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    // what depends on the conversation's number alone is requested together
+    const float heat = heat_of(a, s);
+    const Power power(table, heat);
+    Verdict v;
+    double held[kHeld] = {0.0, 0.0};
+    if (JUDGED) {
+        v = verdicts[s];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (lane + 64 * i < parts) held[i] = rests[(int64_t)s * parts + lane + 64 * i];
+    }
     Span sp;
-    if (!span_of(a, s, sp)) {
+    const bool some = span_of(a, s, sp);
+    fill_table(table);
+    if (!some) {
         if (threadIdx.x == 0) a.accepted[s] = 0, a.next[s] = -1;
         return;
     }
-    const float heat = heat_of(a, s);
-    fill_table(table);
-    Verdict v = judge<F16>(a, stats, parts, sp, heat, seen);
+    if (!JUDGED) v = judge(a, stats, parts, sp, heat, power, seen);
     if (threadIdx.x == 0) {
         a.accepted[s] = v.row - sp.first;
         if (v.how == kNone) a.next[s] = -1;
-        if (v.how == kGreedy) a.next[s] = v.p.at;
+        if (v.how == kGreedy) a.next[s] = v.at;
+        highest = -1;
     }
     if (v.how == kNone || v.how == kGreedy) return;
-    const Power power(table, heat);
-    const double c = kLog2e / (double)heat;
-    const void *x = row_of<F16>(a.logits, v.row, a.stride);
-    const void *y = a.drafted ? row_of<F16>(a.drafted, v.row, a.drafted_stride) : nullptr;
-    // a thread's neighbouring tokens of a part, as weights
-    double w[kEach];
-    const auto weigh = [&](int part) {
-        const int at = part * kPart + threadIdx.x * kEach;
-#pragma unroll
-        for (int i = 0; i < kEach; i += 4) {
-            const f4_t l = load4<F16>(x, at + i, a.vocab);
-            f4_t g = l;
-            if (v.how == kRest) g = load4<F16>(y, at + i, a.vocab);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (v.how == kRest)
-                    w[i + e] = rest_of(power, v, l[e], g[e]);
-                else
-                    w[i + e] = power((double)l[e] - (double)v.p.top);
-                if (v.how == kWithout && at + i + e == v.draft) w[i + e] = 0.0;
-            }
-        }
+    __syncthreads();  // (the table)
+    // Shares of the parts, by every wave alike, 64 at a time: the held ones, then
+    // those of a longer row.
+    const auto share = [&](int i) -> double {
+        const int part = 64 * i + lane;
+        if (i < kHeld) return i == 0 ? held[0] : held[kHeld - 1];
+        if (part >= parts) return 0.0;
+        if (v.how == kRest) return rests[(int64_t)s * parts + part];
+        const Stat st = stats[(int64_t)v.row * parts + part];
+        return st.sum * power.exact((double)st.top - (double)v.p_top);
     };
-    const auto own_sum = [&]() {
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) sum += w[i];
-        return sum;
+    const int rounds = (parts + 63) / 64;
+    double total;
+    const auto add_up = [&] {
+        total = held[0] + held[1];
+        for (int i = kHeld; i < rounds; ++i) total += share(i);
+        total = wave_sum(total);
     };
-    double total = 0.0;
-    if (v.how == kRest) {
-        for (int i = threadIdx.x; i < parts; i += kPickThreads)
-            share[i] = rests[(int64_t)s * parts + i];
-        __syncthreads();
-        for (int i = 0; i < parts; ++i) total += share[i];
+    if (JUDGED && v.how == kRest) {
+        add_up();
         // rounding has left nothing above the draft's: all of p
         if (!(total > 0.0)) v.how = kPlain;
-        __syncthreads();
     }
     if (v.how != kRest) {
-        const Stat *st = stats + (int64_t)v.row * parts;
-        for (int i = threadIdx.x; i < parts; i += kPickThreads)
-            share[i] = st[i].sum > 0.0
-                           ? st[i].sum * exp2(((double)st[i].top - (double)v.p.top) * c)
-                           : 0.0;
-        __syncthreads();
-        if (v.how == kWithout) {
-            double sum;
-            weigh(v.draft / kPart);
-            before(own_sum(), sums, sum);
-            if (threadIdx.x == 0) share[v.draft / kPart] = sum;
-            __syncthreads();
-        }
-        total = 0.0;
-        for (int i = 0; i < parts; ++i) total += share[i];
-        if (v.how == kWithout && !(total > 0.0)) {  // the draft is all there is
-            if (threadIdx.x == 0) a.next[s] = v.draft;
-            return;
-        }
+        Parts of;
+        of.load(stats + (int64_t)v.row * parts, parts);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            held[i] = of.of[i].sum * power.exact((double)of.of[i].top - (double)v.p_top);
+        add_up();
     }
-    const double target = (double)a.uniform[2 * (int64_t)v.row + 1] * total;
+    if (v.how == kWithout && !(total > 0.0)) {
+        if (threadIdx.x == 0) a.next[s] = v.draft;
+        return;
+    }
     // the first part that passes the target, or the last that holds a token
-    int part = 0;
+    const double target = (double)v.u * total;
     double below = 0.0, run = 0.0;
-    for (int i = 0; i < parts; ++i) {
-        if (!(share[i] > 0.0)) continue;
-        part = i, below = run;
-        run += share[i];
-        if (run > target) break;
+    int part = 0;
+    for (int i = 0; i < rounds; ++i) {
+        const double x = share(i), sum = up_to(x);
+        const uint64_t holds = __ballot(x > 0.0);
+        const uint64_t over = __ballot(run + sum > target) & holds;
+        if (holds) {
+            const int at = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll(holds);
+            part = 64 * i + at;
+            below = run + (at ? lane_of(sum, at - 1) : 0.0);
+        }
+        if (over) break;
+        run += lane_of(sum, 63);
     }
-    if (threadIdx.x == 0) found = INT32_MAX, highest = -1;
-    weigh(part);
-    double all;
-    double at = below + before(own_sum(), sums, all);
+    // a thread's four neighbouring tokens, as weights
     const int first = part * kPart + threadIdx.x * kEach;
-    int mine = INT32_MAX, last = -1;
+    const f4_t l = load4<F16>(row_of<F16>(a.logits, v.row, a.stride), first, a.vocab);
+    f4_t g = l;
+    if (JUDGED && v.how == kRest)
+        g = load4<F16>(row_of<F16>(a.drafted, v.row, a.drafted_stride), first, a.vocab);
+    double w[kEach], mine = 0.0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        if (!(w[i] > 0.0)) continue;
-        at += w[i];
-        last = first + i;
-        if (mine == INT32_MAX && at > target) mine = first + i;
+        w[i] = power.exact((double)l[i] - (double)v.p_top);
+        if (JUDGED && v.how == kRest)
+            w[i] = above(w[i], v.p_share, power.exact((double)g[i] - (double)v.q_top), v.q_share);
+        if (v.how == kWithout && first + i == v.draft) w[i] = 0.0;
+        mine += w[i];
     }
-    if (mine != INT32_MAX) atomicMin(&found, mine);
-    if (last >= 0) atomicMax(&highest, last);
+    const double upto = up_to(mine);
+    if (lane == 63) sums[wave] = upto;
     __syncthreads();
-    if (threadIdx.x == 0) a.next[s] = found != INT32_MAX ? found : highest;
+    double at = below;
+    int taken = -1;  // the wave that passes the target
+    double start = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPickWaves; ++i) {
+        if (i == wave) start = at;
+        at += sums[i];
+        if (taken < 0 && sums[i] > 0.0 && at > target) taken = i;
+    }
+    int last = -1;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        if (w[i] > 0.0) last = first + i;
+    if (taken < 0) {  // none does: the highest token of the part
+        if (last >= 0) atomicMax(&highest, last);
+        __syncthreads();
+        if (threadIdx.x == 0) a.next[s] = highest;
+        return;
+    }
+    if (wave != taken) return;
+    // the first lane that passes it, and its first token that does (its last, where
+    // the sums' rounding leaves none)
+    const uint64_t holds = __ballot(last >= 0);
+    const uint64_t over = __ballot(start + upto > target) & holds;
+    const int lead = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll(holds);
+    if (lane != lead) return;
+    at = start + (upto - mine);
+    int token = last;
+#pragma unroll
+    for (int i = kEach; i-- > 0;) {
+        double sum = at;
+#pragma unroll
+        for (int e = 0; e <= i; ++e) sum += w[e];
+        if (w[i] > 0.0 && sum > target) token = first + i;
+    }
+    a.next[s] = token;
 }
 
 int parts_of(int64_t vocab) { return (int)((vocab + kPart - 1) / kPart); }
 
+// The workspace: stats, then (with draft logits) verdicts and rests.
+struct Shares {
+    size_t verdicts, rests, bytes;
+};
+Shares shares_of(int64_t n, int64_t batch, int64_t vocab, bool drafted) {
+    const size_t parts = (size_t)parts_of(vocab);
+    Shares sh = {(size_t)n * (drafted ? 2u : 1u) * parts * sizeof(Stat), 0, 0};
+    sh.rests = sh.verdicts + (drafted ? (size_t)batch * sizeof(Verdict) : 0);
+    sh.bytes = sh.rests + (drafted ? (size_t)batch * parts * sizeof(double) : 0);
+    return sh;
+}
+
 template <bool F16>
 hipError_t run(const VerifyArgs &a, void *ws, hipStream_t stream) {
     const int parts = parts_of(a.vocab);
+    const Shares sh = shares_of(a.n, a.batch, a.vocab, a.drafted != nullptr);
     const int64_t rows = (int64_t)a.n * (a.drafted ? 2 : 1);
     Stat *stats = (Stat *)ws;
-    double *rests = (double *)(stats + rows * parts);
-    hipLaunchKernelGGL((stats_kernel<F16>), dim3((uint32_t)(rows * parts)), dim3(kThreads), 0,
-                       stream, a, stats, parts);
-    if (a.drafted)
-        hipLaunchKernelGGL((rest_kernel<F16>), dim3((uint32_t)((int64_t)a.batch * parts)),
-                           dim3(kThreads), 0, stream, a, stats, rests, parts);
-    hipLaunchKernelGGL((pick_kernel<F16>), dim3((uint32_t)a.batch), dim3(kPickThreads), 0, stream,
-                       a, stats, rests, parts);
+    Verdict *verdicts = (Verdict *)((uint8_t *)ws + sh.verdicts);
+    double *rests = (double *)((uint8_t *)ws + sh.rests);
+    const int64_t cus = device_shape().cus;
+    const int64_t many = rows * ((parts + kWaves - 1) / kWaves);
+    const int64_t groups = (int64_t)a.batch * ((parts + kPickWaves - 1) / kPickWaves);
+    const dim3 batch((uint32_t)a.batch);
+    if (many <= 4 * cus)
+        hipLaunchKernelGGL((stats_kernel<F16, true>), dim3((uint32_t)many), dim3(kThreads), 0,
+                           stream, a, stats, parts);
+    else
+        hipLaunchKernelGGL((stats_kernel<F16, false>), dim3((uint32_t)many), dim3(kThreads), 0,
+                           stream, a, stats, parts);
+    if (!a.drafted) {
+        hipLaunchKernelGGL((pick_kernel<F16, false>), batch, dim3(kPickThreads), 0, stream, a,
+                           stats, nullptr, nullptr, parts);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(judge_kernel, batch, dim3(kPickThreads), 0, stream, a, stats, verdicts,
+                       parts);
+    hipLaunchKernelGGL((rest_kernel<F16>), dim3((uint32_t)groups), dim3(kPickThreads), 0, stream,
+                       a, verdicts, rests, parts);
+    hipLaunchKernelGGL((pick_kernel<F16, true>), batch, dim3(kPickThreads), 0, stream, a, stats,
+                       verdicts, rests, parts);
     return hipGetLastError();
 }
 
 }  // namespace
 
 size_t verify_workspace_bytes(int64_t n, int64_t batch, int64_t vocab, bool drafted) {
-    const size_t parts = (size_t)parts_of(vocab);
-    return (size_t)n * (drafted ? 2u : 1u) * parts * sizeof(Stat) +
-           (drafted ? (size_t)batch * parts * sizeof(double) : 0);
+    return shares_of(n, batch, vocab, drafted).bytes;
 }
 
 hipError_t launch_verify(const VerifyArgs &a, int x_f16, void *ws, hipStream_t stream) {

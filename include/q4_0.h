@@ -535,7 +535,7 @@ int q4_0_embed(const void *packed, const int32_t *tokens, int64_t n, int64_t out
  *   logits  : DEVICE [n] rows of vocab elements of x_dtype, `stride` apart.
  *   drafted : DEVICE rows likewise, or NULL.  Rows that judge nothing are not read.
  *   tokens  : DEVICE int32 [n], the step's own tokens (q4_0_embed's).  A draft outside
- *             [0, vocab) is refused, and nothing is taken from p for it.
+ *             [0, vocab) is refused (without `drafted` next is then drawn from p).
  *   q_start : DEVICE int32 [batch + 1], 0 <= q_start[s] <= q_start[s+1] <= n.  A
  *             conversation without rows gets accepted 0 and next -1.
  *   temperature : DEVICE float32 [batch], finite; or NULL: 1.
