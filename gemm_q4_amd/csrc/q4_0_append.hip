@@ -11,6 +11,13 @@
 // Bound by the bytes: 8191 tokens of 16 + 2 x 8 heads of 256, binary16, in
 // 56.5 us: 4.8 TB/s, where a copy of as many bytes reaches 4.8 to 5.4.  A single
 // token (32 + 2 x 8 heads of 128) takes 3.3 us, one launch.
+//
+// Into a cache of codes a row of K or V needs its largest magnitude, from the same
+// reduction over the group, and goes out as codes x / s rounded to even with s = max
+// |x| / 127.  That is bound by its arithmetic (the sines, and a correctly rounded
+// quotient an element): the 8191 tokens above, half of each head rotated, in 52 us,
+// 4.5 TB/s of its bytes (58 us with the library's division and sine); a single
+// token in 3.7 us.
 #include <float.h>
 
 #include "q4_0_device.h"
@@ -49,16 +56,45 @@ __device__ __forceinline__ void turn(int position, float inv_freq, float *s, flo
     sincosf((float)r, s, c);
 }
 
-// Four elements as codes of scale `s` (0: codes 0), one word.  The division is
-// rounded correctly, so a code is the nearest whole number of x / s in float32.
-__device__ __forceinline__ uint32_t codes_of(f4_t x, float s) {
-    uint32_t w = 0;
+// The same by quarter turns: what is left lies in [-pi/4, pi/4], where the series of
+// sine and cosine need five and six terms (2^-29 at most is left out).  A third of the
+// library function's operations, which an append in 8 bits, bound by its
+// arithmetic, has to spare; the binary16 append, bound by its bytes, has not.
+__device__ __forceinline__ void quarter_turn(int position, float inv_freq, float *s, float *c) {
+    const double angle = (double)position * (double)inv_freq;
+    const double magic = 6755399441055744.0;  // 1.5 2^52: the sum's low bits are the integer
+    const double k = fma(angle, 0.63661977236758134308, magic);
+    const double n = k - magic;
+    const float r =
+        (float)fma(-n, 6.123233995736766e-17, fma(-n, 1.5707963267948965580, angle));
+    const int q = (int)(uint32_t)__builtin_bit_cast(uint64_t, k);
+    const float z = r * r;
+    const float sn =
+        fmaf(r * z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f),
+                         -1.6666667e-1f), r);
+    const float cs = fmaf(
+        z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.7557319e-7f, 2.4801587e-5f), -1.3888889e-3f),
+                        4.1666667e-2f), -0.5f), 1.0f);
+    const float a = q & 1 ? cs : sn, b = q & 1 ? sn : cs;
+    *s = q & 2 ? -a : a;
+    *c = (q + 1) & 2 ? -b : b;
+}
+
+// Four elements as codes of scale `s`, one word; `r` is 1 / s, correctly rounded.
+// The quotient is the product with r corrected twice by its exact remainder, which
+// is the correctly rounded quotient (s is kept where no remainder is subnormal).  It
+// is rounded by an addition that leaves the whole number in the low bits.
+__device__ __forceinline__ uint32_t codes_of(f4_t x, float s, float r) {
+    uint32_t t[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int c = s > 0.0f ? (int)rintf(x[i] / s) : 0;
-        w |= (uint32_t)(c & 255) << (8 * i);
+        float q = x[i] * r;
+        q = fmaf(fmaf(-q, s, x[i]), r, q);
+        q = fmaf(fmaf(-q, s, x[i]), r, q);
+        t[i] = __builtin_bit_cast(uint32_t, q + 12582912.0f);
     }
-    return w;
+    return __builtin_amdgcn_perm(t[1], t[0], 0x0C0C0400u) |
+           __builtin_amdgcn_perm(t[3], t[2], 0x04000C0Cu);
 }
 
 template <bool XF16, bool QF16, bool CODES, int LPH>
@@ -81,7 +117,10 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int chun
         const int p = a.positions[t];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            turn(p, a.inv_freq[4 * j + i], &sn[i], &cs[i]);
+            if (CODES)
+                quarter_turn(p, a.inv_freq[4 * j + i], &sn[i], &cs[i]);
+            else
+                turn(p, a.inv_freq[4 * j + i], &sn[i], &cs[i]);
             sn[i] *= a.amplitude;
             cs[i] *= a.amplitude;
         }
@@ -165,8 +204,16 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int chun
             if (!kept) continue;
             const int64_t row = ((page * heads + hh) << shift) + off;
             uint8_t *dst = (uint8_t *)(is_v ? a.cache.v : a.cache.k) + row * dim;
-            *(uint32_t *)(dst + e0) = codes_of(x0, step);
-            *(uint32_t *)(dst + e1) = codes_of(x1, step);
+            float s = step;
+            if (s < 0x1p-60f) {  // (rarely) up to where remainders are exact
+                s *= 0x1p64f;
+                x0 *= 0x1p64f;
+                x1 *= 0x1p64f;
+            }
+            const bool fine = s > 0.0f;
+            const float r = fine ? 1.0f / s : 0.0f;
+            *(uint32_t *)(dst + e0) = fine ? codes_of(x0, s, r) : 0u;
+            *(uint32_t *)(dst + e1) = fine ? codes_of(x1, s, r) : 0u;
             if (j == 0) (is_v ? a.cache.v_scale : a.cache.k_scale)[row] = step;
         } else if (kept) {
             const int64_t o = (((page * heads + hh) << shift) + off) * dim;
@@ -189,7 +236,11 @@ hipError_t launch(const AppendArgs &a, hipStream_t stream) {
     // 7.4 and 6.7, 2048 tokens 19.6 and 17.4; 16 + 2 x 8 of 256, 256 tokens 5.7
     // and 6.5, 400 tokens 7.8 and 7.1; 64 + 2 x 8 of 64, 341 tokens 5.3 and 6.0,
     // 512 tokens 6.8 and 6.5.
-    const int chunks = a.n * all <= 1024 ? all : 1;
+    // In codes, where a row is more arithmetic: 32 + 2 x 8 heads of 128, 512 tokens 6.4
+    // and 6.6, 640 tokens 7.4 and 7.4, 1024 tokens 10.0 and 8.8; 16 + 2 x 8 of 256,
+    // 512 tokens 7.9 and 7.9, 640 tokens 9.2 and 9.0; 64 + 2 x 8 of 64, 640 tokens
+    // 6.8 and 6.9, 1024 tokens 9.2 and 8.1.
+    const int chunks = a.n * all <= (CODES ? 2048 : 1024) ? all : 1;
     hipLaunchKernelGGL((append_kernel<XF16, QF16, CODES, LPH>), dim3((uint32_t)(a.n * chunks)),
                        dim3(kThreads), 0, stream, a, chunks);
     return hipGetLastError();
@@ -211,7 +262,9 @@ hipError_t by_type(const AppendArgs &a, int x_f16, int q_f16, hipStream_t stream
 }
 
 // Rows of an 8-bit cache as numbers: a group of LPH lanes to a row, 8 codes to a
-// lane; K in one half of the grid's second dimension, V in the other.
+// lane; K in one half of the grid's second dimension, V in the other.  Bound by the
+// bytes it writes: 8191 tokens of 2 x 8 heads of 256 as binary16 (67 MB, and 35 MB
+// read) in 21 us, 4.8 TB/s.
 template <bool YF16, int LPH>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
     constexpr int kGroups = kThreads / LPH;
