@@ -18,8 +18,17 @@
 // are taken as 0 and their codes are finite whatever they are, so what a page
 // holds past its conversation's end never meets the arithmetic.
 //
-// Scores keep their own units: a weight is exp2((x - m) c), the difference first,
-// so that scores of any size lose nothing.
+// A score is formed less the running maximum, by one fused operation on its product:
+// scores of any size lose nothing, and while the maximum holds its exponential
+// follows at once.  Scores of binary16 rows are in powers of two (K's scales carry
+// the factor, the same for all rows); float32 rows have a factor `c` of their own.
+//
+// Measured (32 + 8 heads of 128, binary16 rows, the rates of the bytes or operations
+// that the call cannot do without): one conversation of 448 keys 9.4 us, a chain of
+// lengths, page table, keys and the join of the parts; of 131072 keys 53 us, 5.2
+// TB/s (91 us over binary16); 64 conversations of 400 to 8192 keys, one to five
+// tokens each, 120 us, 4.0 TB/s; two prompts of 5001 and 1800 tokens 321 us, 720
+// TFLOP/s.
 #include "q4_0_attention.h"
 #include "q4_0_dma.h"
 
@@ -134,6 +143,13 @@ struct Source {
 // 16 b + 4 (l / 16) + 0..3 in lane l, and the weights of two such blocks are as they
 // lie the B operand of O^T = V^T P^T, whose A operand (eight keys of one column
 // to a lane) the transposing 8-bit LDS read delivers from row-major V.
+//
+// Bound by the bytes: 6 to 6.7 TB/s while the keys stream.  What keeps a call from that
+// as a whole is the chain before the first key (4 to 5 us), the join (5 us), and, with
+// conversations of several lengths, the slots that end early.  64 keys a tile: the
+// scales of 64 are one copy of 4 bytes to a lane.  Up to 32 rows: 64 rows to a wave
+// (which leaves one wave to a SIMD) took 200 instead of 158 us for 16 conversations
+// of 8192 keys, eight tokens of 8 heads each.
 constexpr int kStepRows = 32, kStepKeys = 64;
 
 // Codes in LDS are rows of DIM bytes, their 16-byte pieces XOR-swizzled: sixteen
@@ -163,6 +179,8 @@ template <int DIM> struct StepFiller : Source {
                 off[g][j] = row * DIM + ((lane % (DIM / 16)) ^ swz8<DIM>(16 * g + row)) * 16;
             }
     }
+    // ONCE: no other tile reads these keys, and the copies carry the non-temporal hint.
+    template <bool ONCE>
     __device__ __forceinline__ void fill(const Reach<kStepKeys> &r, const int (&page)[4], int key,
                                          uint8_t *lds, bool is_v) const {
         const int lane = threadIdx.x % 64;
@@ -171,8 +189,12 @@ template <int DIM> struct StepFiller : Source {
         for (int g = 0; g < 4; ++g) {
             const uint8_t *src = (is_v ? v : k) + row(page[g], key + 16 * g) * DIM;
 #pragma unroll
-            for (int j = 0; j < kCopies; ++j)
-                dma16_once_at(src, off[g & 1][j], dst + g * 16 * DIM + j * 1024);
+            for (int j = 0; j < kCopies; ++j) {
+                if (ONCE)
+                    dma16_once_at(src, off[g & 1][j], dst + g * 16 * DIM + j * 1024);
+                else
+                    dma16_at(src, off[g & 1][j], dst + g * 16 * DIM + j * 1024);
+            }
         }
         // the lane's own page, chosen among copies (an identity move): the pages
         // themselves stay in scalar registers, as the copies' bases have to
@@ -184,16 +206,17 @@ template <int DIM> struct StepFiller : Source {
     }
 };
 
-// A block of 16 rows: queries, running maximum (of scores without `c`), sum (this
-// lane's keys) and unnormalised result.  Weights are held in two binary16 parts,
-// as 2^kShift of the largest.
+// A block of 16 rows: queries, running maximum (of scores without `c`; 0 before the
+// first), sum (this lane's keys) and unnormalised result.  A score above the maximum
+// by more than `over` lifts it (any does, the first time).  Weights are held in two
+// binary16 parts, as 2^kShift of the largest.
 template <int DIM, bool F32> struct Block {
-    static constexpr int kParts = F32 ? 2 : 1;
+    static constexpr int kParts = F32 ? 2 : 1;  // of q
     static constexpr float kLag = 1.0f;
     static constexpr int kShift = 14;
     h8_t q[kParts][DIM / 32];
     f4_t o[DIM / 16];
-    float m, l, c;
+    float m, l, c, over;
     int p, lo;
 
     struct Raw {
@@ -208,7 +231,7 @@ template <int DIM, bool F32> struct Block {
         const int token = rr / group;
         p = position(a, position0, token);
         lo = a.window && p >= a.window ? p - a.window + 1 : 0;
-        c = finite(a.scale * kLog2e);
+        c = F32 ? finite(a.scale * kLog2e) : 1.0f;
         const int64_t at = (int64_t)(pl.first + token) * a.q_stride +
                            (int64_t)(hk * group + rr % group) * DIM + 16 * g;
         const u4_t *src = (const u4_t *)((const uint8_t *)a.q + at * (F32 ? 4 : 2));
@@ -219,7 +242,8 @@ template <int DIM, bool F32> struct Block {
                 raw.x[j * 2 * kParts + x] = src[j * (F32 ? 16 : 8) + x];
     }
     __device__ __forceinline__ void clear() {
-        m = -INFINITY;
+        m = 0.0f;
+        over = -INFINITY;
         l = 0.0f;
 #pragma unroll
         for (int d = 0; d < DIM / 16; ++d) o[d] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -260,8 +284,7 @@ template <int DIM, bool F32> struct Block {
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[d][i] *= f;
     }
-    // Scores of 64 keys to exp(x - m), the maximum brought along; a set bit of
-    // `hidden` is a score whose key the row does not see.
+    // Scores of 64 keys, less the maximum, to weights; the maximum brought along.
     __device__ __forceinline__ void soften(f4_t (&s)[4]) {
         float top = -INFINITY;
 #pragma unroll
@@ -269,47 +292,58 @@ template <int DIM, bool F32> struct Block {
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
         top = quads_max(top);
-        if (__any((top - m) * c > kLag)) {
-            const float mn = fmaxf(m, top);
-            const float f = mn == -INFINITY ? 1.0f : factor_of((m - mn) * c);
-            m = mn;
+        if (__any(top * c > over)) {
+            const bool first = over == -INFINITY;
+            const float to = m + (first ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f));
+            const float up = to - m;
+            const float f = first ? 1.0f : factor_of(-up * c);
+            if (top != -INFINITY) over = kLag;
+            m = to;
             l *= f;
             rescale(f);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[b][i] -= up;
         }
-        const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[b][i] = __builtin_amdgcn_exp2f((s[b][i] - base) * c);
+                s[b][i] = __builtin_amdgcn_exp2f(F32 ? s[b][i] * c : s[b][i]);
                 l += s[b][i];
             }
     }
+    // The maximum in powers of two, minus infinity if there was none.
+    __device__ __forceinline__ float top() const { return over == -INFINITY ? over : m * c; }
 };
 
-template <int DIM, bool F32, int NR>
+//
+// One tile's room to a wave: K is requested again as soon as the scores are formed, V
+// as soon as it is mixed, and the other waves cover what that leaves open.
+template <int DIM, bool F32, bool ONCE, int NR>
 __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFiller<DIM> &f,
                                           const Reach<kStepKeys> &r, int t, int t1, int stride,
-                                          int top_lo, uint8_t *lds, int (&look)[4], int &top) {
+                                          int top_lo, uint8_t *lds, int (&look)[4], int &top,
+                                          float k_factor) {
     using B = Block<DIM, F32>;
     constexpr int kAll = StepFiller<DIM>::kAll, kCodes = StepFiller<DIM>::kCodes;
     const int lane = threadIdx.x % 64, g = lane / 16;
-    const uint8_t *vbuf = lds + kCodes;
-    const float *ksc = (const float *)(lds + 2 * kCodes);
-    float *vsc = (float *)(lds + 2 * kCodes) + kStepKeys;
     // lane i of 16 names the address of half a piece of the (i / 2)-th of its
     // eight keys and receives column i of all eight
     const int i2 = lane % 16 / 2;
     const int vkey = (i2 < 4 ? 4 * g + i2 : 12 + 4 * g + i2);
-    const uint8_t *vrow = vbuf + vkey * DIM + 8 * (lane % 2);
+    const uint8_t *vrow = lds + kCodes + vkey * DIM + 8 * (lane % 2);
+    float *ksc = (float *)(lds + 2 * kCodes);
+    float *vsc = ksc + kStepKeys;
     int i = 0;  // the tile's lane in look
     for (; t < t1; t += stride) {
         const int k0 = r.key(t), next = r.key(t + stride);
         const bool more = t + stride < t1, masked = !r.all(k0, kStepKeys, top_lo);
         f4_t s[NR][4];
-        // outstanding: K, then V
-        Q4_WAIT_VMCNT(kAll);
+        Q4_WAIT_VMCNT(kAll);  // outstanding: K, then V
         asm volatile("" ::: "memory");
+        const float k_mine = ksc[lane];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
 #pragma unroll
@@ -331,14 +365,20 @@ __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFi
                     }
             }
         }
+        // an infinite scale is no number either
+        if (__builtin_expect(__any(fabsf(k_mine) == INFINITY), 0)) {
+            if (fabsf(k_mine) == INFINITY) ksc[lane] = NAN;
+            Q4_WAIT_LGKM0();
+            asm volatile("" ::: "memory");
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const f4_t x = *(const f4_t *)(ksc + 16 * b + 4 * g);
+            f4_t x = *(const f4_t *)(ksc + 16 * b + 4 * g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float none = x[e] * 0.0f;  // an infinite scale is no number either
+                if (!F32) x[e] *= k_factor;
 #pragma unroll
-                for (int n = 0; n < NR; ++n) s[n][b][e] = fmaf(s[n][b][e], x[e], none);
+                for (int n = 0; n < NR; ++n) s[n][b][e] = fmaf(s[n][b][e], x[e], -w[n].m);
             }
         }
         uint32_t hidden[NR];
@@ -369,7 +409,7 @@ __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFi
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) page[x] = __builtin_amdgcn_readlane(look[x], i);
-            f.fill(r, page, next, lds, false);
+            f.template fill<ONCE>(r, page, next, lds, false);
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n) w[n].soften(s[n]);
@@ -439,16 +479,16 @@ __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFi
         }
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
-        if (more) f.fill(r, page, next, lds, true);
+        if (more) f.template fill<ONCE>(r, page, next, lds, true);
     }
 }
 
 // One tile of up to 16 NR rows by a workgroup of W waves.
-template <int DIM, bool F32, int W, int NR>
+template <int DIM, bool F32, bool ONCE, int W, int NR>
 __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl, const Place &at,
                                           int hk, int split, int row0, int row1, uint8_t *lds,
                                           float (*ml)[W][kStepRows]) {
-    constexpr int kPitch = DIM + 4, kShare = 32 * kPitch * 4;
+    constexpr int kPitch = DIM + 4, kShare = kStepRows * kPitch * 4;
     static_assert(2 * StepFiller<DIM>::kCodes + 2 * kStepKeys * 4 <= kShare && kShare % 256 == 0,
                   "a wave's tile, later its rows");
     const int position0 = at.kv - at.rows / pl.group;
@@ -478,8 +518,8 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
             int page[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) page[x] = __builtin_amdgcn_readlane(look[x], 0);
-            f.fill(r, page, r.key(t), mine, false);
-            f.fill(r, page, r.key(t), mine, true);
+            f.template fill<ONCE>(r, page, r.key(t), mine, false);
+            f.template fill<ONCE>(r, page, r.key(t), mine, true);
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n) w[n].take(raw[n]);
@@ -487,12 +527,13 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
         for (int n = 0; n < NR; ++n) w[n].clear();
     }
     int top = kNoExponent;
-    step_loop<DIM, F32, NR>(w, f, r, t, t1, W, top_lo, mine, look, top);
+    step_loop<DIM, F32, ONCE, NR>(w, f, r, t, t1, W, top_lo, mine, look, top,
+                                   finite(a.scale * kLog2e));
     // join the waves
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         w[n].l = quads_sum(w[n].l);
-        w[n].m = w[n].m * w[n].c;  // in powers of two
+        w[n].m = w[n].top();
         if (g == 0) {
             ml[0][wave][16 * n + lane] = w[n].m;
             ml[1][wave][16 * n + lane] = w[n].l;
@@ -541,10 +582,11 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
     }
 }
 
-template <int DIM, bool F32, int W>
+// ONCE: a conversation's rows are one tile, most likely.
+template <int DIM, bool F32, bool ONCE, int W>
 __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(AttentionArgs a, Plan pl,
                                                                          int base) {
-    __shared__ __align__(1024) uint8_t lds[W * 32 * (DIM + 4) * 4];
+    __shared__ __align__(1024) uint8_t lds[W * kStepRows * (DIM + 4) * 4];
     __shared__ float ml[2][W][kStepRows];
     const int hk = blockIdx.x, split = blockIdx.y;
     const Place at = find_tile<kStepRows>(a, pl.group, base + blockIdx.z);
@@ -552,9 +594,9 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Attenti
     if (row0 < 0 || row0 >= at.rows) return;
     const int row1 = min(row0 + kStepRows, at.rows);
     if (row1 - row0 <= 16)
-        step_tile<DIM, F32, W, 1>(a, pl, at, hk, split, row0, row1, lds, ml);
+        step_tile<DIM, F32, ONCE, W, 1>(a, pl, at, hk, split, row0, row1, lds, ml);
     else
-        step_tile<DIM, F32, W, 2>(a, pl, at, hk, split, row0, row1, lds, ml);
+        step_tile<DIM, F32, ONCE, W, 2>(a, pl, at, hk, split, row0, row1, lds, ml);
 }
 
 // ---- many rows: waves of 32 rows share each key tile ------------------------
@@ -564,8 +606,21 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Attenti
 // the other of two stages while this one is worked on, and read there by all RW
 // waves.  Both products are v_mfma_f32_32x32x16_f16 on transposed scores; weights of
 // binary16 rows are rounded once, of float32 rows held in two parts.
-template <int DIM, int RW, int KW> struct Pass {
-    static constexpr int KT = 16 * RW;
+//
+// Bound by vector instructions: 384 and 64 exponentials to 64 keys of 32 rows, 63% of
+// the time, with the matrix cores busy for 31%; two waves to a SIMD overlap them but
+// little.  What brought them down: codes converted once for all waves (they were half
+// of the instructions when each wave converted its own), scores less the running
+// maximum by one fused operation, no rescaling while the maximum lags by less than
+// 2^8.  Eight waves on a key tile, which halves the conversions again, gained
+// nothing (two prompts of 5001 and 3146 tokens 406 us, four waves 397).
+//
+// Every wave brings 16 keys of K and V; wide float32 rows, whose registers are few,
+// take half as many keys a tile, and a wave brings 16 of K or of V (44 prompts of 356
+// tokens, 16 + 4 heads of 256: 343 us, with whole tiles 517).
+template <int DIM, bool F32, int RW, int KW> struct Pass {
+    static constexpr bool kBoth = !(DIM > 128 && F32 && RW > 2);
+    static constexpr int KT = kBoth ? 16 * RW : 8 * RW;
     static constexpr int kTile = KT * DIM * 2;
     static constexpr int kPitch = DIM + 4, kShare = 32 * kPitch * 4;
     static constexpr int kStages = KW * 4 * kTile;
@@ -574,13 +629,23 @@ template <int DIM, int RW, int KW> struct Pass {
     static constexpr int kWavesPerSimd = DIM > 128 ? 1 : 2;
 };
 
+// Where 16-byte piece `piece` of a staged key row lies: eight lanes of a wave write the
+// even pieces of one row, then the odd ones, and eight others those of the next row,
+// so the rows' places differ in parity (or the halves of a 512-byte row's); both
+// kinds of reads touch every bank once, as with swz().
+template <int DIM> __device__ __forceinline__ int place(int key, int piece) {
+    if (DIM == 64) return piece ^ ((((key >> 1) & 1) << 2) | (((key >> 2) ^ (key >> 1)) & 1) | ((key >> 2) & 2));
+    const int low = DIM == 128 ? ((key >> 2) & 3) ^ (key & 1) : (key >> 2) & 3;
+    return piece ^ (((key & 3) << 2) | low) ^ (DIM == 256 ? (piece >> 4) & 1 : 0);
+}
+
 // Scales of a stage: of K, of V (against 2^top), and top.
-template <int KT> struct Scales {
+template <int KT> struct alignas(16) Scales {
     float k[KT], v[KT];
     int top;
 };
 
-// One wave's 32 rows.
+// One wave's 32 rows, as a Block's.
 template <int DIM, bool F32> struct Rows {
     static constexpr int kParts = F32 ? 2 : 1;
     // weights as 2^kShift of the largest, which may lag behind by kLag (powers of two)
@@ -588,7 +653,7 @@ template <int DIM, bool F32> struct Rows {
     static constexpr int kShift = F32 ? 14 : 7;
     h8_t q[kParts][DIM / 16];
     f16x_t o[DIM / 32];
-    float m, l, c;
+    float m, l, c, over;
     int p, lo;
 
     struct Raw {
@@ -601,7 +666,7 @@ template <int DIM, bool F32> struct Rows {
         const int token = rr / group;
         p = position(a, position0, token);
         lo = a.window && p >= a.window ? p - a.window + 1 : 0;
-        c = finite(a.scale * kLog2e);
+        c = F32 ? finite(a.scale * kLog2e) : 1.0f;
         const int64_t at = (int64_t)(pl.first + token) * a.q_stride +
                            (int64_t)(hk * group + rr % group) * DIM + 8 * half;
         const u4_t *src = (const u4_t *)((const uint8_t *)a.q + at * (F32 ? 4 : 2));
@@ -609,7 +674,8 @@ template <int DIM, bool F32> struct Rows {
         for (int s = 0; s < DIM / 16; ++s)
 #pragma unroll
             for (int x = 0; x < kParts; ++x) raw.x[s * kParts + x] = src[s * (F32 ? 4 : 2) + x];
-        m = -INFINITY;
+        m = 0.0f;
+        over = -INFINITY;
         l = 0.0f;
 #pragma unroll
         for (int d = 0; d < DIM / 32; ++d)
@@ -653,6 +719,7 @@ template <int DIM, bool F32> struct Rows {
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] *= f;
     }
+    __device__ __forceinline__ float top() const { return over == -INFINITY ? over : m * c; }
     // One tile: binary16 codes of K and V in LDS, and its scales.
     template <int KT>
     __device__ __forceinline__ void step(const uint8_t *kbuf, const uint8_t *vbuf,
@@ -667,7 +734,7 @@ template <int DIM, bool F32> struct Rows {
             const uint8_t *row = kbuf + (t * 32 + key) * DIM * 2;
 #pragma unroll
             for (int d = 0; d < DIM / 16; ++d) {
-                const h8_t k = *(const h8_t *)(row + (((2 * d + half) ^ swz<DIM>(key)) * 16));
+                const h8_t k = *(const h8_t *)(row + place<DIM>(key, 2 * d + half) * 16);
 #pragma unroll
                 for (int x = 0; x < kParts; ++x)
                     s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[x][d], s[t], 0, 0, 0);
@@ -679,7 +746,7 @@ template <int DIM, bool F32> struct Rows {
             for (int i = 0; i < 16; i += 4) {
                 const f4_t x = *(const f4_t *)(sc.k + t * 32 + 2 * i + 4 * half);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][i + e] *= x[e];
+                for (int e = 0; e < 4; ++e) s[t][i + e] = fmaf(s[t][i + e], x[e], -m);
             }
         uint32_t hidden = 0;
         if (masked) {
@@ -699,14 +766,20 @@ template <int DIM, bool F32> struct Rows {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
         top = halves_max(top);
-        if (__any((top - m) * c > kLag)) {
-            const float mn = fmaxf(m, top);
-            const float f = mn == -INFINITY ? 1.0f : factor_of((m - mn) * c);
-            m = mn;
+        if (__any(top * c > over)) {
+            const bool first = over == -INFINITY;
+            const float to = m + (first ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f));
+            const float up = to - m;
+            const float f = first ? 1.0f : factor_of(-up * c);
+            if (top != -INFINITY) over = kLag;
+            m = to;
             l *= f;
             rescale(f);
+#pragma unroll
+            for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[t][i] -= up;
         }
-        const float base = m == -INFINITY ? 0.0f : m;
         h8_t w[KT / 16][kParts];
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t)
@@ -715,7 +788,7 @@ template <int DIM, bool F32> struct Rows {
                 const f4_t x = *(const f4_t *)(sc.v + t * 32 + 2 * i + 4 * half);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float y = __builtin_amdgcn_exp2f((s[t][i + e] - base) * c);
+                    const float y = __builtin_amdgcn_exp2f(F32 ? s[t][i + e] * c : s[t][i + e]);
                     l += y;
                     s[t][i + e] = y * x[e];
                 }
@@ -746,9 +819,9 @@ template <int DIM, bool F32> struct Rows {
 #pragma unroll
             for (int d = 0; d < DIM / 32; ++d) {
                 const s4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s4_t)(r0 + ((4 * d + piece) ^ swz<DIM>(key)) * 16));
+                    (lds_s4_t)(r0 + place<DIM>(key, 4 * d + piece) * 16));
                 const s4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s4_t)(r1 + ((4 * d + piece) ^ swz<DIM>(key + 8)) * 16));
+                    (lds_s4_t)(r1 + place<DIM>(key + 8, 4 * d + piece) * 16));
                 const h8_t v = __builtin_bit_cast(
                     h8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
@@ -760,15 +833,16 @@ template <int DIM, bool F32> struct Rows {
 };
 
 template <int DIM, bool F32, int RW, int KW>
-__global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
-                             (Pass<DIM, RW, KW>::kWavesPerSimd)) void pass_kernel(AttentionArgs a,
+__global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
+                             (Pass<DIM, F32, RW, KW>::kWavesPerSimd)) void pass_kernel(AttentionArgs a,
                                                                                   Plan pl,
                                                                                   int base) {
-    using P = Pass<DIM, RW, KW>;
+    using P = Pass<DIM, F32, RW, KW>;
     using W = Rows<DIM, F32>;
+    constexpr bool kBoth = P::kBoth;
     constexpr int KT = P::KT, kTile = P::kTile, R = 32 * RW, kLoads = DIM / 64;
     __shared__ __align__(1024) uint8_t lds[P::kLds];
-    __shared__ __align__(16) Scales<KT> scales[2][KW];
+    __shared__ Scales<KT> scales[2][KW];
     __shared__ float ml[2][KW][R];
     const int hk = blockIdx.x, split = blockIdx.y;
     Place at = find_tile<R>(a, pl.group, base + blockIdx.z);
@@ -798,34 +872,39 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
     const Source f(a, at.s, hk);
     uint8_t *stages = lds + kw * 4 * kTile;
     const auto key_of = [&](int i) { return r.key(t0 + kw + i * KW); };
-    // a tile's loads: this wave's 16 rows of K and V, and the scales of V (first
-    // wave) or K (second), a key to a lane
+    // a tile's loads: this wave's 16 rows of K and V (or of one of them, in kx), and the
+    // scales of V (first wave) or K (second), a key to a lane
+    const int group = rw % (KT / 16);
     u4_t kx[kLoads], vx[kLoads];
     float sx = 0.0f;
     const auto look = [&](int i) { return f.look(key_of(min(i, tiles - 1)) + lane % KT); };
     const auto load = [&](int i, int pages) {
-        const int k0 = key_of(i), k = k0 + 16 * rw;
-        const int64_t at16 = f.row(__builtin_amdgcn_readlane(pages, 16 * rw), k) * DIM + lane * 16;
+        const int k0 = key_of(i), k = k0 + 16 * group;
+        const int64_t at16 =
+            f.row(__builtin_amdgcn_readlane(pages, 16 * group), k) * DIM + lane * 16;
+        const uint8_t *src = kBoth || rw < KT / 16 ? f.k : f.v;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            kx[j] = *(const u4_t *)(f.k + at16 + j * 1024);
-            vx[j] = *(const u4_t *)(f.v + at16 + j * 1024);
+            kx[j] = *(const u4_t *)(src + at16 + j * 1024);
+            if (kBoth) vx[j] = *(const u4_t *)(f.v + at16 + j * 1024);
         }
         if (rw < 2) sx = *(const float *)f.scale(r, pages, k0 + lane % KT, rw == 0);
     };
+    const float k_factor = F32 ? 1.0f : finite(a.scale * kLog2e);
     int lifted = kNoExponent;  // the running exponent, of the wave that stages V's scales
     const auto stage = [&](int i) {
-        uint8_t *dst = stages + (i & 1) * 2 * kTile;
+        uint8_t *dst = stages + (i & 1) * 2 * kTile + (kBoth || rw < KT / 16 ? 0 : kTile);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int key = 16 * rw + j * (1024 / DIM) + lane / (DIM / 16);
+            const int key = 16 * group + j * (1024 / DIM) + lane / (DIM / 16);
             const int piece = lane % (DIM / 16) * 2;
-            uint8_t *to = dst + key * DIM * 2;
-            *(h8_t *)(to + ((piece ^ swz<DIM>(key)) * 16)) = codes8(kx[j][0], kx[j][1]);
-            *(h8_t *)(to + (((piece + 1) ^ swz<DIM>(key)) * 16)) = codes8(kx[j][2], kx[j][3]);
-            to += kTile;
-            *(h8_t *)(to + ((piece ^ swz<DIM>(key)) * 16)) = codes8(vx[j][0], vx[j][1]);
-            *(h8_t *)(to + (((piece + 1) ^ swz<DIM>(key)) * 16)) = codes8(vx[j][2], vx[j][3]);
+            uint8_t *even = dst + key * DIM * 2 + place<DIM>(key, piece) * 16;
+            uint8_t *odd = dst + key * DIM * 2 + place<DIM>(key, piece + 1) * 16;
+            *(h8_t *)even = codes8(kx[j][0], kx[j][1]);
+            *(h8_t *)odd = codes8(kx[j][2], kx[j][3]);
+            if (!kBoth) continue;
+            *(h8_t *)(even + kTile) = codes8(vx[j][0], vx[j][1]);
+            *(h8_t *)(odd + kTile) = codes8(vx[j][2], vx[j][3]);
         }
         Scales<KT> &sc = scales[i & 1][kw];
         if (rw == 0) {
@@ -834,7 +913,7 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
             if (lane < KT) sc.v[lane] = relative(sx, lifted, W::kShift);
             if (lane == 0) sc.top = lifted;
         } else if (rw == 1 && lane < KT) {
-            sc.k[lane] = fabsf(sx) <= FLT_MAX ? sx : NAN;
+            sc.k[lane] = fabsf(sx) <= FLT_MAX ? sx * k_factor : NAN;
         }
     };
     int pages = -1;
@@ -872,7 +951,7 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             w.o[d][i] = __builtin_amdgcn_ldexpf(w.o[d][i], top - W::kShift);
-    float l = halves_sum(w.l), m = w.m * w.c;
+    float l = halves_sum(w.l), m = w.top();
     if (KW > 1) {
         // join the groups: the first takes over its rows' sum
         if (lane < 32) ml[0][kw][mine] = m, ml[1][kw][mine] = l;
@@ -935,10 +1014,77 @@ __global__ __launch_bounds__((Pass<DIM, RW, KW>::kThreads),
                         w.p >= 0);
 }
 
+// ---- joining the parts of many rows -----------------------------------------
+// A wave to a row, where there are rows enough to fill the device that way: the
+// parts' maxima and sums in its lanes, then the rows' elements, four to a lane, the
+// parts dealt to the lanes that a row leaves free.
+template <int DIM, bool F32>
+__global__ __launch_bounds__(256) void join_rows_kernel(AttentionArgs a, Plan pl) {
+    constexpr int kCols = DIM / 4, kGroups = 64 / kCols;
+    const int lane = threadIdx.x % 64;
+    const int64_t rows = (int64_t)a.n * a.q_heads;
+    const int64_t row = uniform((int)(blockIdx.x * 4 + threadIdx.x / 64));
+    if (row >= rows) return;
+    const int token = (int)(row / a.q_heads);
+    float m = -INFINITY, l = 0.0f;
+    if (lane < pl.splits) {
+        const float *ml = pl.part_ml + (lane * rows + row) * 2;
+        m = ml[0], l = ml[1];
+    }
+    constexpr int kAhead = 4;
+    f4_t ahead[kAhead];
+    const float *src = pl.part + row * DIM + lane % kCols * 4;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int part = lane / kCols + i * kGroups;
+        if (part < pl.splits) ahead[i] = *(const f4_t *)(src + part * rows * DIM);
+    }
+    const int s = find_last(a.batch, [&](int i) { return a.q_start[i] <= token; });
+    const meta_t qs = meta(a.q_start);
+    const int begin = min(max(qs[s], 0), a.n), end = min(max(qs[s + 1], begin), a.n);
+    if (token < begin || token >= end) return;
+    const bool sees = max(meta(a.kv_len)[s], 0) - end + token >= 0;
+    float top = m;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i));
+    // a part that saw none of the row's keys wrote no elements: marked by -1
+    const bool used = m != -INFINITY || l != 0.0f;
+    const float f = used ? factor_of(m - (top == -INFINITY ? 0.0f : top)) : -1.0f;
+    l = used ? l * f : 0.0f;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) l += __shfl_xor(l, i);
+    f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int rounds = (pl.splits + kGroups - 1) / kGroups;
+    for (int i = 0; i < rounds; ++i) {
+        const int part = lane / kCols + i * kGroups;
+        const float g = __shfl(f, min(part, 63));
+        if (part >= pl.splits || g == -1.0f) continue;
+        f4_t v;
+        if (i == 0)
+            v = ahead[0];
+        else if (i == 1)
+            v = ahead[1];
+        else if (i == 2)
+            v = ahead[2];
+        else if (i == 3)
+            v = ahead[3];
+        else
+            v = *(const f4_t *)(src + part * rows * DIM);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += v[e] * g;
+    }
+#pragma unroll
+    for (int i = kCols; i < 64; i <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], i);
+    if (lane < kCols) put_y4<F32>(a, row, DIM, 4 * lane, o, l, sees);
+}
+
 // ---- choices on the host ----------------------------------------------------
 struct Choice {
     int rows;   // of a tile: 32 (every wave on its own keys), 64 or 128 (waves share them)
     int waves;  // of a 32-row workgroup
+    bool once;  // a conversation's rows are one such tile, likely
     int64_t tiles;
     int splits;
     int least;  // key tiles of a part, at least
@@ -952,10 +1098,23 @@ Choice choose(const AttentionArgs &a) {
     const int dim = a.cache.dim, heads = a.cache.heads;
     const int64_t rows = (int64_t)a.n * (a.q_heads / heads);
     const int64_t cus = device_shape().cus;
-    if (rows <= (int64_t)kStepRows * a.batch)
-        ch.rows = 32;
+    // 32-row tiles where one holds a conversation's rows: it reads each key once.
+    // With more rows 128-row tiles, if that gives every compute unit one.  Between
+    // them 32-row tiles again, as long as one and a half times as many as there are
+    // compute units do (two run on each at once): the conversation's tiles read its
+    // keys side by side, from L2.  Else 64-row tiles, whose waves share them.  32- and
+    // 64-row tiles (us; 32 + 8 heads of 128, binary16): 16 conversations of 8192 keys, 16
+    // new tokens each, 107 and 160; one of 131072, 32 new tokens, 162 and 242; 256 new
+    // tokens of 4112 51 and 67; 512 of 4112 80 and 67, 512 of 512 17.4 and 16.1.  The
+    // rule takes a few short calls from the wrong side: 64 of 4112 25.8 and 21.6, four
+    // times 32 of 2048 (heads of 64) 21.8 and 17.1.
+    const bool one = rows <= (int64_t)kStepRows * a.batch;
+    const bool few = 2 * (rows / 32 + a.batch) * heads <= 3 * cus;
+    if (!one && (rows / 128 + (a.batch + 1) / 2) * heads >= cus)
+        ch.rows = 128;
     else
-        ch.rows = (rows / 128 + (a.batch + 1) / 2) * heads >= cus ? 128 : 64;
+        ch.rows = one || few ? 32 : 64;
+    ch.once = one;
     const int R = ch.rows;
     ch.tiles = rows / R + a.batch;
     // the items that are likely to have work: not all tiles do
@@ -963,6 +1122,7 @@ Choice choose(const AttentionArgs &a) {
                                    : (rows / R > a.batch ? rows / R : a.batch)) *
                            heads;
     // the key tiles a row tile can have at most
+    // (128-row tiles are never split: their key tiles are not counted)
     const int KT = R == 64 ? 32 : 64;
     int64_t keys = (int64_t)a.table_stride << a.cache.page_shift;
     if (a.window) {
@@ -978,12 +1138,22 @@ Choice choose(const AttentionArgs &a) {
     } else {
         // workgroups that run at once: two to a compute unit, four of 64-wide heads
         const int64_t slots = cus * (dim > 64 ? 2 : 4);
-        splits = ((a.batch == 1 ? 1 : 4) * slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
+        // As many parts as run at once, of what gives every slot one or 1024 keys if
+        // that is more; none where the conversations alone fill the device.  Four
+        // times as many, so that long conversations do not end alone, gain less
+        // than writing and joining parts costs: 128 conversations of 100 to 2048
+        // keys, one token each, 63 us so and 78 us, four tokens each 69 and 91; 16
+        // of 8192, eight tokens of 64 heads each, 95 and 116; 64 of 400 to 8192
+        // keys (heads of 64) 78 and 90, (heads of 128, one to five tokens) 131 and
+        // 135; only one token each of the same 121 and 113.  Parts of 512, 1024 and
+        // 2048 keys at least: 48 conversations of 200 to 4096 keys 53, 56 and 62; 24
+        // of 800 to 16384 99, 99 and 101; others alike.
+        splits = (slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
         const int64_t fair = (most * likely + slots - 1) / slots;
         ch.least = fair > 16 ? 16 : fair < ch.waves ? ch.waves : (int)fair;
         // too few keys to split: the workgroup's own waves take them, eight
         // (four) instead of four (two) while there are units to spare
-        if (most / ch.least < 2 && likely <= cus) ch.waves *= 2;
+        if (ch.once && most / ch.least < 2 && likely <= cus) ch.waves *= 2;
     }
     if (splits > most / ch.least) splits = most / ch.least;
     if (splits > kMaxSplits) splits = kMaxSplits;
@@ -1011,16 +1181,25 @@ hipError_t run(const AttentionArgs &a, const Choice &ch, const Plan &pl, hipStre
         else if (ch.rows == 64)
             hipLaunchKernelGGL((pass_kernel<DIM, F32, 2, W>), grid, dim3(128 * W), 0, stream, a,
                                pl, (int)base);
-        else if (ch.waves == W)
-            hipLaunchKernelGGL((step_kernel<DIM, F32, W>), grid, dim3(64 * W), 0, stream, a, pl,
-                               (int)base);
-        else
-            hipLaunchKernelGGL((step_kernel<DIM, F32, 2 * W>), grid, dim3(128 * W), 0, stream, a,
+        else if (!ch.once)
+            hipLaunchKernelGGL((step_kernel<DIM, F32, false, W>), grid, dim3(64 * W), 0, stream, a,
                                pl, (int)base);
+        else if (ch.waves == W)
+            hipLaunchKernelGGL((step_kernel<DIM, F32, true, W>), grid, dim3(64 * W), 0, stream, a,
+                               pl, (int)base);
+        else
+            hipLaunchKernelGGL((step_kernel<DIM, F32, true, 2 * W>), grid, dim3(128 * W), 0,
+                               stream, a, pl, (int)base);
     }
-    if (ch.splits > 1)
-        hipLaunchKernelGGL((join_kernel<F32>), dim3((uint32_t)(a.n * a.q_heads)), dim3(256), 0,
-                           stream, a, pl);
+    const int64_t out = (int64_t)a.n * a.q_heads;
+    // Parts of many rows are joined a wave to a row, of few by a workgroup each (whole
+    // calls, us): 8192 rows 101 and 104, the same of 256 new tokens of 4112 keys 51 and
+    // 60, 1024 rows 25.7 and 29.1; 256 rows 66 and 63.
+    if (ch.splits > 1 && ch.splits <= 64 && out >= 4 * device_shape().cus)
+        hipLaunchKernelGGL((join_rows_kernel<DIM, F32>), dim3((uint32_t)((out + 3) / 4)), dim3(256),
+                           0, stream, a, pl);
+    else if (ch.splits > 1)
+        hipLaunchKernelGGL((join_kernel<F32>), dim3((uint32_t)out), dim3(256), 0, stream, a, pl);
     return hipGetLastError();
 }
 
