@@ -17,8 +17,8 @@
 // that the number falls into, then the token.  Without draft logits pick judges, and
 // two launches are all.
 //
-// Measured: one conversation of four picked drafts over 151936 tokens 9.7 us, a chain of
-// two launches; 12 conversations of up to three drafts over 32003 tokens 18 us, a
+// Measured: one conversation of four picked drafts over 151936 tokens 8.3 us, a chain of
+// two launches; 12 conversations of up to three drafts over 32003 tokens 16 us, a
 // chain of four; 64 conversations of up to four drafts over 151936 tokens (318 MB that
 // the four have to read) 81 us, of which stats 62: 14 operations of 64 bits and five
 // others an element, 71% of its time, where the bytes alone are 44 us.
@@ -37,11 +37,11 @@ typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
 typedef f4_t f4_any_t __attribute__((aligned(4)));
 typedef h4_t h4_any_t __attribute__((aligned(2)));
 
-constexpr int kPart = 2048;        // tokens of a part, one wave's
+constexpr int kPart = 2048;        // tokens of a part: one wave's, or four's
 constexpr int kLoads = kPart / 256;
-constexpr int kThreads = 256;      // of stats: four parts
+constexpr int kThreads = 256;      // of stats: four parts, or one
 constexpr int kWaves = kThreads / 64;
-constexpr int kPickThreads = 512;  // of the others: eight parts, or eight rows judged at once
+constexpr int kPickThreads = 512;  // of the others: one part, or eight rows judged at once
 constexpr int kPickWaves = kPickThreads / 64;
 constexpr int kHeld = 2;           // parts that a lane keeps: rows of 262144 tokens need no more
 constexpr double kFaint = 0x1p-980;
@@ -254,38 +254,51 @@ __device__ __forceinline__ float heat_of(const VerifyArgs &a, int s) {
 }
 
 // ---- every part of every row ------------------------------------------------
-// EAGER: few workgroups.  Every row is requested before the conversation that holds
-// it is known; otherwise the draft's rows only then, since of those one in each
+// A part to W waves of a workgroup.  Four where there are few: the chain is as short
+// as it gets, and every row is requested before the conversation that holds it is
+// known; otherwise the draft's rows only then, since of those one in each
 // conversation is not needed, and none of the greedy ones.
-template <bool F16, bool EAGER>
+template <bool F16, int W>
 __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *stats, int parts) {
+    constexpr bool EAGER = W > 1;
+    constexpr int kParts = kWaves / W, kMine = kLoads / W;
     __shared__ double table[256];
-    const int groups = (parts + kWaves - 1) / kWaves, lane = threadIdx.x % 64;
-    const int part =
-        __builtin_amdgcn_readfirstlane(blockIdx.x % groups * kWaves + threadIdx.x / 64);
+    __shared__ double sums[W];
+    __shared__ float tops[W];
+    __shared__ int firsts[W];
+    const int groups = (parts + kParts - 1) / kParts, lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int part = __builtin_amdgcn_readfirstlane(blockIdx.x % groups * kParts + wave / W);
+    const int from = wave % W * kMine;
     const bool drafted = blockIdx.x / groups >= (uint32_t)a.n;
     const int row = blockIdx.x / groups - (drafted ? a.n : 0);
-    f4_t l[kLoads];
+    f4_t l[kMine];
     const void *x = drafted ? row_of<F16>(a.drafted, row, a.drafted_stride)
                             : row_of<F16>(a.logits, row, a.stride);
-    if (EAGER || !drafted) load_part<F16>(l, x, part, a.vocab);
+    if (EAGER || !drafted) load_part<F16>(l, x, part, a.vocab, from);
     fill_table(table);
     Span sp;
     if (!span_of(a, holder(a, row), sp) || row < sp.first || row > sp.last) return;
     const float heat = heat_of(a, sp.s);
     const bool cold = !(heat > 0.0f);
     if (drafted && (row == sp.last || cold)) return;
-    if (!EAGER && drafted) load_part<F16>(l, x, part, a.vocab);
+    if (!EAGER && drafted) load_part<F16>(l, x, part, a.vocab, from);
     const int draft = row < sp.last ? a.tokens[row + 1] : -1;
     __syncthreads();
-    if (part >= parts) return;
-    const int base = part * kPart + lane * 4;
+    if (part >= parts) return;  // (waves that share no part)
+    const int base = part * kPart + from * 256 + lane * 4;
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
+    for (int i = 0; i < kMine; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = larger(top, l[i][e]);
     top = wave_max(top);
+    if (W > 1) {
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i) top = larger(top, tops[i]);
+    }
     Stat st = {0.0, top, INT32_MAX};
     if (!(top <= FLT_MAX)) {
         st.sum = NAN;
@@ -294,13 +307,19 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
         // (read again: a loop that is not unrolled, beside the one that is)
         int first = INT32_MAX;
 #pragma nounroll
-        for (int i = kLoads; i-- > 0;) {
+        for (int i = kMine; i-- > 0;) {
             const f4_t again = load4<F16>(x, base + i * 256, a.vocab);
 #pragma unroll
             for (int e = 4; e-- > 0;)
                 if (again[e] == top) first = base + i * 256 + e;
         }
         st.at = wave_min(first);
+        if (W > 1) {
+            if (lane == 0) firsts[wave] = st.at;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < W; ++i) st.at = min(st.at, firsts[i]);
+        }
     } else {
         const Power power(table, heat);
         const double m = top;
@@ -310,7 +329,7 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
         if (judged && !a.drafted) {
             // the judged draft's weight stays out
 #pragma nounroll
-            for (int i = 0; i < kLoads; ++i) {
+            for (int i = 0; i < kMine; ++i) {
                 const f4_t again = load4<F16>(x, base + i * 256, a.vocab);
                 double d[4], w[4];
 #pragma unroll
@@ -321,7 +340,7 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4 * kLoads; i += 2) {
+            for (int i = 0; i < 4 * kMine; i += 2) {
                 const double d[2] = {(double)l[i / 4][i % 4] - m, (double)l[i / 4][i % 4 + 1] - m};
                 double w[2];
                 power.of(d, w);
@@ -331,9 +350,16 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
             }
         }
         sum = wave_sum(sum);
+        if (W > 1) {
+            if (lane == 0) sums[wave] = sum;
+            __syncthreads();
+            sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum += sums[i];
+        }
         st.sum = sum < kFaint ? 0.0 : sum;
     }
-    if (lane == 0) stats[(row + (drafted ? (int64_t)a.n : 0)) * parts + part] = st;
+    if (lane == 0 && wave % W == 0) stats[(row + (drafted ? (int64_t)a.n : 0)) * parts + part] = st;
 }
 
 // ---- the refused draft ------------------------------------------------------
@@ -702,11 +728,15 @@ hipError_t run(const VerifyArgs &a, void *ws, hipStream_t stream) {
     const int64_t many = rows * ((parts + kWaves - 1) / kWaves);
     const dim3 batch((uint32_t)a.batch);
     const uint32_t across = a.batch < 32768 ? (uint32_t)a.batch : 32768u;
-    if (many <= 4 * cus)
-        hipLaunchKernelGGL((stats_kernel<F16, true>), dim3((uint32_t)many), dim3(kThreads), 0,
-                           stream, a, stats, parts);
+    // (whole calls, us, a part to a wave and to four: rows of 151936 tokens without draft
+    // logits, four 9.9 and 8.4, 16 11.2 and 9.9, 32 12.9 and 12.2, 64 17.3 and 18.2, 256
+    // 35.6 and 41.9; rows of 32003 with draft logits, 8 16.0 and 13.9, 64 17.5 and 17.0,
+    // 96 19.0 and 18.9, 256 28.1 and 31.4)
+    if (rows * parts <= 8 * cus)
+        hipLaunchKernelGGL((stats_kernel<F16, kWaves>), dim3((uint32_t)(rows * parts)),
+                           dim3(kThreads), 0, stream, a, stats, parts);
     else
-        hipLaunchKernelGGL((stats_kernel<F16, false>), dim3((uint32_t)many), dim3(kThreads), 0,
+        hipLaunchKernelGGL((stats_kernel<F16, 1>), dim3((uint32_t)many), dim3(kThreads), 0,
                            stream, a, stats, parts);
     if (!a.drafted) {
         hipLaunchKernelGGL((pick_kernel<F16, false>), batch, dim3(kPickThreads), 0, stream, a,
