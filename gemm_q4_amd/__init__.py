@@ -674,8 +674,9 @@ def rotary(inv_freq=None, interleaved: bool = False, amplitude: float = 1.0, q_n
 def kv_append(cache, rot, q, k, v, positions, slots, q_out=None, stream=None):
     """Append k and v to `cache` (kv_cache()'s; kv_cache8()'s: in 8 bits) and rotate
     q: q [n, q_heads * dim] (or None), k and v [n, heads * dim], or the same with
-    the heads as a dimension; rows may be slices of wider ones.  positions int32 [n], slots int64 [n].  Returns the
-    rotated q [n, q_heads, dim]: q_out, or a new tensor of q's type."""
+    the heads as a dimension; rows may be slices of wider ones.  positions int32 [n],
+    slots int64 [n].  Returns the rotated q [n, q_heads, dim]: q_out, or a new tensor
+    of q's type."""
     if q is not None and q_out is None:
         heads = q.shape[1] if q.dim() == 3 else q.shape[1] // cache.dim
         q_out = _new(stream, (q.shape[0], heads, cache.dim), dtype=q.dtype, device=q.device)
@@ -702,8 +703,8 @@ def kv_read(cache, slots, k=None, v=None, dtype=None, stream=None):
 def attention(cache, q, q_start, kv_len, table, window: int = 0, sinks: int = 0, scale=None,
               y=None, stream=None, ws=None):
     """Attention of q [n, q_heads, dim] over `cache` (q4_0_attention; kv_cache8()'s:
-    q4_0_attention8): q_start int32 [batch + 1], kv_len int32 [batch], table int32 [batch, pages of the
-    longest].  scale: dim ** -0.5 unless given.  Returns y, like q."""
+    q4_0_attention8): q_start int32 [batch + 1], kv_len int32 [batch], table int32
+    [batch, pages of the longest].  scale: dim ** -0.5 unless given.  Returns y, like q."""
     if y is None:
         y = _new(stream, q.shape, dtype=q.dtype, device=q.device)
     if ws is None:

@@ -27,7 +27,7 @@
 // that the call cannot do without): one conversation of 448 keys 9.4 us, a chain of
 // lengths, page table, keys and the join of the parts; of 131072 keys 53 us, 5.2
 // TB/s (91 us over binary16); 64 conversations of 400 to 8192 keys, one to five
-// tokens each, 120 us, 4.0 TB/s; two prompts of 5001 and 1800 tokens 321 us, 720
+// tokens each, 119 us, 4.9 TB/s; two prompts of 5001 and 1800 tokens 318 us, 730
 // TFLOP/s.
 #include "q4_0_attention.h"
 #include "q4_0_dma.h"
@@ -844,7 +844,7 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
     __shared__ __align__(1024) uint8_t lds[P::kLds];
     __shared__ Scales<KT> scales[2][KW];
     __shared__ float ml[2][KW][R];
-    const int hk = blockIdx.x, split = blockIdx.y;
+    const int hk = blockIdx.x;
     Place at = find_tile<R>(a, pl.group, base + blockIdx.z);
     const int count = (at.rows + R - 1) / R;
     if (at.tile < 0 || at.tile >= count) return;
@@ -855,8 +855,6 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
     const int p1 = position(a, position0, (row1 - 1) / pl.group);
     const Reach<KT> r(a, p0, p1);
     const int top_lo = a.window && p1 >= a.window ? p1 - a.window + 1 : 0;
-    const int per = max((r.tiles + pl.splits - 1) / pl.splits, pl.least);
-    const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
     const int lane = threadIdx.x % 64, half = lane / 32, wave = uniform(threadIdx.x / 64);
     const int rw = wave % RW, kw = wave / RW;
     const int mine = rw * 32 + lane % 32, row = row0 + mine;
@@ -867,11 +865,11 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
         w.take(raw);
     }
     int top = kNoExponent;  // of the values in o
-    const int tiles = max((t1 - t0 - kw + KW - 1) / KW, 0);  // this group's
-    const int rounds = uniform((t1 - t0 + KW - 1) / KW);     // the first group's
+    const int tiles = max((r.tiles - kw + KW - 1) / KW, 0);  // this group's
+    const int rounds = uniform((r.tiles + KW - 1) / KW);     // the first group's
     const Source f(a, at.s, hk);
     uint8_t *stages = lds + kw * 4 * kTile;
-    const auto key_of = [&](int i) { return r.key(t0 + kw + i * KW); };
+    const auto key_of = [&](int i) { return r.key(kw + i * KW); };
     // a tile's loads: this wave's 16 rows of K and V (or of one of them, in kx), and the
     // scales of V (first wave) or K (second), a key to a lane
     const int group = rw % (KT / 16);
@@ -951,7 +949,8 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             w.o[d][i] = __builtin_amdgcn_ldexpf(w.o[d][i], top - W::kShift);
-    float l = halves_sum(w.l), m = w.top();
+    float l = halves_sum(w.l);
+    const float m = w.top();
     if (KW > 1) {
         // join the groups: the first takes over its rows' sum
         if (lane < 32) ml[0][kw][mine] = m, ml[1][kw][mine] = l;
@@ -964,7 +963,6 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
 #pragma unroll
         for (int i = 0; i < KW; ++i) l += ml[1][i][mine] * factor_of(ml[0][i][mine] - zero);
         const float fs = factor_of(m - zero);
-        m = most;
         float *share = (float *)(lds + wave * P::kShare) + (lane % 32) * P::kPitch + 4 * half;
 #pragma unroll
         for (int d = 0; d < DIM / 32; ++d)
@@ -976,14 +974,8 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
                 *(f4_t *)(share + 32 * d + 2 * i) = v;
             }
         __syncthreads();
-        if (pl.splits > 1 && wave < RW && lane < 32 && row < row1) {
-            const int64_t out = (int64_t)(at.first + row / pl.group) * a.q_heads +
-                                hk * pl.group + row % pl.group;
-            put_ml(a, pl, split, out, m, l);
-        }
         if (wave < RW && lane < 32) ml[1][0][mine] = l;
         __syncthreads();
-        if (pl.splits > 1 && t0 >= t1) return;
         for (int e = threadIdx.x; e < (row1 - row0) * (DIM / 4); e += P::kThreads) {
             const int rr = e / (DIM / 4), d = e % (DIM / 4) * 4;
             const float *src = (const float *)(lds + rr / 32 * P::kShare) + rr % 32 * P::kPitch + d;
@@ -997,14 +989,13 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
             const int token = (row0 + rr) / pl.group;
             const int64_t out = (int64_t)(at.first + token) * a.q_heads + hk * pl.group +
                                 (row0 + rr) % pl.group;
-            put4<F32>(a, pl, split, out, DIM, d, o, ml[1][0][rr], position0 + token >= 0);
+            put_y4<F32>(a, out, DIM, d, o, ml[1][0][rr], position0 + token >= 0);
         }
         return;
     }
     if (row >= row1) return;
     const int64_t out = (int64_t)(at.first + row / pl.group) * a.q_heads + hk * pl.group +
                         row % pl.group;
-    // (one wave group: 128-row tiles, whose key axis is never split)
 #pragma unroll
     for (int d = 0; d < DIM / 32; ++d)
 #pragma unroll
@@ -1115,46 +1106,38 @@ Choice choose(const AttentionArgs &a) {
     else
         ch.rows = one || few ? 32 : 64;
     ch.once = one;
-    const int R = ch.rows;
-    ch.tiles = rows / R + a.batch;
+    ch.tiles = rows / ch.rows + a.batch;
+    ch.waves = dim > 128 ? 2 : 4;
+    ch.splits = ch.least = 1;
+    ch.part = ch.bytes = 0;
+    if (ch.rows > 32) return ch;  // (such tiles fill three quarters of the device, or all)
     // the items that are likely to have work: not all tiles do
-    const int64_t likely = (R > 32 ? rows / R + (a.batch + 1) / 2
-                                   : (rows / R > a.batch ? rows / R : a.batch)) *
-                           heads;
+    const int64_t likely = (rows / 32 > a.batch ? rows / 32 : a.batch) * heads;
     // the key tiles a row tile can have at most
-    // (128-row tiles are never split: their key tiles are not counted)
-    const int KT = R == 64 ? 32 : 64;
     int64_t keys = (int64_t)a.table_stride << a.cache.page_shift;
     if (a.window) {
-        const int64_t near = (int64_t)a.window + a.sinks + 2 * R + 2 * KT;
+        const int64_t near = (int64_t)a.window + a.sinks + 2 * kStepRows + 2 * kStepKeys;
         if (near < keys) keys = near;
     }
-    const int64_t most = (keys + KT - 1) / KT;
-    int64_t splits;
-    ch.waves = dim > 128 ? 2 : 4;
-    if (R > 32) {
-        splits = cus / likely;  // (128-row tiles are taken where that is one at most)
-        ch.least = 16;
-    } else {
-        // workgroups that run at once: two to a compute unit, four of 64-wide heads
-        const int64_t slots = cus * (dim > 64 ? 2 : 4);
-        // As many parts as run at once, of what gives every slot one or 1024 keys if
-        // that is more; none where the conversations alone fill the device.  Four
-        // times as many, so that long conversations do not end alone, gain less
-        // than writing and joining parts costs: 128 conversations of 100 to 2048
-        // keys, one token each, 63 us so and 78 us, four tokens each 69 and 91; 16
-        // of 8192, eight tokens of 64 heads each, 95 and 116; 64 of 400 to 8192
-        // keys (heads of 64) 78 and 90, (heads of 128, one to five tokens) 131 and
-        // 135; only one token each of the same 121 and 113.  Parts of 512, 1024 and
-        // 2048 keys at least: 48 conversations of 200 to 4096 keys 53, 56 and 62; 24
-        // of 800 to 16384 99, 99 and 101; others alike.
-        splits = (slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
-        const int64_t fair = (most * likely + slots - 1) / slots;
-        ch.least = fair > 16 ? 16 : fair < ch.waves ? ch.waves : (int)fair;
-        // too few keys to split: the workgroup's own waves take them, eight
-        // (four) instead of four (two) while there are units to spare
-        if (ch.once && most / ch.least < 2 && likely <= cus) ch.waves *= 2;
-    }
+    const int64_t most = (keys + kStepKeys - 1) / kStepKeys;
+    // workgroups that run at once: two to a compute unit, four of 64-wide heads
+    const int64_t slots = cus * (dim > 64 ? 2 : 4);
+    // As many parts as run at once, of 1024 keys at least, or of what gives every slot
+    // one where that is less; none where the conversations alone fill the device.
+    // Four times as many, so that long conversations do not end alone, gain less
+    // than writing and joining parts costs: 128 conversations of 100 to 2048
+    // keys, one token each, 63 us so and 78 us, four tokens each 69 and 91; 16
+    // of 8192, eight tokens of 64 heads each, 95 and 116; 64 of 400 to 8192
+    // keys (heads of 64) 78 and 90, (heads of 128, one to five tokens) 131 and
+    // 135; only one token each of the same 121 and 113.  Parts of 512, 1024 and
+    // 2048 keys at least: 48 conversations of 200 to 4096 keys 53, 56 and 62; 24
+    // of 800 to 16384 99, 99 and 101; others alike.
+    int64_t splits = (slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
+    const int64_t fair = (most * likely + slots - 1) / slots;
+    ch.least = fair > 16 ? 16 : fair < ch.waves ? ch.waves : (int)fair;
+    // too few keys to split: the workgroup's own waves take them, eight
+    // (four) instead of four (two) while there are units to spare
+    if (ch.once && most / ch.least < 2 && likely <= cus) ch.waves *= 2;
     if (splits > most / ch.least) splits = most / ch.least;
     if (splits > kMaxSplits) splits = kMaxSplits;
     const int64_t out = (int64_t)a.n * a.q_heads;

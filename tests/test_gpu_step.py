@@ -370,6 +370,22 @@ def test_attention8_long_axis(lengths, half):
     check8(lengths, 8, 2, 64, 16, 700, 40, half, seed=12, spread=2.0)
 
 
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention8_parts_of_many_rows(dim, half):
+    """Enough rows that a wave joins a row's parts, some of which see none of its
+    keys; conversations that are empty or see nothing among them."""
+    lengths = [(8, 900 - 31 * i) for i in range(13)] + [(0, 0), (8, 3), (5, 0), (8, 70)]
+    hq, hk = 16, 2
+    c = q4.q4_0_kv_cache8(0, 0, 0, 0, 1, hk, 16, dim)
+    call = (hq, q4.F16 if half else q4.F32, sum(n for n, _ in lengths), 57, len(lengths))
+    rows = call[2] * hq
+    assert rows >= 1024 and q4.q4_0_select_attention8(c, *call) == 32
+    assert 2 <= q4.q4_0_attention8_workspace_size(c, *call) // (rows * (dim + 2) * 4) <= 64
+    check8(lengths, hq, hk, dim, 16, 0, 0, half, seed=dim)
+    check8(lengths, hq, hk, dim, 16, 300, 20, half, seed=dim + 1, spread=2.0)
+
+
 @pytest.mark.parametrize("count,tokens,longest", [(65, 1, 90), (150, 1, 40), (300, 3, 30),
                                                   (4500, 1, 9), (130, 40, 50)])
 def test_attention8_many_conversations(count, tokens, longest):
@@ -617,6 +633,35 @@ def test_verify_many_conversations(modelled):
     logits, tokens, start, uniform, drafted = drafts(rng, [3], 50, False, modelled)
     empty[200:] = 3
     check_verify(logits, tokens, empty, uniform, drafted)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("modelled", [False, True])
+def test_verify_many_parts(modelled, half):
+    """More than 2048 parts, a wave to each: conversations that draw, that take the
+    greatest, and whose rows are no distribution."""
+    rng = np.random.default_rng([11, modelled, half])
+    rows = [4, 1, 7, 3] * (5 if modelled else 9)
+    logits, tokens, start, uniform, drafted = drafts(rng, rows, 33001, half, modelled)
+    assert logits.shape[0] * (2 if modelled else 1) * 17 > 2048
+    heat = np.tile(np.array([1.0, 0.8, 0.0, 1.2, 0.6, 0.9], np.float32), 6)[:len(rows)]
+    check_verify(logits, tokens, start, uniform, drafted, heat, pad=5)
+    for s in range(0, len(rows), 3):
+        logits[start[s], rng.integers(0, 33001)] = [np.nan, np.inf][s % 2]
+    logits[start[7]] = -np.inf
+    logits[start[8], 100:] = -np.inf
+    _, t = check_verify(logits, tokens, start, uniform, drafted, heat)
+    assert (t == -1).sum() > len(rows) // 3
+
+
+@pytest.mark.parametrize("modelled", [False, True])
+def test_verify_more_parts_than_lanes_hold(modelled):
+    """Vocabularies past 262144 tokens; what is drawn lies in the last parts too."""
+    rng = np.random.default_rng([12, modelled])
+    for heat in (1.0, 3.0, 0.0):
+        logits, tokens, start, uniform, drafted = drafts(rng, [3, 1, 4], 300007, False, modelled)
+        logits[:, 290000:] += 1.5
+        check_verify(logits, tokens, start, uniform, drafted, np.full(3, heat, np.float32))
 
 
 def test_verify_borders():
