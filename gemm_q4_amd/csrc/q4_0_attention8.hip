@@ -23,12 +23,12 @@
 // follows at once.  Scores of binary16 rows are in powers of two (K's scales carry
 // the factor, the same for all rows); float32 rows have a factor `c` of their own.
 //
-// Measured (32 + 8 heads of 128, binary16 rows, the rates of the bytes or operations
-// that the call cannot do without): one conversation of 448 keys 9.4 us, a chain of
-// lengths, page table, keys and the join of the parts; of 131072 keys 53 us, 5.2
-// TB/s (91 us over binary16); 64 conversations of 400 to 8192 keys, one to five
-// tokens each, 119 us, 4.9 TB/s; two prompts of 5001 and 1800 tokens 318 us, 730
-// TFLOP/s.
+// Measured (32 + 8 heads of 128, binary16 rows but for the first; rates of the bytes or
+// operations that the call cannot do without): one conversation of 448 keys 9.4 us, a
+// chain of lengths, page table, keys and the join of the waves; of 131072 keys 53 us, 5.2
+// TB/s (over binary16 91 us); 64 conversations of 470 to 8192 keys, one to four tokens
+// each, 119 us, 4.9 TB/s; the last 2438 of 5001 tokens beside a prompt of 3146 318 us,
+// 730 TFLOP/s.
 #include "q4_0_attention.h"
 #include "q4_0_dma.h"
 
@@ -607,13 +607,15 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Attenti
 // waves.  Both products are v_mfma_f32_32x32x16_f16 on transposed scores; weights of
 // binary16 rows are rounded once, of float32 rows held in two parts.
 //
-// Bound by vector instructions: 384 and 64 exponentials to 64 keys of 32 rows, 63% of
-// the time, with the matrix cores busy for 31%; two waves to a SIMD overlap them but
-// little.  What brought them down: codes converted once for all waves (they were half
-// of the instructions when each wave converted its own), scores less the running
-// maximum by one fused operation, no rescaling while the maximum lags by less than
-// 2^8.  Eight waves on a key tile, which halves the conversions again, gained
-// nothing (two prompts of 5001 and 3146 tokens 406 us, four waves 397).
+// Bound by vector instructions, 360 to 64 keys of 32 rows, of which 32 exponentials take
+// four times as long; they hardly overlap with the matrix cores (busy for 31% of the
+// cycles) at two waves to a SIMD, where waits for LDS and barriers take the rest;
+// priorities change nothing (316 to 326 us).  What brought them down: codes converted
+// once for all waves (they were half of the instructions when each wave converted its
+// own), scores less the running maximum by one fused operation, no rescaling while the
+// maximum lags by less than 2^8.  Eight waves on a key tile, which halves the
+// conversions again, gained nothing (prompts of 5001 and 3146 tokens 406 us, four
+// waves 390).
 //
 // Every wave brings 16 keys of K and V; wide float32 rows, whose registers are few,
 // take half as many keys a tile, and a wave brings 16 of K or of V (44 prompts of 356

@@ -4,6 +4,12 @@
 // 4g + 3 and 4g + 16 .. 4g + 19 of a block.  q - 8 and d are exact in float32, so is
 // their product; the scale rounds it once.  The row stays in registers for its
 // norm.
+//
+// Bound by the bytes it writes: 8191 tokens of 2560 with a binary16 norm (126 MB out,
+// 12 MB of the table) in 43 us.  A row's codes lie in pieces of 16 bytes, 256 bytes
+// apart (the layout is the products'), so whole lines bring 76 MB
+// where 12 are needed: 200 MB in all, 4.7 TB/s.  Five tokens take 4 us, one
+// launch.  Non-temporal stores of h: 44.35 us a call, without 44.4.
 #include "q4_0_device.h"
 #include "q4_0_internal.h"
 
