@@ -14,17 +14,15 @@
 // weights (without draft logits: of all but the judged draft's, so that taking it
 // out costs no digits).  judge: each conversation's first refused draft.  rest (with
 // draft logits): sums of max(p - q, 0) over the parts of that row.  pick: the part
-// that the number falls into, then the token.  Without draft logits pick judges, and
-// two launches are all.
+// that the number falls into, then the token.  Few parts: rest judges, three launches.
+// Without draft logits pick judges, and two are all.
 //
 // Measured: one conversation of four picked drafts over 151936 tokens 8.3 us, a chain of
-// two launches; 12 conversations of up to three drafts over 32003 tokens 16 us, a
-// chain of four; 64 conversations of up to four drafts over 151936 tokens (318 MB that
-// the four have to read) 81 us, of which stats 62: 14 operations of 64 bits and five
+// two launches; 12 conversations of up to three drafts over 32003 tokens 14 us, a
+// chain of three; 64 conversations of up to six drafts over 151936 tokens (318 MB that
+// stats has to read) 79 us, of which stats 60: ten operations of 64 bits and five
 // others an element, 71% of its time, where the bytes alone are 44 us.
 #include <float.h>
-
-#include <type_traits>
 
 #include "q4_0_device.h"
 #include "q4_0_internal.h"
@@ -122,8 +120,10 @@ struct Power {
         for (int i = 0; i < N; ++i) z[i] = fma(z[i], r[i], 1.0);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            w[i] = z[i] * __builtin_bit_cast(double, t[i] + ((uint64_t)((k[i] << 12) & 0xFFF00000u)
-                                                             << 32));
+            w[i] = z[i] * __builtin_bit_cast(
+                              double, (uint64_t)((uint32_t)(t[i] >> 32) + ((k[i] & ~255u) << 12))
+                                              << 32 |
+                                          (uint32_t)t[i]);
     }
     // One, 0 below that.
     __device__ __forceinline__ double exact(double d) const {
@@ -512,22 +512,31 @@ __device__ __forceinline__ double above(double p, double p_share, double q, doub
 // of q: a chain as short as it gets (the whole call, a part to a wave and so, us: 12
 // conversations over 32003 tokens 23.5 and 17.3, of 151936 29.8 and 26.6; 64 of them 73
 // and 68).  Parts fastest in the grid: 64 conversations' 12.8 us, the other way 17.2.
-template <bool F16>
-__global__ __launch_bounds__(kPickThreads) void rest_kernel(VerifyArgs a, const Verdict *verdicts,
-                                                            double *rests, int parts) {
+// JUDGED: the verdicts are there; else every workgroup judges its conversation, and its
+// first one notes the verdict.
+template <bool F16, bool JUDGED>
+__global__ __launch_bounds__(kPickThreads) void rest_kernel(VerifyArgs a, const Stat *stats,
+                                                            Verdict *verdicts, double *rests,
+                                                            int parts) {
     static_assert(kLoads == kPickWaves, "a load to a wave");
     __shared__ double table[256];
     __shared__ double sums[kPickWaves];
+    __shared__ Verdict seen[kPickWaves];
     const int part = blockIdx.x, s = blockIdx.z * gridDim.y + blockIdx.y;
     if (s >= a.batch) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const Verdict v = verdicts[s];  // (of an empty conversation: whatever is there)
+    Verdict v;
+    if (JUDGED) v = verdicts[s];  // (of an empty conversation: whatever is there)
     const float heat = heat_of(a, s);
     const Power power(table, heat);
     Span sp;
     const bool some = span_of(a, s, sp);
     fill_table(table);
     if (!some) return;
+    if (!JUDGED) {
+        v = judge(a, stats, parts, sp, heat, power, seen);
+        if (part == 0 && threadIdx.x == 0) verdicts[s] = v;
+    }
     if (v.how != kRest) return;
     f4_t l[1], g[1];
     load_part<F16>(l, row_of<F16>(a.logits, v.row, a.stride), part, a.vocab, wave);
@@ -563,10 +572,6 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(VerifyArgs a, const 
     __shared__ double table[256];
     __shared__ double sums[kPickWaves];
     __shared__ Verdict seen[kPickWaves];
-    __shared__ struct {
-        double target, below;
-        int part;  // -1: the draft is all there is
-    } goal;
     __shared__ int highest;
     const int s = blockIdx.x, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     // what depends on the conversation's number alone is requested together
@@ -743,10 +748,20 @@ hipError_t run(const VerifyArgs &a, void *ws, hipStream_t stream) {
                            stats, nullptr, nullptr, parts);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(judge_kernel, batch, dim3(kPickThreads), 0, stream, a, stats, verdicts,
-                       parts);
-    hipLaunchKernelGGL((rest_kernel<F16>), dim3((uint32_t)parts, across, (uint32_t)(a.batch + across - 1) / across),
-                       dim3(kPickThreads), 0, stream, a, verdicts, rests, parts);
+    const dim3 all((uint32_t)parts, across, ((uint32_t)a.batch + across - 1) / across);
+    // As many parts as run at once: every workgroup of rest judges its conversation, a
+    // launch less (whole calls of four rows a conversation, us, so and with a launch of
+    // their own: over 32003 tokens 7 conversations 13.8 and 15.4, 32 19.7 and 21.0, 48
+    // 25.1 and 24.0; over 151936 four 15.2 and 16.8, 12 27.3 and 26.8, 64 83 and 64)
+    if ((int64_t)a.batch * parts <= 2 * cus) {
+        hipLaunchKernelGGL((rest_kernel<F16, false>), all, dim3(kPickThreads), 0, stream, a, stats,
+                           verdicts, rests, parts);
+    } else {
+        hipLaunchKernelGGL(judge_kernel, batch, dim3(kPickThreads), 0, stream, a, stats, verdicts,
+                           parts);
+        hipLaunchKernelGGL((rest_kernel<F16, true>), all, dim3(kPickThreads), 0, stream, a, stats,
+                           verdicts, rests, parts);
+    }
     hipLaunchKernelGGL((pick_kernel<F16, true>), batch, dim3(kPickThreads), 0, stream, a, stats,
                        verdicts, rests, parts);
     return hipGetLastError();
