@@ -27,8 +27,8 @@
 // operations that the call cannot do without): one conversation of 448 keys 9.4 us, a
 // chain of lengths, page table, keys and the join of the waves; of 131072 keys 53 us, 5.2
 // TB/s (over binary16 91 us); 64 conversations of 470 to 8192 keys, one to four tokens
-// each, 119 us, 4.9 TB/s; the last 2438 of 5001 tokens beside a prompt of 3146 318 us,
-// 730 TFLOP/s.
+// each, 99 us, 5.9 TB/s (185 us over binary16 with a token each); the last 2438 of 5001
+// tokens beside a prompt of 3146 315 us, 740 TFLOP/s.
 #include "q4_0_attention.h"
 #include "q4_0_dma.h"
 
@@ -146,7 +146,7 @@ struct Source {
 //
 // Bound by the bytes: 6 to 6.7 TB/s while the keys stream.  What keeps a call from that
 // as a whole is the chain before the first key (4 to 5 us), the join (5 us), and, with
-// conversations of several lengths, the slots that end early.  64 keys a tile: the
+// conversations of several lengths, the slots that end early: the longest come first.  64 keys a tile: the
 // scales of 64 are one copy of 4 bytes to a lane.  Up to 32 rows: 64 rows to a wave
 // (which leaves one wave to a SIMD) took 200 instead of 158 us for 16 conversations
 // of 8192 keys, eight tokens of 8 heads each.
@@ -582,6 +582,43 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
     }
 }
 
+// Tile `w` of up to 64 conversations, the longest first: the first tiles of all, then
+// what further ones there are.
+__device__ __forceinline__ Place longest_first(const AttentionArgs &a, int group, int w) {
+    const int lane = threadIdx.x % 64, s = min(lane, a.batch - 1);
+    const bool held = lane < a.batch;
+    const int b = min(max(a.q_start[s], 0), a.n), e = min(max(a.q_start[s + 1], b), a.n);
+    const int kv = max(a.kv_len[s], 0);
+    const int rows = (e - b) * group;
+    int who, tile = 0;
+    if (w < a.batch) {
+        // (no two conversations have one key)
+        const int key = (rows ? min(kv, (1 << 24) - 1) << 6 : 0) | lane;
+        int before = 0;
+        for (int i = 0; i < a.batch; ++i) before += __builtin_amdgcn_readlane(key, i) > key;
+        who = __ffsll((unsigned long long)__ballot(held && before == w)) - 1;
+    } else {
+        const int more = held ? max((rows + kStepRows - 1) / kStepRows - 1, 0) : 0;
+        int sum = more;
+#pragma unroll
+        for (int i = 1; i < 64; i <<= 1) {
+            const int x = __shfl_up(sum, i);
+            if (lane >= i) sum += x;
+        }
+        const uint64_t past = __ballot(sum > w - a.batch);
+        who = past ? __ffsll((unsigned long long)past) - 1 : 0;
+        tile = past ? w - a.batch + 1 - __builtin_amdgcn_readlane(sum - more, who) : -1;
+    }
+    who = uniform(who);
+    Place p;
+    p.s = who;
+    p.first = __builtin_amdgcn_readlane(b, who);
+    p.rows = __builtin_amdgcn_readlane(rows, who);
+    p.kv = __builtin_amdgcn_readlane(kv, who);
+    p.tile = uniform(tile);
+    return p;
+}
+
 // ONCE: a conversation's rows are one tile, most likely.
 template <int DIM, bool F32, bool ONCE, int W>
 __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(AttentionArgs a, Plan pl,
@@ -589,7 +626,8 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Attenti
     __shared__ __align__(1024) uint8_t lds[W * kStepRows * (DIM + 4) * 4];
     __shared__ float ml[2][W][kStepRows];
     const int hk = blockIdx.x, split = blockIdx.y;
-    const Place at = find_tile<kStepRows>(a, pl.group, base + blockIdx.z);
+    const Place at = ONCE && a.batch <= 64 ? longest_first(a, pl.group, base + blockIdx.z)
+                                           : find_tile<kStepRows>(a, pl.group, base + blockIdx.z);
     const int row0 = at.tile * kStepRows;
     if (row0 < 0 || row0 >= at.rows) return;
     const int row1 = min(row0 + kStepRows, at.rows);
@@ -1129,17 +1167,24 @@ Choice choose(const AttentionArgs &a) {
     // Four times as many, so that long conversations do not end alone, gain less
     // than writing and joining parts costs: 128 conversations of 100 to 2048
     // keys, one token each, 63 us so and 78 us, four tokens each 69 and 91; 16
-    // of 8192, eight tokens of 64 heads each, 95 and 116; 64 of 400 to 8192
-    // keys (heads of 64) 78 and 90, (heads of 128, one to five tokens) 131 and
-    // 135; only one token each of the same 121 and 113.  Parts of 512, 1024 and
+    // of 8192, eight tokens of 64 heads each, 95 and 116.  Parts of 512, 1024 and
     // 2048 keys at least: 48 conversations of 200 to 4096 keys 53, 56 and 62; 24
     // of 800 to 16384 99, 99 and 101; others alike.
     int64_t splits = (slots + (a.batch == 1 ? 0 : likely - 1)) / likely;
     const int64_t fair = (most * likely + slots - 1) / slots;
     ch.least = fair > 16 ? 16 : fair < ch.waves ? ch.waves : (int)fair;
-    // too few keys to split: the workgroup's own waves take them, eight
-    // (four) instead of four (two) while there are units to spare
-    if (ch.once && most / ch.least < 2 && likely <= cus) ch.waves *= 2;
+    // Up to 64 conversations come the longest first.  With more of them than fill the
+    // device when each workgroup has eight waves (four), that evens out several
+    // lengths better than parts do: 64 of 400 to 8192 keys 99 and 112 us, one to five
+    // tokens each 120 and 131, 48 of 200 to 4096 45 and 54; short ones and equal ones
+    // lose (64 of 25 to 512 keys 22 and 16, all of 4096 98 and 92).
+    if (ch.once && a.batch <= 64 && 4 * likely > 5 * cus && most >= 32)
+        splits = 1, ch.waves *= 2;
+    // Few keys: the workgroup's own waves take them, eight (four), while there are
+    // units to spare; and where half of them are busy anyhow (20 conversations of 50
+    // to 1024 keys 13.7 us, in parts 16.5; eight of them 13.1 and 10.8).
+    else if (ch.once && likely <= cus && (most / ch.least < 2 || (2 * likely > cus && most <= 16)))
+        splits = 1, ch.waves *= 2;
     if (splits > most / ch.least) splits = most / ch.least;
     if (splits > kMaxSplits) splits = kMaxSplits;
     const int64_t out = (int64_t)a.n * a.q_heads;

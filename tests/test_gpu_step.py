@@ -371,6 +371,35 @@ def test_attention8_long_axis(lengths, half):
 
 
 @pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("count", [1, 2, 63, 64, 65])
+def test_attention8_conversations_of_many_lengths(count, half):
+    """Few rows to a conversation on average, several tiles of them to some; equal
+    lengths, empty conversations, rows that see nothing."""
+    rng = np.random.default_rng([13, count])
+    kvs = rng.choice([0, 1, 5, 33, 64, 65, 130, 130, 190], count)
+    news = [int(rng.choice([0, 1, 1, 2])) for _ in range(count)]
+    for s in range(0, count, 7):
+        news[s], kvs[s] = (6, 40, 20)[s % 3], max(kvs[s], 1)
+    if count > 16:
+        news[15], kvs[15] = 33, 12
+    assert sum(news) * 4 <= 32 * count or count < 3
+    check8([(n, int(kv)) for n, kv in zip(news, kvs)], 8, 2, 64, 16, 0, 0, half, seed=count)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention8_full_device_of_long_contexts(dim, half):
+    """More conversations' heads than units and long tables: a workgroup of twice the
+    waves to each, the longest first, no parts."""
+    heads = 16 if dim > 128 else 8
+    lengths = [(1 + i % 2, 40 + (53 * i) % 333) for i in range(45)] + [(1, 2100), (3, 1500)]
+    c = q4.q4_0_kv_cache8(0, 0, 0, 0, 1, heads, 64, dim)
+    assert q4.q4_0_attention8_workspace_size(c, heads, q4.F16 if half else q4.F32,
+                                             sum(n for n, _ in lengths), 33, len(lengths)) == 0
+    check8(lengths, heads, heads, dim, 64, 0, 0, half, seed=dim)
+
+
+@pytest.mark.parametrize("half", [True, False])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_attention8_parts_of_many_rows(dim, half):
     """Enough rows that a wave joins a row's parts, some of which see none of its
