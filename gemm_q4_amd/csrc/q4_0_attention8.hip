@@ -25,7 +25,7 @@
 //
 // Measured (32 + 8 heads of 128, binary16 rows but for the first; rates of the bytes or
 // operations that the call cannot do without): one conversation of 448 keys 9.4 us, a
-// chain of lengths, page table, keys and the join of the waves; of 131072 keys 53 us, 5.2
+// chain of lengths, page table, keys and the join of the waves; of 131072 keys 52 us, 5.3
 // TB/s (over binary16 91 us); 64 conversations of 470 to 8192 keys, one to four tokens
 // each, 99 us, 5.9 TB/s (185 us over binary16 with a token each); the last 2438 of 5001
 // tokens beside a prompt of 3146 315 us, 740 TFLOP/s.
@@ -1160,8 +1160,14 @@ Choice choose(const AttentionArgs &a) {
         if (near < keys) keys = near;
     }
     const int64_t most = (keys + kStepKeys - 1) / kStepKeys;
+    // One conversation of many keys: half as many parts of twice the waves (4 + 1 heads and
+    // 32 + 8 of 128: 20000 keys 13.3 us and 14.5, otherwise 14.0 and 17.8; 12000 keys
+    // 12.6 and 13.1, otherwise 11.0 and 13.6; 131072 keys of 32 + 8 53.1 and 51.6, of
+    // 16 + 4 heads of 256 60.9 and 55.2).
+    const bool solo = ch.once && a.batch == 1 && most >= 256;
+    if (solo) ch.waves *= 2;
     // workgroups that run at once: two to a compute unit, four of 64-wide heads
-    const int64_t slots = cus * (dim > 64 ? 2 : 4);
+    const int64_t slots = cus * (dim > 64 ? 2 : 4) / (solo ? 2 : 1);
     // As many parts as run at once, of 1024 keys at least, or of what gives every slot
     // one where that is less; none where the conversations alone fill the device.
     // Four times as many, so that long conversations do not end alone, gain less
@@ -1183,9 +1189,12 @@ Choice choose(const AttentionArgs &a) {
     // Few keys: the workgroup's own waves take them, eight (four), while there are
     // units to spare; and where half of them are busy anyhow (20 conversations of 50
     // to 1024 keys 13.7 us, in parts 16.5; eight of them 13.1 and 10.8).
-    else if (ch.once && likely <= cus && (most / ch.least < 2 || (2 * likely > cus && most <= 16)))
+    else if (!solo && ch.once && likely <= cus && (most / ch.least < 2 || (2 * likely > cus && most <= 16)))
         splits = 1, ch.waves *= 2;
-    if (splits > most / ch.least) splits = most / ch.least;
+    // (a part of the fewest keys, a tile to a wave, is not made longer by the rest: 700
+    // keys in three parts, 10.2 us, in two 12.7; 4000 keys 10.4 and 12.3)
+    const int64_t fit = (most + (ch.least > ch.waves ? 0 : ch.least - 1)) / ch.least;
+    if (splits > fit) splits = fit;
     if (splits > kMaxSplits) splits = kMaxSplits;
     const int64_t out = (int64_t)a.n * a.q_heads;
     const int64_t room = (int64_t)kWorkspaceBytes / (out * (dim + 2) * 4);
