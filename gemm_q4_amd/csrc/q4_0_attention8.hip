@@ -28,7 +28,7 @@
 // chain of lengths, page table, keys and the join of the waves; of 131072 keys 52 us, 5.3
 // TB/s (over binary16 91 us); 64 conversations of 470 to 8192 keys, one to four tokens
 // each, 99 us, 5.9 TB/s (185 us over binary16 with a token each); the last 2438 of 5001
-// tokens beside a prompt of 3146 315 us, 740 TFLOP/s.
+// tokens beside a prompt of 3146 318 us, 730 TFLOP/s.
 #include "q4_0_attention.h"
 #include "q4_0_dma.h"
 
@@ -306,13 +306,15 @@ template <int DIM, bool F32> struct Block {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[b][i] -= up;
         }
+        float sum = 0.0f;  // of the tile first: beside a strong key's, one faint weight is nothing
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s[b][i] = __builtin_amdgcn_exp2f(F32 ? s[b][i] * c : s[b][i]);
-                l += s[b][i];
+                sum += s[b][i];
             }
+        l += sum;
     }
     // The maximum in powers of two, minus infinity if there was none.
     __device__ __forceinline__ float top() const { return over == -INFINITY ? over : m * c; }
@@ -821,6 +823,7 @@ template <int DIM, bool F32> struct Rows {
                 for (int i = 0; i < 16; ++i) s[t][i] -= up;
         }
         h8_t w[KT / 16][kParts];
+        float sum = 0.0f;
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t)
 #pragma unroll
@@ -829,10 +832,11 @@ template <int DIM, bool F32> struct Rows {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float y = __builtin_amdgcn_exp2f(F32 ? s[t][i + e] * c : s[t][i + e]);
-                    l += y;
+                    sum += y;
                     s[t][i + e] = y * x[e];
                 }
             }
+        l += sum;
         if (masked) {
             asm volatile("; masked tile");
 #pragma unroll
@@ -868,6 +872,46 @@ template <int DIM, bool F32> struct Rows {
                 for (int x = 0; x < kParts; ++x)
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[b][x], o[d], 0, 0, 0);
             }
+        }
+    }
+};
+
+// Sums that took in many tiles: a faint weight's share would vanish in them (each is off
+// by half a step of the sum, and of 10^5 keys beside a strong one most would be lost).
+// So every kFold tiles, if half as many are left, they are put aside, in memory:
+// registers are few, and the way there is rare.  144 tokens of 89120 keys, float32:
+// off by 5e-7 so, by 3e-5 without.  (Every 32 tiles: 5000 keys 343 us instead of 316.)
+constexpr int kFold = 64;
+template <int DIM, bool F32> struct Total {
+    volatile f4_t o[DIM / 8];
+    float l, m;
+    int top;
+    bool seen;
+    __device__ __forceinline__ void fold(Rows<DIM, F32> &w, int now, bool more) {
+        if (more) back(w, now);
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                o[4 * d + i / 4] = f4_t{w.o[d][i], w.o[d][i + 1], w.o[d][i + 2], w.o[d][i + 3]};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w.o[d][i + e] = 0.0f;
+            }
+        l = w.l, m = w.m, top = now, seen = w.over != -INFINITY;
+        w.l = 0.0f;
+    }
+    // What was put aside, brought to the maximum and the exponent now and added again.
+    __device__ __forceinline__ void back(Rows<DIM, F32> &w, int now) const {
+        const float f = seen ? factor_of((m - w.m) * w.c) : 1.0f;
+        const float fo = f * __builtin_amdgcn_ldexpf(1.0f, top - now);
+        w.l += l * f;
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d) {
+            f4_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = o[4 * d + i];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w.o[d][i] = fmaf(x[i / 4][i % 4], fo, w.o[d][i]);
         }
     }
 };
@@ -954,6 +998,7 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
             sc.k[lane] = fabsf(sx) <= FLT_MAX ? sx * k_factor : NAN;
         }
     };
+    Total<DIM, F32> total;
     int pages = -1;
     if (tiles > 0) {
         load(0, look(0));
@@ -982,7 +1027,9 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
         const int k0 = key_of(i);
         const uint8_t *kbuf = stages + (i & 1) * 2 * kTile;
         w.template step<KT>(kbuf, kbuf + kTile, sc, k0, !r.all(k0, KT, top_lo), r.sinks);
+        if (i % kFold == kFold - 1 && tiles - i > kFold / 2) total.fold(w, top, i >= kFold);
     }
+    if (tiles >= kFold + kFold / 2) total.back(w, top);
     // the values' own magnitude again, the maximum in powers of two
 #pragma unroll
     for (int d = 0; d < DIM / 32; ++d)

@@ -354,6 +354,31 @@ def test_attention8_many_faint_weights_beside_a_strong_one(gap, half):
     assert (y[0, :, 2:] == 0).all()
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,heads,rows", [(256, 48, 64), (1024, 32, 128), (1, 4, 32)])
+def test_attention8_faint_weights_of_many_keys(new, heads, rows, dim):
+    """One strong key of weight 1 and value 1 among 20000 of weight 2^-24.5 and value -1:
+    each alone is less than half a step of the sums, all of them are 8e-4."""
+    keys, page, gap = 20000, 64, 24.5
+    pages = (keys + page - 1) // page
+    kc = torch.zeros(pages, heads, page, dim, dtype=torch.int8, device=DEV)
+    vc = torch.full_like(kc, -1)
+    kc[0, :, 5, 0], vc[0, :, 5] = 127, 1
+    one = torch.ones(pages, heads, page, device=DEV)
+    q = torch.zeros(new, heads, dim, device=DEV)
+    q[:, :, 0] = gap / np.log2(np.e) / 127
+    c = q4.kv_cache8(kc, vc, one, one.clone())
+    assert q4.q4_0_select_attention8(c, heads, q4.F32, new, pages, 1) == rows
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    y = q4.attention(c, q, i32(0, new), i32(keys),
+                     torch.arange(pages, dtype=torch.int32, device=DEV)[None], scale=1.0)
+    faint = np.exp(-127 * float(q[0, 0, 0])) * np.arange(keys - new, keys)
+    want = ((1 - faint) / (1 + faint))[:, None, None]
+    # sums beside the strong key's: at most 96 tiles of 64 keys, each four products of two
+    # parts (off by a step, 2^-23, at most) and a sum (2^-24); then a dozen such sums
+    near(y, np.broadcast_to(want, y.shape), (96 * (8 * 2 + 1) + 24 + gap * 2) * H32 * np.ones(y.shape))
+
+
 @pytest.mark.parametrize("half", [True, False])
 def test_attention8_rows_that_see_nothing(half):
     check8([(10, 4), (3, 0), (1, 0), (40, 20), (2, 2)], 4, 2, 64, 16, 0, 0, half, seed=8)
