@@ -989,8 +989,10 @@ int q4_0_verify(const void *logits, int64_t stride, const void *drafted, int64_t
         !aligned(q_start, 4) || !aligned(temperature, 4) || !aligned(uniform, 4) ||
         !aligned(accepted, 4) || !aligned(next, 4))
         return Q4_0_EALIGN;
+    // (the last row of `drafted` judges nothing: it need not be there)
+    const size_t judged = drafted && n > 1 ? rows_bytes(n - 1, drafted_stride, vocab, el) : 0;
     const Span spans[8] = {{logits, rows_bytes(n, stride, vocab, el)},
-                           {drafted, drafted ? rows_bytes(n, drafted_stride, vocab, el) : 0},
+                           {drafted, judged},
                            {tokens, (size_t)n * 4u},
                            {q_start, (size_t)(batch + 1) * 4u},
                            {temperature, (size_t)batch * 4u},

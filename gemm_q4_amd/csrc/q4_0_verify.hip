@@ -254,13 +254,12 @@ __device__ __forceinline__ float heat_of(const VerifyArgs &a, int s) {
 }
 
 // ---- every part of every row ------------------------------------------------
-// A part to W waves of a workgroup.  Four where there are few: the chain is as short
-// as it gets, and every row is requested before the conversation that holds it is
-// known; otherwise the draft's rows only then, since of those one in each
-// conversation is not needed, and none of the greedy ones.
+// A part to W waves of a workgroup, four where there are few: the chain is as short as
+// it gets.  A row of logits is requested before the conversation that holds it is
+// known, the draft's only then: those that judge nothing (each conversation's last, all
+// of a greedy one) need not be there.
 template <bool F16, int W>
 __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *stats, int parts) {
-    constexpr bool EAGER = W > 1;
     constexpr int kParts = kWaves / W, kMine = kLoads / W;
     __shared__ double table[256];
     __shared__ double sums[W];
@@ -275,14 +274,14 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
     f4_t l[kMine];
     const void *x = drafted ? row_of<F16>(a.drafted, row, a.drafted_stride)
                             : row_of<F16>(a.logits, row, a.stride);
-    if (EAGER || !drafted) load_part<F16>(l, x, part, a.vocab, from);
+    if (!drafted) load_part<F16>(l, x, part, a.vocab, from);
     fill_table(table);
     Span sp;
     if (!span_of(a, holder(a, row), sp) || row < sp.first || row > sp.last) return;
     const float heat = heat_of(a, sp.s);
     const bool cold = !(heat > 0.0f);
     if (drafted && (row == sp.last || cold)) return;
-    if (!EAGER && drafted) load_part<F16>(l, x, part, a.vocab, from);
+    if (drafted) load_part<F16>(l, x, part, a.vocab, from);
     const int draft = row < sp.last ? a.tokens[row + 1] : -1;
     __syncthreads();
     if (part >= parts) return;  // (waves that share no part)

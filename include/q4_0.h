@@ -533,7 +533,9 @@ int q4_0_embed(const void *packed, const int32_t *tokens, int64_t n, int64_t out
  * T no number) the target is its greatest logit, the lowest token where several
  * are: drafts equal to it are taken and next is the first that would have been.
  *   logits  : DEVICE [n] rows of vocab elements of x_dtype, `stride` apart.
- *   drafted : DEVICE rows likewise, or NULL.  Rows that judge nothing are not read.
+ *   drafted : DEVICE rows likewise, or NULL.  Rows that judge nothing (each
+ *             conversation's last, all of one with T not above 0, those that no
+ *             conversation holds) are not read and need not be there.
  *   tokens  : DEVICE int32 [n], the step's own tokens (q4_0_embed's).  A draft outside
  *             [0, vocab) is refused (without `drafted` next is then drawn from p).
  *   q_start : DEVICE int32 [batch + 1], 0 <= q_start[s] <= q_start[s+1] <= n.  A

@@ -187,6 +187,17 @@ def test_verify_workspace():
     assert status_of(size, 65536, 1, q4.MAX_OUT) == q4.EUNSUPPORTED
 
 
+def test_verify_draft_logits_without_their_last_row():
+    """The last row judges nothing: what lies where it would be is no overlap."""
+    last = B + 5 * 1000 * 4
+    near = dict(workspace=0, workspace_bytes=0)        # refused, but after the overlaps
+    assert status_of(q4.q4_0_verify, *verify_args(accepted=last, **near)) == q4.EWORKSPACE
+    assert status_of(q4.q4_0_verify, *verify_args(accepted=last - 4, **near)) == q4.EALIAS
+    one = dict(n=1, batch=1, **near)
+    assert status_of(q4.q4_0_verify, *verify_args(accepted=B, **one)) == q4.EWORKSPACE
+    assert status_of(q4.q4_0_verify, *verify_args(accepted=A, **one)) == q4.EALIAS
+
+
 # ---- the conveniences --------------------------------------------------------
 def host_cache(pages=2, heads=2, page=16, dim=64):
     k = torch.zeros(pages, heads, page, dim, dtype=torch.int8)
