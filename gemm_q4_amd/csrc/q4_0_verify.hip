@@ -8,10 +8,11 @@
 // A draw is a border among up to 10^5 shares, so weights and sums are 64-bit: the
 // same token comes out whatever the order of the sums.  A weight 2^x is a table's
 // entry (256 of them) times a polynomial of the third degree, off by 2e-13; weights
-// below 2^-980 of a row's largest count as none.
+// below 2^-980 of a row's largest count as none, in every kernel by the same comparison,
+// so that a part has a share exactly if a token in it has a weight.
 //
 // stats: every part of every row, one read: its largest logit and the sum of its
-// weights (without draft logits: of all but the judged draft's, so that taking it
+// weights (without draft logits both of all but the judged draft, so that taking it
 // out costs no digits).  judge: each conversation's first refused draft.  rest (with
 // draft logits): sums of max(p - q, 0) over the parts of that row.  pick: the part
 // that the number falls into, then the token.  Few parts: rest judges, three launches.
@@ -42,12 +43,12 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kPickThreads = 512;  // of the others: one part, or eight rows judged at once
 constexpr int kPickWaves = kPickThreads / 64;
 constexpr int kHeld = 2;           // parts that a lane keeps: rows of 262144 tokens need no more
-constexpr double kFaint = 0x1p-980;
 
 // A part of a row: its largest logit, the sum of its weights relative to that
-// logit, and `at`: of a greedy row the first token that has the largest, else (as
-// bits) the judged draft's logit, where it is in this part.  A sum that is no
-// number: the part holds a logit that is NaN or plus infinity.
+// logit (without draft logits the judged draft is in neither), and `at`: of a greedy
+// row the first token that has the largest, else (as bits) the judged draft's logit,
+// where it is in this part.  A sum that is no number: the part holds a logit that is
+// NaN or plus infinity.
 struct Stat {
     double sum;
     float top;
@@ -94,8 +95,10 @@ __device__ __forceinline__ void fill_table(double *table) {
 struct Power {
     const double *table;
     double c, least;  // 256 log2(e) / T, and the difference that stands for all below
+    double faint;     // differences below this one have no weight
     __device__ __forceinline__ Power(const double *t, double heat)
-        : table(t), c(369.3299304675746 / heat), least(-1010.0 * 0.6931471805599453 * heat) {}
+        : table(t), c(369.3299304675746 / heat), least(-1010.0 * 0.6931471805599453 * heat),
+          faint(-980.0 * 0.6931471805599453 * heat) {}
     // Sum of the weights of N differences, side by side: a single one is a chain of
     // ten operations and an LDS read.  None is below about 2^-1010, so that the
     // exponent is a plain addition.
@@ -125,12 +128,18 @@ struct Power {
                                               << 32 |
                                           (uint32_t)t[i]);
     }
-    // One, 0 below that.
+    // The same, 0 where there is none.
+    template <int N>
+    __device__ __forceinline__ void exact(const double (&d)[N], double (&w)[N]) const {
+        of(d, w);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = d[i] >= faint ? w[i] : 0.0;
+    }
     __device__ __forceinline__ double exact(double d) const {
         const double one[1] = {d};
         double w[1];
-        of(one, w);
-        return d > least ? w[0] : 0.0;
+        exact(one, w);
+        return w[0];
     }
 };
 
@@ -286,6 +295,18 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
     __syncthreads();
     if (part >= parts) return;  // (waves that share no part)
     const int base = part * kPart + from * 256 + lane * 4;
+    const bool judged = !cold && draft >= part * kPart && draft < min(part * kPart + kPart, a.vocab);
+    float its = -INFINITY;
+    if (judged) {
+        its = load1<F16>(x, draft);
+        if (!a.drafted) {
+            const int at = draft - base;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) l[i][e] = at == i * 256 + e ? -INFINITY : l[i][e];
+        }
+    }
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
@@ -298,8 +319,8 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
 #pragma unroll
         for (int i = 0; i < W; ++i) top = larger(top, tops[i]);
     }
-    Stat st = {0.0, top, INT32_MAX};
-    if (!(top <= FLT_MAX)) {
+    Stat st = {0.0, top, judged ? __builtin_bit_cast(int, its) : INT32_MAX};
+    if (!(larger(top, its) <= FLT_MAX)) {
         st.sum = NAN;
     } else if (top == -INFINITY) {
     } else if (cold) {
@@ -323,30 +344,14 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
         const Power power(table, heat);
         const double m = top;
         double sum = 0.0;
-        const bool judged = draft >= part * kPart && draft < min(part * kPart + kPart, a.vocab);
-        if (judged) st.at = __builtin_bit_cast(int, load1<F16>(x, draft));
-        if (judged && !a.drafted) {
-            // the judged draft's weight stays out
-#pragma nounroll
-            for (int i = 0; i < kMine; ++i) {
-                const f4_t again = load4<F16>(x, base + i * 256, a.vocab);
-                double d[4], w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[e] = (double)again[e] - m;
-                power.of(d, w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum += base + i * 256 + e == draft ? 0.0 : w[e];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4 * kMine; i += 2) {
-                const double d[2] = {(double)l[i / 4][i % 4] - m, (double)l[i / 4][i % 4 + 1] - m};
-                double w[2];
-                power.of(d, w);
-                sum += w[0];
-                sum += w[1];
-                __builtin_amdgcn_sched_barrier(0);  // else all are formed side by side
-            }
+        for (int i = 0; i < 4 * kMine; i += 2) {
+            const double d[2] = {(double)l[i / 4][i % 4] - m, (double)l[i / 4][i % 4 + 1] - m};
+            double w[2];
+            power.of(d, w);
+            sum += w[0];
+            sum += w[1];
+            __builtin_amdgcn_sched_barrier(0);  // else all are formed side by side
         }
         sum = wave_sum(sum);
         if (W > 1) {
@@ -356,14 +361,14 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Stat *
 #pragma unroll
             for (int i = 0; i < W; ++i) sum += sums[i];
         }
-        st.sum = sum < kFaint ? 0.0 : sum;
+        st.sum = sum;  // (of 1 and more)
     }
     if (lane == 0 && wave % W == 0) stats[(row + (drafted ? (int64_t)a.n : 0)) * parts + part] = st;
 }
 
 // ---- the refused draft ------------------------------------------------------
-// A row's distribution: largest logit, its first token, total weight (without the
-// judged draft's where stats left it out); `fine` if it is one.
+// A row's distribution: largest logit (`its`, the judged draft's, included), its first
+// token, total weight (without the draft's where stats left it out); `fine` if it is one.
 struct Whole {
     double sum;
     float top;
@@ -383,9 +388,9 @@ struct Parts {
 };
 // By all lanes of a wave.
 __device__ __forceinline__ Whole whole_of(const Stat *stats, const Parts &held, int parts,
-                                          bool cold, const Power &power) {
+                                          bool cold, const Power &power, float its) {
     const int lane = threadIdx.x % 64;
-    Whole w = {0.0, -INFINITY, INT32_MAX, true};
+    Whole w = {0.0, its, INT32_MAX, true};
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) w.top = larger(w.top, held.of[i].top);
     for (int i = lane + 64 * kHeld; i < parts; i += 64) w.top = larger(w.top, stats[i].top);
@@ -410,18 +415,12 @@ __device__ __forceinline__ float drafted_logit(const Stat *stats, const Parts &h
                                                bool real) {
     if (!real) return -INFINITY;
     const int part = draft / kPart;
-    Stat st;
-    if (part < 64 * kHeld) {
-        const Stat &mine = held.of[0];
-        st.top = __builtin_bit_cast(
-            float, __builtin_amdgcn_readlane(
-                       __builtin_bit_cast(int, part < 64 ? mine.top : held.of[1].top), part % 64));
-        st.at = __builtin_amdgcn_readlane(part < 64 ? mine.at : held.of[1].at, part % 64);
-    } else {
-        st = stats[part];
-    }
-    // (a part of minus infinities alone has noted none)
-    return st.top == -INFINITY ? st.top : __builtin_bit_cast(float, st.at);
+    int at;
+    if (part < 64 * kHeld)
+        at = __builtin_amdgcn_readlane(part < 64 ? held.of[0].at : held.of[1].at, part % 64);
+    else
+        at = stats[part].at;
+    return __builtin_bit_cast(float, at);
 }
 
 // The first row of the conversation whose draft is refused (its last row, if none
@@ -450,7 +449,8 @@ __device__ __forceinline__ Verdict judge(const VerifyArgs &a, const Stat *stats,
         __syncthreads();  // (the table, in the first round)
         if (row <= sp.last) {
             const bool real = v.draft >= 0 && v.draft < a.vocab;
-            const Whole p = whole_of(ps, of_p, parts, cold, power);
+            const float its = drafted_logit(ps, of_p, v.draft, real && !cold);
+            const Whole p = whole_of(ps, of_p, parts, cold, power, its);
             v.p_top = p.top;
             v.at = p.at;
             if (!p.fine) {
@@ -458,19 +458,18 @@ __device__ __forceinline__ Verdict judge(const VerifyArgs &a, const Stat *stats,
             } else if (cold) {
                 if (last || v.draft != p.at) v.how = kGreedy;
             } else {
-                const double wd =
-                    power.exact((double)drafted_logit(ps, of_p, v.draft, real) - (double)p.top);
+                const double wd = power.exact((double)its - (double)p.top);
                 v.p_share = 1.0 / (p.sum + (a.drafted ? 0.0 : wd));
                 if (last) {
                     v.how = kPlain;
                 } else if (!drafted) {
                     if (!((double)u < wd * v.p_share)) v.how = real ? kWithout : kPlain;
                 } else {
-                    const Whole q = whole_of(qs, of_q, parts, false, power);
+                    const float its_q = drafted_logit(qs, of_q, v.draft, real);
+                    const Whole q = whole_of(qs, of_q, parts, false, power, its_q);
                     v.q_top = q.top;
                     v.q_share = 1.0 / q.sum;
-                    const double qd = power.exact((double)drafted_logit(qs, of_q, v.draft, real) -
-                                                  (double)q.top) * v.q_share;
+                    const double qd = power.exact((double)its_q - (double)q.top) * v.q_share;
                     if (!q.fine)
                         v.how = kNone;
                     else if (!((double)u * qd < wd * v.p_share))
@@ -547,7 +546,7 @@ __global__ __launch_bounds__(kPickThreads) void rest_kernel(VerifyArgs a, const 
         d[e] = (double)l[0][e] - (double)v.p_top;
         d[4 + e] = (double)g[0][e] - (double)v.q_top;
     }
-    power.of(d, w);
+    power.exact(d, w);
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum += above(w[e], v.p_share, w[4 + e], v.q_share);
     sum = wave_sum(sum);
@@ -557,7 +556,7 @@ __global__ __launch_bounds__(kPickThreads) void rest_kernel(VerifyArgs a, const 
     sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kPickWaves; ++i) sum += sums[i];
-    rests[(int64_t)s * parts + part] = sum < kFaint ? 0.0 : sum;
+    rests[(int64_t)s * parts + part] = sum;
 }
 
 // ---- the next token ---------------------------------------------------------

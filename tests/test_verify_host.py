@@ -100,3 +100,76 @@ def test_rows_that_judge_nothing_are_not_read(run, cus):
     agree(run, args, heat=heat[1:-1], cus=cus, marked=unjudged(args[2], 12, heat[1:-1]))
     one = rows_of(rng, [1], 300)
     agree(run, one, cus=cus, marked=np.ones(1, np.uint8))
+
+
+# ---- weights next to nothing ---------------------------------------------------
+# A weight below 2^-980 of its row's largest counts as none: a logit 679.3 below it.
+def faint_rows():
+    """(logits, tokens, uniform, next): rows of two (a pick that is refused, then the
+    row after it) of 5000 tokens, three parts."""
+    def row(**at):
+        x = np.full(5000, -np.inf, np.float32)
+        for k, v in at.items():
+            x[int(k[1:])] = v
+        return x
+    return [
+        # the last part holds the draft, and a token whose weight beside the draft's is one and
+        # beside the row's largest is none
+        (row(t7=0.0, t4500=-450.0, t4600=-740.0), 4500, 1.0, 7),
+        (row(t7=0.0, t4500=-600.0, t4600=-690.0), 4500, 2.0, 7),
+        # .. and one whose weight is just one beside the row's largest
+        (row(t7=0.0, t4500=-450.0, t4600=-679.0), 4500, 1.0, 4600),
+        # the draft is the row's largest: nothing else has a weight, or just one token
+        (row(t7=-680.0, t4500=0.0, t4600=-690.0), 4500, 0.5, 4500),
+        (row(t7=-680.0, t4500=0.0, t4600=-679.0), 4500, 0.5, 4600),
+        (row(t7=-679.0, t4500=0.0, t4600=-680.0), 4500, 1.0, 7),
+        # the draft's part holds nothing else
+        (row(t7=3.0, t4500=3.0), 4500, 1.0, 7),
+        (row(t4500=3.0), 4500, 0.0, 4500),
+        # the lowest token with a weight, in the part of the others and in one of its own
+        (row(t7=-680.0, t8=-679.0, t9=0.0, t20=0.0), 9, 0.0, 8),
+        (row(t7=-680.0, t3000=-679.0, t4500=0.0), 20, 0.0, 3000),
+        (row(t7=-680.0, t3000=-690.0, t4500=0.0, t4999=-680.0), 20, 1.0, 4500),
+    ]
+
+
+@pytest.mark.parametrize("cus", [256, 1])
+def test_faint_weights(run, cus):
+    cases = faint_rows()
+    n = 2 * len(cases)
+    logits, tokens = np.zeros((n, 5000), np.float32), np.zeros(n, np.int32)
+    uniform = np.full((n, 2), 2.0, np.float32)
+    for i, (row, draft, u, _) in enumerate(cases):
+        logits[2 * i], tokens[2 * i + 1], uniform[2 * i, 1] = row, draft, u
+    start = np.arange(0, n + 1, 2, dtype=np.int32)
+    accepted, following = run(logits, tokens, start, uniform, cus=cus)
+    assert accepted.tolist() == [0] * len(cases)
+    assert following.tolist() == [c[3] for c in cases]
+    # with temperatures: logits as many times as far apart (a power of two: exactly)
+    heat = np.full(len(cases), 0.25, np.float32)
+    assert run(logits / 4, tokens, start, uniform, heat=heat, cus=cus)[1].tolist() == [
+        c[3] for c in cases]
+    # one row each, nothing refused: all of p
+    rows, us = logits[::2], np.array([[0.0, x] for x in (0.0, 1.0)], np.float32)
+    for u in us:
+        _, t = run(rows, tokens[::2], np.arange(len(rows) + 1, dtype=np.int32),
+                   np.tile(u, (len(rows), 1)), cus=cus)
+        for x, got in zip(rows, t.tolist()):
+            some = np.nonzero(x - x.max() >= -679.28)[0]
+            assert got == (some[0] if u[1] == 0.0 else some[-1])
+
+
+@pytest.mark.parametrize("cus", [256, 1])
+def test_faint_weights_of_draft_models(run, cus):
+    """Where the target has next to nothing, and where the draft has."""
+    p, q = (np.full((2, 5000), -np.inf, np.float32) for _ in range(2))
+    p[0, [5, 3000]] = 0.0
+    q[0, 5] = 0.0
+    p[0, 4000:4900] = -682.0                            # 900 of 2^-984: more than 2^-980 together
+    run2 = lambda u: run(p, np.array([0, 5], np.int32), np.array([0, 2], np.int32),
+                         np.array([[1.5, u], [0, 0]], np.float32), q, cus=cus)
+    assert [int(run2(u)[1][0]) for u in (0.0, 0.5, 1.0)] == [3000] * 3
+    p[0, 4800] = -679.0
+    assert [int(run2(u)[1][0]) for u in (0.5, 1.0)] == [3000, 4800]
+    q[0, 4800] = 0.0
+    assert int(run2(1.0)[1][0]) == 3000
