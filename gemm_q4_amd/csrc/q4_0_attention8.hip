@@ -11,12 +11,21 @@
 // under the exponent byte 0x64 reads as 1024 + 128 + c; one packed subtraction
 // leaves c.  Five instructions for four codes.
 //
-// A value's weight is p t with p = exp(x - m) in float32, t brought to the
-// largest scale met so far (a power of two, so without rounding) before it is
-// multiplied; that running exponent is lifted, and what is accumulated rescaled,
-// like the maximum of the softmax.  The scales of keys that no row of a tile sees
-// are taken as 0 and their codes are finite whatever they are, so what a page
-// holds past its conversation's end never meets the arithmetic.
+// A value's weight is p t with p = exp(x - m) in float32, which enters its product in
+// binary16 parts.  While all scales t of a wave's keys lie within some powers of two, t
+// is brought to the largest met so far (a power of two, so without rounding) before it
+// is multiplied; that running exponent is lifted, and what is accumulated rescaled,
+// like the maximum of the softmax.  A row's strongest key then has a weight that
+// binary16 holds in full.  Where a tile's scales lie further apart than that (a token
+// whose values are a thousand times another's, seen by other rows of the tile, or with
+// next to no weight) the tile is done again with an exponent of its own for every row, of
+// the largest p t among the keys it sees: in blocks of 16 rows, by code apart, so that
+// the usual loops have none of its instructions and registers.  The scales of keys that
+// no row of a tile sees are taken as 0 and their codes are finite whatever they are, so
+// what a page holds past its conversation's end never meets the arithmetic.  (One key
+// half way with a scale 2^12 below the others': 64 conversations 191 us instead of 101,
+// prompts 1075 instead of 320; a loop that keeps every row's own exponent at all times
+// would take half as many instructions again.)
 //
 // A score is formed less the running maximum, by one fused operation on its product:
 // scores of any size lose nothing, and while the maximum holds its exponential
@@ -64,6 +73,20 @@ __device__ __forceinline__ void dma4(const void *src, uint8_t *lds) {
 
 static __device__ const uint32_t kNanWord = 0x7FC00000u;
 
+// A launch's arguments; `base`: the first of its tiles.
+struct Call {
+    AttentionArgs a;
+    Plan pl;
+    int base;
+};
+// They once more, from memory: a rare path that took them from the kernel's own would
+// keep registers for them through the usual one.
+__device__ __forceinline__ const Call &call_again() {
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const Call *)p;
+}
+
 // x of the four lanes l, l + 16, l + 32, l + 48 joined.
 template <typename F> __device__ __forceinline__ float quads(float x, F f) {
     uint32_t u = __builtin_bit_cast(uint32_t, x);
@@ -84,18 +107,68 @@ __device__ __forceinline__ float quads_sum(float x) {
 // The exponent that brings a scale into [1/2, 1); far below any for 0 and for
 // what is no number.
 constexpr int kNoExponent = -1000;
+// The same where exponents are compared with maxima of scores: below any of those too.
+constexpr float kNever = 1e6f;
+// Powers of two that the scales of a row's keys may lie apart for one exponent to do.
+// The strongest key's weight is then 2^(kShift - 1 - kSpread) or more, where half a step
+// of the least numbers is 2^-25.
+constexpr int kSpread = 10;
 __device__ __forceinline__ int exponent(float t) {
     const float a = fabsf(t);
     return a > 0.0f && a <= FLT_MAX ? __builtin_amdgcn_frexp_expf(a) : kNoExponent;
 }
-__device__ __forceinline__ int wave_max(int x) {
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) x = max(x, __shfl_xor(x, i));
-    return uniform(x);
+template <int CTRL> __device__ __forceinline__ int turned_max(int x) {
+    return max(x, __builtin_amdgcn_mov_dpp(x, CTRL, 0xF, 0xF, true));
 }
-// A value's scale relative to 2^top; one that is infinite is no number either.
+// By lane moves alone: LDS permutes would be a chain of six latencies.
+__device__ __forceinline__ int wave_max(int x) {
+    x = turned_max<0x121>(x);  // within 16 lanes, turned by one, two, four, eight
+    x = turned_max<0x122>(x);
+    x = turned_max<0x124>(x);
+    x = turned_max<0x128>(x);
+    auto r = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    x = max((int)r[0], (int)r[1]);
+    r = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
+    return uniform(max((int)r[0], (int)r[1]));
+}
+// A value's scale, relative to 2^top; one that is infinite is no number either.
+__device__ __forceinline__ float number(float t) { return fabsf(t) <= FLT_MAX ? t : NAN; }
 __device__ __forceinline__ float relative(float t, int top, int shift) {
-    return fabsf(t) <= FLT_MAX ? __builtin_amdgcn_ldexpf(t, shift - top) : NAN;
+    return __builtin_amdgcn_ldexpf(number(t), shift - top);
+}
+
+// The exponents of the scales that a wave has met: the largest and the smallest.
+struct Span8 {
+    int top = kNoExponent, low = -kNoExponent;
+    __device__ __forceinline__ bool apart() const { return top - low > kSpread; }
+    // `mine` (this lane's scale; by all lanes) taken in: whether that changed them.
+    __device__ __forceinline__ bool take(float mine) {
+        const int e = exponent(mine);
+        if (!__any(e > top || (e != kNoExponent && e < low))) return false;
+        top = max(wave_max(e), top);
+        low = min(-wave_max(e == kNoExponent ? e : -e), low);
+        return true;
+    }
+};
+
+// A row's own exponent as the ceiling of `ref`, the power of two of the largest weight
+// (p t) that the row has met, relative to its maximum of the softmax.
+__device__ __forceinline__ int own_exponent(float ref) { return (int)ceilf(ref); }
+// p times the mantissa of the scale t, and the power of two of p t (none for 0, and for
+// what is no number).
+__device__ __forceinline__ float mantissa(float p, float t) {
+    return p * __builtin_amdgcn_frexp_mantf(t);
+}
+__device__ __forceinline__ float power(float z, float t) {
+    return fabsf(z) > 0.0f ? (float)(__builtin_amdgcn_frexp_expf(z) + __builtin_amdgcn_frexp_expf(t))
+                           : -kNever;
+}
+// `ref` after the maximum rose by `u` powers of two and a tile's largest weight is 2^most;
+// what is accumulated is multiplied by the result (less than 4, 0 for what has vanished).
+__device__ __forceinline__ float lifted_to(float &ref, float u, float most) {
+    const int was = own_exponent(ref);
+    ref = fmaxf(fmaxf(ref - u, most), -kNever);
+    return __builtin_amdgcn_exp2f((float)(was - own_exponent(ref)) - u);
 }
 
 // The cache as a tile's loads see it: head hk of the pages of conversation s.
@@ -167,10 +240,10 @@ template <int DIM> struct StepFiller : Source {
     static constexpr int kCopies = DIM / 64;  // of 16 rows, 1 KB each
     static constexpr int kAll = kStepKeys / 16 * kCopies + 1;  // a tile's, of K or of V
     static constexpr int kCodes = kStepKeys * DIM;
+    const int lane;
     uint32_t off[2][kCopies];
-    __device__ __forceinline__ StepFiller(const AttentionArgs &a, int s, int hk)
-        : Source(a, s, hk) {
-        const int lane = threadIdx.x % 64;
+    __device__ __forceinline__ StepFiller(const AttentionArgs &a, int s, int hk, int lane_)
+        : Source(a, s, hk), lane(lane_) {
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -183,7 +256,6 @@ template <int DIM> struct StepFiller : Source {
     template <bool ONCE>
     __device__ __forceinline__ void fill(const Reach<kStepKeys> &r, const int (&page)[4], int key,
                                          uint8_t *lds, bool is_v) const {
-        const int lane = threadIdx.x % 64;
         uint8_t *dst = lds + (is_v ? kCodes : 0);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -209,14 +281,15 @@ template <int DIM> struct StepFiller : Source {
 // A block of 16 rows: queries, running maximum (of scores without `c`; 0 before the
 // first), sum (this lane's keys) and unnormalised result.  A score above the maximum
 // by more than `over` lifts it (any does, the first time).  Weights are held in two
-// binary16 parts, as 2^kShift of the largest.
+// binary16 parts, as 2^kShift of the largest: what is lost of one is 2^-28 of the row's
+// strongest key's or less, 2^-38 with the row's own exponent, `ref`.
 template <int DIM, bool F32> struct Block {
     static constexpr int kParts = F32 ? 2 : 1;  // of q
     static constexpr float kLag = 1.0f;
     static constexpr int kShift = 14;
     h8_t q[kParts][DIM / 32];
     f4_t o[DIM / 16];
-    float m, l, c, over;
+    float m, l, c, over, ref;
     int p, lo;
 
     struct Raw {
@@ -225,8 +298,7 @@ template <int DIM, bool F32> struct Block {
     // Row r (of the conversation's `rows`); rows past the end repeat the last.
     // Lane l holds elements 64 j + 16 (l / 16) + 0..15 of row l % 16.
     __device__ __forceinline__ void request(Raw &raw, const AttentionArgs &a, const Place &pl,
-                                            int group, int hk, int r, int position0) {
-        const int g = threadIdx.x % 64 / 16;
+                                            int group, int hk, int r, int position0, int g) {
         const int rr = min(r, pl.rows - 1);
         const int token = rr / group;
         p = position(a, position0, token);
@@ -244,6 +316,7 @@ template <int DIM, bool F32> struct Block {
     __device__ __forceinline__ void clear() {
         m = 0.0f;
         over = -INFINITY;
+        ref = -kNever;
         l = 0.0f;
 #pragma unroll
         for (int d = 0; d < DIM / 16; ++d) o[d] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -284,8 +357,10 @@ template <int DIM, bool F32> struct Block {
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[d][i] *= f;
     }
-    // Scores of 64 keys, less the maximum, to weights; the maximum brought along.
-    __device__ __forceinline__ void soften(f4_t (&s)[4]) {
+    // Scores of 64 keys, less the maximum, to weights; the maximum brought along.  By how
+    // many powers of two it rose; APART: `o` is yet to fall by as much.
+    template <bool APART> __device__ __forceinline__ float soften(f4_t (&s)[4]) {
+        float u = 0.0f;
         float top = -INFINITY;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
@@ -293,14 +368,16 @@ template <int DIM, bool F32> struct Block {
             for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
         top = quads_max(top);
         if (__any(top * c > over)) {
+            // (rows that need not be lifted stay as they are, whatever the others do)
             const bool first = over == -INFINITY;
-            const float to = m + (first ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f));
+            const float to = top * c > over ? m + top : m;
             const float up = to - m;
             const float f = first ? 1.0f : factor_of(-up * c);
+            u = first ? kNever : up * c;
             if (top != -INFINITY) over = kLag;
             m = to;
             l *= f;
-            rescale(f);
+            if (!APART) rescale(f);
 #pragma unroll
             for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -315,6 +392,33 @@ template <int DIM, bool F32> struct Block {
                 sum += s[b][i];
             }
         l += sum;
+        return u;
+    }
+    // Weights of 64 keys times their scales, relative to the row's own exponent, which
+    // `most` lifts.  `hidden`: keys that the row does not see.
+    __device__ __forceinline__ void weigh(f4_t (&s)[4], const float *scales, uint32_t hidden,
+                                          float u) {
+        float most = -kNever;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const f4_t t = *(const f4_t *)(scales + 16 * b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[b][e] = hidden >> (4 * b + e) & 1 ? 0.0f : mantissa(s[b][e], t[e]);
+                most = fmaxf(most, power(s[b][e], t[e]));
+            }
+        }
+        rescale(lifted_to(ref, u, quads_max(most)));
+        asm volatile("" ::: "memory");  // (the scales are read again, not held)
+        const int down = kShift - own_exponent(ref);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const f4_t t = *(const f4_t *)(scales + 16 * b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[b][e] = __builtin_amdgcn_ldexpf(s[b][e],
+                                                  __builtin_amdgcn_frexp_expf(t[e]) + down);
+        }
     }
     // The maximum in powers of two, minus infinity if there was none.
     __device__ __forceinline__ float top() const { return over == -INFINITY ? over : m * c; }
@@ -323,14 +427,16 @@ template <int DIM, bool F32> struct Block {
 //
 // One tile's room to a wave: K is requested again as soon as the scores are formed, V
 // as soon as it is mixed, and the other waves cover what that leaves open.
-template <int DIM, bool F32, bool ONCE, int NR>
+// APART: every row has its own exponent.  Without, the loop ends early where scales lie too
+// far apart for one (span.apart()): what it leaves is of no use then.
+template <int DIM, bool F32, bool ONCE, int NR, bool APART>
 __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFiller<DIM> &f,
                                           const Reach<kStepKeys> &r, int t, int t1, int stride,
-                                          int top_lo, uint8_t *lds, int (&look)[4], int &top,
+                                          int top_lo, uint8_t *lds, int (&look)[4], Span8 &span,
                                           float k_factor) {
     using B = Block<DIM, F32>;
     constexpr int kAll = StepFiller<DIM>::kAll, kCodes = StepFiller<DIM>::kCodes;
-    const int lane = threadIdx.x % 64, g = lane / 16;
+    const int lane = f.lane, g = lane / 16;
     // lane i of 16 names the address of half a piece of the (i / 2)-th of its
     // eight keys and receives column i of all eight
     const int i2 = lane % 16 / 2;
@@ -413,38 +519,49 @@ __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFi
             for (int x = 0; x < 4; ++x) page[x] = __builtin_amdgcn_readlane(look[x], i);
             f.template fill<ONCE>(r, page, next, lds, false);
         }
+        float u[NR];
 #pragma unroll
-        for (int n = 0; n < NR; ++n) w[n].soften(s[n]);
+        for (int n = 0; n < NR; ++n) u[n] = w[n].template soften<APART>(s[n]);
         // outstanding: V, then the next K
         if (more)
             Q4_WAIT_VMCNT(kAll);
         else
             Q4_WAIT_VMCNT(0);
         asm volatile("" ::: "memory");
-        // V's scales against the largest so far
         {
             const float t4 = vsc[lane];
-            const int e = exponent(t4);
-            if (__any(e > top)) {
-                const int up = max(wave_max(e), top);
-                const float fall = __builtin_amdgcn_ldexpf(1.0f, top - up);
+            if (!APART) {
+                // V's scales against the largest so far
+                const int was = span.top;
+                if (span.take(t4)) {
+                    // (no way out of the loop here, which would cost registers: the next
+                    // tile, whose keys are on their way, is the last)
+                    if (__builtin_expect(span.apart(), 0)) t1 = min(t1, t + 2 * stride);
+                    const float fall = __builtin_amdgcn_ldexpf(1.0f, was - span.top);
 #pragma unroll
-                for (int n = 0; n < NR; ++n) w[n].rescale(fall);
-                top = up;
+                    for (int n = 0; n < NR; ++n) w[n].rescale(fall);
+                }
+                vsc[lane] = relative(t4, span.top, B::kShift);
+            } else {
+                vsc[lane] = number(t4);
             }
-            vsc[lane] = relative(t4, top, B::kShift);
         }
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
+        if (APART) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const f4_t x = *(const f4_t *)(vsc + 16 * b + 4 * g);
+            for (int n = 0; n < NR; ++n) w[n].weigh(s[n], vsc + 4 * g, hidden[n], u[n]);
+        } else {
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+            for (int b = 0; b < 4; ++b) {
+                const f4_t x = *(const f4_t *)(vsc + 16 * b + 4 * g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][b][e] *= x[e];
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][b][e] *= x[e];
+            }
         }
-        if (masked) {
+        if (!APART && masked) {
             asm volatile("; masked tile");
 #pragma unroll
             for (int n = 0; n < NR; ++n)
@@ -485,11 +602,13 @@ __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFi
     }
 }
 
-// One tile of up to 16 NR rows by a workgroup of W waves.
-template <int DIM, bool F32, bool ONCE, int W, int NR>
-__device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl, const Place &at,
-                                          int hk, int split, int row0, int row1, uint8_t *lds,
-                                          float (*ml)[W][kStepRows]) {
+// Rows `first` to `last` (up to 16 NR) of the tile of rows row0 to row1, by W waves.  True
+// if the scales of a wave's keys lie too far apart (without APART): nothing is written.
+template <int DIM, bool F32, bool ONCE, int W, int NR, bool APART>
+__device__ __forceinline__ bool step_tile(const AttentionArgs &a, const Plan &pl, const Place &at,
+                                          int hk, int split, int row0, int row1, int first,
+                                          int last, uint8_t *lds, float (*ml)[W][kStepRows],
+                                          uint32_t *votes, int wave) {
     constexpr int kPitch = DIM + 4, kShare = kStepRows * kPitch * 4;
     static_assert(2 * StepFiller<DIM>::kCodes + 2 * kStepKeys * 4 <= kShare && kShare % 256 == 0,
                   "a wave's tile, later its rows");
@@ -499,10 +618,15 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
     const Reach<kStepKeys> r(a, p0, p1);
     const int top_lo = a.window && p1 >= a.window ? p1 - a.window + 1 : 0;
     const int per = max((r.tiles + pl.splits - 1) / pl.splits, pl.least);
-    const int t0 = min(split * per, r.tiles), t1 = min(t0 + per, r.tiles);
-    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), g = lane / 16;
+    const int t0 = min(split * per, r.tiles);
+    const int t1 = first < last ? min(t0 + per, r.tiles) : t0;
+    // (two ways to name the lane: what the usual path has computed from it would else be
+    // kept through its loop for the other)
+    const int lane = APART ? __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u))
+                           : threadIdx.x % 64;
+    const int g = lane / 16;
     uint8_t *mine = lds + wave * kShare;
-    const StepFiller<DIM> f(a, at.s, hk);
+    const StepFiller<DIM> f(a, at.s, hk, lane);
     Block<DIM, F32> w[NR];
     const int t = t0 + wave;
     int look[4] = {-1, -1, -1, -1};
@@ -515,7 +639,8 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n)
-            w[n].request(raw[n], a, at, pl.group, hk, row0 + 16 * n + lane % 16, position0);
+            w[n].request(raw[n], a, at, pl.group, hk, first + 16 * n + lane % 16, position0,
+                         g);
         if (t < t1) {
             int page[4];
 #pragma unroll
@@ -528,9 +653,14 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
 #pragma unroll
         for (int n = 0; n < NR; ++n) w[n].clear();
     }
-    int top = kNoExponent;
-    step_loop<DIM, F32, ONCE, NR>(w, f, r, t, t1, W, top_lo, mine, look, top,
-                                   finite(a.scale * kLog2e));
+    Span8 span;
+    step_loop<DIM, F32, ONCE, NR, APART>(w, f, r, t, t1, W, top_lo, mine, look, span,
+                                         finite(a.scale * kLog2e));
+    if (!APART && __builtin_expect(span.apart(), 0)) {
+        if (lane == 0) votes[wave] = 1;
+        __syncthreads();
+        return true;
+    }
     // join the waves
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -541,7 +671,14 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
             ml[1][wave][16 * n + lane] = w[n].l;
         }
     }
+    if (!APART && lane == 0) votes[wave] = 0;
     __syncthreads();
+    if (!APART) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) any |= votes[i];
+        if (__builtin_expect(uniform((int)any), 0)) return true;
+    }
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         const int rr = 16 * n + lane % 16;
@@ -549,7 +686,8 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
 #pragma unroll
         for (int i = 0; i < W; ++i) m = fmaxf(m, ml[0][i][rr]);
         const float fs = factor_of(w[n].m - (m == -INFINITY ? 0.0f : m));
-        if (rr < row1 - row0) {
+        if (rr < last - first) {
+            const int top = APART ? own_exponent(w[n].ref) : span.top;
             float *row = (float *)mine + rr * kPitch + 4 * g;
 #pragma unroll
             for (int d = 0; d < DIM / 16; ++d) {
@@ -562,7 +700,7 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < (row1 - row0) * (DIM / 4); e += 64 * W) {
+    for (int e = 64 * wave + lane; e < (last - first) * (DIM / 4); e += 64 * W) {
         const int rr = e / (DIM / 4), d = e % (DIM / 4) * 4;
         f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
         float m = -INFINITY, l = 0.0f;
@@ -575,13 +713,14 @@ __device__ __forceinline__ void step_tile(const AttentionArgs &a, const Plan &pl
             for (int x = 0; x < 4; ++x) o[x] += v[x];
             l += ml[1][i][rr] * factor_of(ml[0][i][rr] - (m == -INFINITY ? 0.0f : m));
         }
-        const int token = (row0 + rr) / pl.group;
+        const int token = (first + rr) / pl.group;
         const int64_t out = (int64_t)(at.first + token) * a.q_heads + hk * pl.group +
-                            (row0 + rr) % pl.group;
+                            (first + rr) % pl.group;
         if (pl.splits > 1 && d == 0) put_ml(a, pl, split, out, m, l);
         if (pl.splits > 1 && t0 >= t1) continue;
         put4<F32>(a, pl, split, out, DIM, d, o, l, position0 + token >= 0);
     }
+    return false;
 }
 
 // Tile `w` of up to 64 conversations, the longest first: the first tiles of all, then
@@ -622,21 +761,40 @@ __device__ __forceinline__ Place longest_first(const AttentionArgs &a, int group
 }
 
 // ONCE: a conversation's rows are one tile, most likely.
+template <bool ONCE> __device__ __forceinline__ Place step_place(const Call &c) {
+    const int w = c.base + (int)blockIdx.z;
+    return ONCE && c.a.batch <= 64 ? longest_first(c.a, c.pl.group, w)
+                                   : find_tile<kStepRows>(c.a, c.pl.group, w);
+}
+
 template <int DIM, bool F32, bool ONCE, int W>
-__global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(AttentionArgs a, Plan pl,
-                                                                         int base) {
+__global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Call c) {
     __shared__ __align__(1024) uint8_t lds[W * kStepRows * (DIM + 4) * 4];
     __shared__ float ml[2][W][kStepRows];
-    const int hk = blockIdx.x, split = blockIdx.y;
-    const Place at = ONCE && a.batch <= 64 ? longest_first(a, pl.group, base + blockIdx.z)
-                                           : find_tile<kStepRows>(a, pl.group, base + blockIdx.z);
-    const int row0 = at.tile * kStepRows;
-    if (row0 < 0 || row0 >= at.rows) return;
-    const int row1 = min(row0 + kStepRows, at.rows);
-    if (row1 - row0 <= 16)
-        step_tile<DIM, F32, ONCE, W, 1>(a, pl, at, hk, split, row0, row1, lds, ml);
-    else
-        step_tile<DIM, F32, ONCE, W, 2>(a, pl, at, hk, split, row0, row1, lds, ml);
+    __shared__ uint32_t votes[W];
+    const int hk = blockIdx.x, split = blockIdx.y, wave = uniform(threadIdx.x / 64);
+    {
+        const Place at = step_place<ONCE>(c);
+        const int row0 = at.tile * kStepRows;
+        if (row0 < 0 || row0 >= at.rows) return;
+        const int row1 = min(row0 + kStepRows, at.rows);
+        const bool apart =
+            row1 - row0 <= 16
+                ? step_tile<DIM, F32, ONCE, W, 1, false>(c.a, c.pl, at, hk, split, row0, row1,
+                                                         row0, row1, lds, ml, votes, wave)
+                : step_tile<DIM, F32, ONCE, W, 2, false>(c.a, c.pl, at, hk, split, row0, row1,
+                                                         row0, row1, lds, ml, votes, wave);
+        if (!apart) return;
+    }
+    const Call &again = call_again();
+    const Place at = step_place<ONCE>(again);
+    const int row0 = at.tile * kStepRows, row1 = min(row0 + kStepRows, at.rows);
+#pragma nounroll
+    for (int first = row0; first < row1; first += 16) {
+        __syncthreads();
+        step_tile<DIM, F32, ONCE, W, 1, true>(again.a, again.pl, at, hk, split, row0, row1, first,
+                                              min(first + 16, row1), lds, ml, votes, wave);
+    }
 }
 
 // ---- many rows: waves of 32 rows share each key tile ------------------------
@@ -666,7 +824,7 @@ template <int DIM, bool F32, int RW, int KW> struct Pass {
     static constexpr int kTile = KT * DIM * 2;
     static constexpr int kPitch = DIM + 4, kShare = 32 * kPitch * 4;
     static constexpr int kStages = KW * 4 * kTile;
-    static constexpr int kLds = KW > 1 && RW * KW * kShare > kStages ? RW * KW * kShare : kStages;
+    static constexpr int kLds = RW * KW * kShare > kStages ? RW * KW * kShare : kStages;
     static constexpr int kThreads = 64 * RW * KW;
     static constexpr int kWavesPerSimd = DIM > 128 ? 1 : 2;
 };
@@ -809,8 +967,9 @@ template <int DIM, bool F32> struct Rows {
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
         top = halves_max(top);
         if (__any(top * c > over)) {
+            // (rows that need not be lifted stay as they are, whatever the others do)
             const bool first = over == -INFINITY;
-            const float to = m + (first ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f));
+            const float to = top * c > over ? m + top : m;
             const float up = to - m;
             const float f = first ? 1.0f : factor_of(-up * c);
             if (top != -INFINITY) over = kLag;
@@ -916,11 +1075,20 @@ template <int DIM, bool F32> struct Total {
     }
 };
 
+// This workgroup's tile of R rows, those with the most keys first; false if it has none.
+template <int R> __device__ __forceinline__ bool pass_place(const Call &c, Place &at) {
+    at = find_tile<R>(c.a, c.pl.group, c.base + (int)blockIdx.z);
+    const int count = (at.rows + R - 1) / R;
+    if (at.tile < 0 || at.tile >= count) return false;
+    at.tile = count - 1 - at.tile;
+    return true;
+}
+
 template <int DIM, bool F32, int RW, int KW>
 __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
-                             (Pass<DIM, F32, RW, KW>::kWavesPerSimd)) void pass_kernel(AttentionArgs a,
-                                                                                  Plan pl,
-                                                                                  int base) {
+                             (Pass<DIM, F32, RW, KW>::kWavesPerSimd)) void pass_kernel(Call c) {
+    const AttentionArgs &a = c.a;
+    const Plan &pl = c.pl;
     using P = Pass<DIM, F32, RW, KW>;
     using W = Rows<DIM, F32>;
     constexpr bool kBoth = P::kBoth;
@@ -928,11 +1096,10 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
     __shared__ __align__(1024) uint8_t lds[P::kLds];
     __shared__ Scales<KT> scales[2][KW];
     __shared__ float ml[2][KW][R];
+    __shared__ uint32_t votes[KW];
     const int hk = blockIdx.x;
-    Place at = find_tile<R>(a, pl.group, base + blockIdx.z);
-    const int count = (at.rows + R - 1) / R;
-    if (at.tile < 0 || at.tile >= count) return;
-    at.tile = count - 1 - at.tile;  // the tiles with the most keys first
+    Place at;
+    if (!pass_place<R>(c, at)) return;
     const int position0 = at.kv - at.rows / pl.group;
     const int row0 = at.tile * R, row1 = min(row0 + R, at.rows);
     const int p0 = position(a, position0, row0 / pl.group);
@@ -973,7 +1140,7 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
         if (rw < 2) sx = *(const float *)f.scale(r, pages, k0 + lane % KT, rw == 0);
     };
     const float k_factor = F32 ? 1.0f : finite(a.scale * kLog2e);
-    int lifted = kNoExponent;  // the running exponent, of the wave that stages V's scales
+    Span8 span;  // of the wave that stages V's scales
     const auto stage = [&](int i) {
         uint8_t *dst = stages + (i & 1) * 2 * kTile + (kBoth || rw < KT / 16 ? 0 : kTile);
 #pragma unroll
@@ -990,10 +1157,9 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
         }
         Scales<KT> &sc = scales[i & 1][kw];
         if (rw == 0) {
-            const int e = exponent(sx);
-            if (__any(e > lifted)) lifted = max(wave_max(e), lifted);
-            if (lane < KT) sc.v[lane] = relative(sx, lifted, W::kShift);
-            if (lane == 0) sc.top = lifted;
+            span.take(sx);
+            if (lane < KT) sc.v[lane] = relative(sx, span.top, W::kShift);
+            if (lane == 0) sc.top = span.top;
         } else if (rw == 1 && lane < KT) {
             sc.k[lane] = fabsf(sx) <= FLT_MAX ? sx * k_factor : NAN;
         }
@@ -1028,6 +1194,31 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
         const uint8_t *kbuf = stages + (i & 1) * 2 * kTile;
         w.template step<KT>(kbuf, kbuf + kTile, sc, k0, !r.all(k0, KT, top_lo), r.sinks);
         if (i % kFold == kFold - 1 && tiles - i > kFold / 2) total.fold(w, top, i >= kFold);
+    }
+    // Scales too far apart for one exponent are asked for at the end alone (as soon as
+    // they are met, in the loop: attend both prompts in 329 us, so in 322).
+    if (rw == 0 && lane == 0) votes[kw] = span.apart();
+    __syncthreads();
+    uint32_t apart = 0;
+#pragma unroll
+    for (int i = 0; i < KW; ++i) apart |= votes[i];
+    if (__builtin_expect(uniform((int)apart), 0)) {
+        // 16 rows to a wave, which takes all keys
+        constexpr int kAll = RW * KW;
+        const Call &again = call_again();
+        Place at;
+        pass_place<R>(again, at);
+        const int row0 = at.tile * R, row1 = min(row0 + R, at.rows);
+#pragma nounroll
+        for (int x = 0; x < R / 16; x += kAll) {
+            const int first = row0 + 16 * (x + wave);
+            __syncthreads();
+            step_tile<DIM, F32, false, 1, 1, true>(
+                again.a, again.pl, at, blockIdx.x, 0, row0, row1, min(first, row1),
+                min(first + 16, row1), lds + wave * P::kShare,
+                (float(*)[1][kStepRows])(&ml[0][0][0] + wave * 2 * kStepRows), nullptr, 0);
+        }
+        return;
     }
     if (tiles >= kFold + kFold / 2) total.back(w, top);
     // the values' own magnitude again, the maximum in powers of two
@@ -1261,21 +1452,18 @@ hipError_t run(const AttentionArgs &a, const Choice &ch, const Plan &pl, hipStre
     for (int64_t base = 0; base < ch.tiles; base += 65535) {
         const int64_t tiles = ch.tiles - base < 65535 ? ch.tiles - base : 65535;
         const dim3 grid((uint32_t)a.cache.heads, (uint32_t)ch.splits, (uint32_t)tiles);
+        const Call c = {a, pl, (int)base};
         if (ch.rows == 128)
-            hipLaunchKernelGGL((pass_kernel<DIM, F32, 4, 1>), grid, dim3(256), 0, stream, a, pl,
-                               (int)base);
+            hipLaunchKernelGGL((pass_kernel<DIM, F32, 4, 1>), grid, dim3(256), 0, stream, c);
         else if (ch.rows == 64)
-            hipLaunchKernelGGL((pass_kernel<DIM, F32, 2, W>), grid, dim3(128 * W), 0, stream, a,
-                               pl, (int)base);
+            hipLaunchKernelGGL((pass_kernel<DIM, F32, 2, W>), grid, dim3(128 * W), 0, stream, c);
         else if (!ch.once)
-            hipLaunchKernelGGL((step_kernel<DIM, F32, false, W>), grid, dim3(64 * W), 0, stream, a,
-                               pl, (int)base);
+            hipLaunchKernelGGL((step_kernel<DIM, F32, false, W>), grid, dim3(64 * W), 0, stream, c);
         else if (ch.waves == W)
-            hipLaunchKernelGGL((step_kernel<DIM, F32, true, W>), grid, dim3(64 * W), 0, stream, a,
-                               pl, (int)base);
+            hipLaunchKernelGGL((step_kernel<DIM, F32, true, W>), grid, dim3(64 * W), 0, stream, c);
         else
             hipLaunchKernelGGL((step_kernel<DIM, F32, true, 2 * W>), grid, dim3(128 * W), 0,
-                               stream, a, pl, (int)base);
+                               stream, c);
     }
     const int64_t out = (int64_t)a.n * a.q_heads;
     // Parts of many rows are joined a wave to a row, of few by a workgroup each (whole

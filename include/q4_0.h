@@ -482,8 +482,10 @@ int q4_0_kv_read8(const q4_0_kv_cache8 *cache, const int64_t *slots, int64_t n, 
  * the same arguments, checks and limits.  Codes enter both products exactly; scales
  * multiply scores and weights in float32.  Binary16 x: the weights of passes
  * (q4_0_select_attention8: 64 and 128 rows) are rounded to binary16, else held in
- * two parts, as with float32 x.  Codes and scales that a row does not see never
- * change it. */
+ * two parts, as with float32 x; either is off, besides, by at most 2^-28 (rounded:
+ * 2^-21) of the row's largest weight times scale.  Codes and scales that a row does not
+ * see, whatever they are, change it by less than that.  Value scales of one head more
+ * than 2^10 apart make the call slower (steps to twice, passes to four times). */
 int q4_0_attention8(const q4_0_kv_cache8 *cache, const void *q, int64_t q_stride, int x_dtype,
                     int64_t q_heads, void *y, int64_t n, const int32_t *q_start,
                     const int32_t *kv_len, const int32_t *table, int64_t table_stride,

@@ -9,9 +9,9 @@ import pytest
 import torch
 
 import gemm_q4_amd as q4
-from oracle import step
-from test_gpu_block import DEV, dev
-from test_gpu_step import check_verify, drafts
+from oracle import block, step
+from test_gpu_block import DEV, H16, H32, dev, near
+from test_gpu_step import check_verify, drafts, i32, tol8
 from test_verify_host import faint_rows
 
 pytestmark = pytest.mark.gpu
@@ -80,3 +80,125 @@ def test_verify_the_largest_batch(modelled):
     rows[[0, 32767, 32768, 40000, 65535]] = 3
     logits, tokens, start, uniform, drafted = drafts(rng, rows, 23, False, modelled)
     check_verify(logits, tokens, start, uniform, drafted)
+
+
+# ---- attention over 8 bits: value scales far apart -----------------------------
+# (new tokens, keys), the rows of the tiles that take them, and (query, key/value) heads
+KINDS = [(2, 2, 32, (4, 2)), (5, 300, 32, (8, 2)), (40, 130, 32, (4, 2)), (400, 400, 64, (32, 16)),
+         (1100, 1100, 128, (32, 16))]
+
+
+def far_apart(new, kv, heads, dim, half, seed, spots, rest, window=0, sinks=0, page=64):
+    """One conversation whose values' scales are `rest`, but for those of keys `spots`
+    (key: scale); what the call gives and what it should, rows sampled."""
+    rng = np.random.default_rng([seed, new, dim])
+    hq, hk = heads
+    pages = (kv + page - 1) // page
+    kc, vc = (rng.integers(-127, 128, (pages, 1, page, dim)).astype(np.int8) for _ in range(2))
+    ks = (np.exp(0.3 * rng.standard_normal((pages, 1, page))) / 70).astype(np.float32)
+    vs = np.full((pages, 1, page), rest, np.float32)
+    for j, x in spots.items():
+        vs[j // page, 0, j % page] = x
+    table = np.arange(pages, dtype=np.int32)[None]
+    q = rng.standard_normal((new, 1, dim)).astype(np.float16 if half else np.float32)
+    wide = lambda a: dev(np.ascontiguousarray(np.repeat(a, hk, 1)))
+    cache = q4.kv_cache8(*(wide(a) for a in (kc, vc, ks, vs)))
+    tq = dev(np.ascontiguousarray(np.repeat(q, hq, 1)))
+    scale = dim ** -0.5
+    y = q4.attention(cache, tq, i32(0, new), i32(kv), dev(table), window, sinks, scale)
+    assert torch.equal(y[:, :1].expand(-1, hq, -1).isnan(), y.isnan())
+    rows = sorted({*range(0, new, max(1, new // 23)), *(j - (kv - new) + d for j in spots
+                                                         for d in (-1, 0, 1))} & set(range(new)))
+    numbers = step.numbers(kc, ks), step.numbers(vc, vs)
+    want = [block.attend(*numbers, q[t:t + 1], [0, 1], [kv - new + t + 1], table, window, sinks,
+                         scale) for t in rows]
+    return y[rows, :1], *(np.concatenate([w[i] for w in want]) for i in range(3))
+
+
+def near8(y, ref, absolute, score, keys, dim, half, rows):
+    """As tol8's, and what binary16 parts lose of a weight: half of their least step, where
+    the row's strongest key has 2^3 (2^-4 in passes of binary16 rows, one part), times the
+    codes.  The strongest key's largest code is above 100: the row's largest element
+    tells its share.  What does not fit binary16 is infinite."""
+    lost = 2.0 ** (-21 if half and rows > 32 else -28) * keys * 1.3
+    with np.errstate(invalid="ignore"):
+        ref = np.where(np.abs(ref) > 65504 * 1.0001, np.sign(ref) * np.inf, ref) if half else ref
+    fine = np.where(np.isfinite(ref), ref, 0.0)
+    tol = tol8(fine, absolute, score, keys, dim, half, 2.0 ** -25 if half else 1e-37)
+    near(y, ref, tol + lost * absolute.max(-1, keepdims=True))
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,kv,rows,heads", KINDS)
+def test_attention8_scales_that_a_row_does_not_see(new, kv, rows, heads, dim, half):
+    """A later token's values far larger than the others': rows before it are as if it
+    were not there, rows from it on as the definition has them."""
+    c = q4.q4_0_kv_cache8(0, 0, 0, 0, 1, heads[1], 64, dim)
+    assert q4.q4_0_select_attention8(c, heads[0], q4.F16 if half else q4.F32, new,
+                                     (kv + 63) // 64, 1) == rows
+    late = kv - 1 if new < 9 else kv - new + new * 2 // 3
+    for i, (rest, much) in enumerate([(1e-3, 2.0 ** 25 * 1e-5), (2.0 ** -9, 1e30), (1e-4, 0.2),
+                                      (1e-3, 1e36)] + ([] if half else [(1e-12, 1.0), (1e-30, 1e8)])):
+        y, *want = far_apart(new, kv, heads, dim, half, i, {late: much}, rest)
+        near8(y, *want, kv, dim, half, rows)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,kv,rows,heads", KINDS[1:])
+def test_attention8_scales_out_of_the_window(new, kv, rows, heads, dim, half):
+    """Far larger values that leave the window, and far smaller ones before them."""
+    spots = {0: 1e30, 7: 1e30, kv - new - 3: 1e25, kv - new // 2: 2e-9, kv - 2: 3e-7}
+    for window, sinks in ((20, 0), (64, 0), (20, 1)):
+        y, *want = far_apart(new, kv, heads, dim, half, 31, spots, 2.0 ** -9, window, sinks)
+        near8(y, *want, kv, dim, half, rows)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,kv,rows,heads", KINDS[1:] + [(1, 3000, 32, (4, 2))])
+def test_attention8_scales_of_every_magnitude(new, kv, rows, heads, dim, half):
+    """Scales of every key its own, over sixty powers of two (as far as binary16 rows
+    carry: thirty), rising, falling and mixed."""
+    rng = np.random.default_rng([41, dim])
+    bits = np.linspace(-33 if half else -45, -3 if half else 15, kv)
+    for order in (np.arange(kv), np.arange(kv)[::-1], rng.permutation(kv)):
+        spots = dict(enumerate(np.float32(2.0) ** bits[order]))
+        y, *want = far_apart(new, kv, heads, dim, half, 42, spots, 1.0)
+        near8(y, *want, kv, dim, half, rows)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("new,rows", [(1, 32), (2, 32), (900, 64)])
+@pytest.mark.parametrize("first", [False, True])
+def test_attention8_large_values_of_little_weight(first, new, rows, half):
+    """A key of weight 2^-30 with values 2^30 times the others' counts as much as they
+    do; of weight 2^-60 it is nothing; the strong keys are in other tiles, before or
+    after it."""
+    dim, kv, page, heads = 64, 700 if new < 9 else 1500, 64, 16
+    pages = (kv + page - 1) // page
+    for down in (30, 60):
+        kc = torch.zeros(pages, heads, page, dim, dtype=torch.int8, device=DEV)
+        vc = torch.ones_like(kc)
+        ks = torch.ones(pages, heads, page, device=DEV)
+        vs = torch.full_like(ks, 2.0 ** -20)
+        at = 3 if first else 300                       # seen by every row
+        kc[at // page, :, at % page, 0] = -1
+        vc[at // page, :, at % page] = 3
+        vs[at // page, :, at % page] = 2.0 ** 10
+        q = torch.zeros(new, heads, dim, dtype=torch.float16 if half else torch.float32, device=DEV)
+        q[:, :, 0] = down
+        c = q4.kv_cache8(kc, vc, ks, vs)
+        assert q4.q4_0_select_attention8(c, heads, q4.F16 if half else q4.F32, new, pages, 1) == rows
+        scale = float(np.float32(np.log(2.0)))
+        y = q4.attention(c, q, i32(0, new), i32(kv), torch.arange(pages, device=DEV).int()[None],
+                         scale=scale)
+        w = np.exp(-scale * down)
+        n = np.arange(kv - new, kv)
+        want = ((n * 2.0 ** -20 + 3 * 2.0 ** 10 * w) / (n + w))[:, None, None]
+        # scores of 60 at most, off by their roundings; a weight's (2^-12 in passes of binary16
+        # rows); sums of kv
+        steps = (60 * 8 + 2 * (kv + 18)) * H32 + (2 * H16 if half else 0.0) + 2.0 ** -22
+        near(y, np.broadcast_to(want, y.shape),
+             np.broadcast_to(want * steps + 2.0 ** -25 * half, y.shape))
