@@ -583,17 +583,24 @@ __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFi
                     p[n][0][e] = hi;
                     p[n][1][e] = (_Float16)(y - (float)hi);
                 }
+            // (two columns side by side: the two parts of one depend on each other)
 #pragma unroll
-            for (int d = 0; d < DIM / 16; ++d) {
-                const i2_t x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                    (lds_i2_t)(vrow + b * 32 * DIM + ((d ^ swz8<DIM>(vkey)) * 16)));
-                const h8_t a = codes8((uint32_t)x[0], (uint32_t)x[1]);
+            for (int d = 0; d < DIM / 16; d += 2) {
+                h8_t a[2];
 #pragma unroll
-                for (int n = 0; n < NR; ++n)
+                for (int i = 0; i < 2; ++i) {
+                    const i2_t x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                        (lds_i2_t)(vrow + b * 32 * DIM + (((d + i) ^ swz8<DIM>(vkey)) * 16)));
+                    a[i] = codes8((uint32_t)x[0], (uint32_t)x[1]);
+                }
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        w[n].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, p[n][y], w[n].o[d],
-                                                                           0, 0, 0);
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            w[n].o[d + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                a[i], p[n][y], w[n].o[d + i], 0, 0, 0);
             }
         }
         Q4_WAIT_LGKM0();
