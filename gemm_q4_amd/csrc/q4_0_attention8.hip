@@ -171,6 +171,42 @@ __device__ __forceinline__ float lifted_to(float &ref, float u, float most) {
     return __builtin_amdgcn_exp2f((float)(was - own_exponent(ref)) - u);
 }
 
+// Sums that took in many tiles: a faint weight's share would vanish in them (each is off
+// by half a step of the sum, and of 10^5 keys beside a strong one most would be lost).
+// So every kFold tiles of a wave, if half as many are left, they are put aside, in memory:
+// registers are few, and the way there is rare.  144 tokens of 89120 keys, float32:
+// off by 5e-7 so, by 3e-5 without; 320 of 131072 with heads of 256, 1024 tiles to a
+// wave, beside a strong key by 1.5e-5 and by 2.2e-4.  It takes 2 to 6% of such calls' time
+// (128 conversations of 131072 keys 5.48 ms instead of 5.17).  Every 32 tiles, passes over
+// 5000 keys would take 343 us instead of 316.
+constexpr int kFold = 64;
+typedef volatile __attribute__((address_space(5))) f4_t *private_f4_t;
+template <typename W> struct Total {
+    f4_t o[W::kQuads];
+    float l, m;
+    int top;
+    bool seen;
+    // now: the exponent of the sums; more: some were put aside before.
+    __device__ __forceinline__ void fold(W &w, int now, bool more) {
+        if (more) back(w, now);
+        const private_f4_t at = (private_f4_t)o;
+#pragma unroll
+        for (int i = 0; i < W::kQuads; ++i) at[i] = w.quad(i);
+        l = w.l, m = w.m, top = now, seen = w.over != -INFINITY;
+        w.l = 0.0f;
+        w.zero();
+    }
+    // What was put aside, brought to the maximum and the exponent now and added again.
+    __device__ __forceinline__ void back(W &w, int now) {
+        const float down = (m - w.m) * w.c;
+        const float f = seen ? __builtin_amdgcn_exp2f((float)(top - now) + down) : 0.0f;
+        if (seen) w.l += l * factor_of(down);
+        const private_f4_t at = (private_f4_t)o;
+#pragma unroll
+        for (int i = 0; i < W::kQuads; ++i) w.add(i, at[i], f);
+    }
+};
+
 // The cache as a tile's loads see it: head hk of the pages of conversation s.
 struct Source {
     const uint8_t *k, *v;  // codes of this head on page 0
@@ -318,8 +354,7 @@ template <int DIM, bool F32> struct Block {
         over = -INFINITY;
         ref = -kNever;
         l = 0.0f;
-#pragma unroll
-        for (int d = 0; d < DIM / 16; ++d) o[d] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        zero();
     }
     __device__ __forceinline__ void take(const Raw &raw) {
         if (!F32) {
@@ -350,6 +385,16 @@ template <int DIM, bool F32> struct Block {
     }
     __device__ __forceinline__ bool sees(int key, int sinks) const {
         return key <= p && (key >= lo || key < sinks);
+    }
+    static constexpr int kQuads = DIM / 16;  // of o
+    __device__ __forceinline__ f4_t quad(int i) const { return o[i]; }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int d = 0; d < DIM / 16; ++d) o[d] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __device__ __forceinline__ void add(int i, f4_t x, float f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = fmaf(x[e], f, o[i][e]);
     }
     __device__ __forceinline__ void rescale(float f) {
 #pragma unroll
@@ -428,8 +473,9 @@ template <int DIM, bool F32> struct Block {
 // One tile's room to a wave: K is requested again as soon as the scores are formed, V
 // as soon as it is mixed, and the other waves cover what that leaves open.
 // APART: every row has its own exponent.  Without, the loop ends early where scales lie too
-// far apart for one (span.apart()): what it leaves is of no use then.
-template <int DIM, bool F32, bool ONCE, int NR, bool APART>
+// far apart for one (span.apart()): what it leaves is of no use then.  FOLD: sums of many
+// tiles are put aside (which a wave of fewer than kFold + kFold / 2 never does).
+template <int DIM, bool F32, bool ONCE, int NR, bool APART, bool FOLD>
 __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFiller<DIM> &f,
                                           const Reach<kStepKeys> &r, int t, int t1, int stride,
                                           int top_lo, uint8_t *lds, int (&look)[4], Span8 &span,
@@ -445,7 +491,9 @@ __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFi
     float *ksc = (float *)(lds + 2 * kCodes);
     float *vsc = ksc + kStepKeys;
     int i = 0;  // the tile's lane in look
-    for (; t < t1; t += stride) {
+    Total<B> total[NR];
+    bool aside = false;
+    for (int count = 1; t < t1; t += stride, ++count) {
         const int k0 = r.key(t), next = r.key(t + stride);
         const bool more = t + stride < t1, masked = !r.all(k0, kStepKeys, top_lo);
         f4_t s[NR][4];
@@ -606,12 +654,25 @@ __device__ __forceinline__ void step_loop(Block<DIM, F32> (&w)[NR], const StepFi
         Q4_WAIT_LGKM0();
         asm volatile("" ::: "memory");
         if (more) f.template fill<ONCE>(r, page, next, lds, true);
+        if (FOLD && __builtin_expect(count % kFold == 0 && t1 - t > stride * (kFold / 2), 0)) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                total[n].fold(w[n], APART ? own_exponent(w[n].ref) : span.top, aside);
+            aside = true;
+            // (none of these between the copies that are counted)
+            Q4_WAIT_VMCNT(0);
+            asm volatile("" ::: "memory");
+        }
     }
+    if (__builtin_expect(aside, 0))
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+            total[n].back(w[n], APART ? own_exponent(w[n].ref) : span.top);
 }
 
 // Rows `first` to `last` (up to 16 NR) of the tile of rows row0 to row1, by W waves.  True
 // if the scales of a wave's keys lie too far apart (without APART): nothing is written.
-template <int DIM, bool F32, bool ONCE, int W, int NR, bool APART>
+template <int DIM, bool F32, bool ONCE, int W, int NR, bool APART, bool FOLD>
 __device__ __forceinline__ bool step_tile(const AttentionArgs &a, const Plan &pl, const Place &at,
                                           int hk, int split, int row0, int row1, int first,
                                           int last, uint8_t *lds, float (*ml)[W][kStepRows],
@@ -661,8 +722,8 @@ __device__ __forceinline__ bool step_tile(const AttentionArgs &a, const Plan &pl
         for (int n = 0; n < NR; ++n) w[n].clear();
     }
     Span8 span;
-    step_loop<DIM, F32, ONCE, NR, APART>(w, f, r, t, t1, W, top_lo, mine, look, span,
-                                         finite(a.scale * kLog2e));
+    step_loop<DIM, F32, ONCE, NR, APART, FOLD>(w, f, r, t, t1, W, top_lo, mine, look, span,
+                                               finite(a.scale * kLog2e));
     if (!APART && __builtin_expect(span.apart(), 0)) {
         if (lane == 0) votes[wave] = 1;
         __syncthreads();
@@ -774,7 +835,7 @@ template <bool ONCE> __device__ __forceinline__ Place step_place(const Call &c) 
                                    : find_tile<kStepRows>(c.a, c.pl.group, w);
 }
 
-template <int DIM, bool F32, bool ONCE, int W>
+template <int DIM, bool F32, bool ONCE, int W, bool FOLD>
 __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Call c) {
     __shared__ __align__(1024) uint8_t lds[W * kStepRows * (DIM + 4) * 4];
     __shared__ float ml[2][W][kStepRows];
@@ -787,10 +848,12 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Call c)
         const int row1 = min(row0 + kStepRows, at.rows);
         const bool apart =
             row1 - row0 <= 16
-                ? step_tile<DIM, F32, ONCE, W, 1, false>(c.a, c.pl, at, hk, split, row0, row1,
-                                                         row0, row1, lds, ml, votes, wave)
-                : step_tile<DIM, F32, ONCE, W, 2, false>(c.a, c.pl, at, hk, split, row0, row1,
-                                                         row0, row1, lds, ml, votes, wave);
+                ? step_tile<DIM, F32, ONCE, W, 1, false, FOLD>(c.a, c.pl, at, hk, split, row0,
+                                                               row1, row0, row1, lds, ml, votes,
+                                                               wave)
+                : step_tile<DIM, F32, ONCE, W, 2, false, FOLD>(c.a, c.pl, at, hk, split, row0,
+                                                               row1, row0, row1, lds, ml, votes,
+                                                               wave);
         if (!apart) return;
     }
     const Call &again = call_again();
@@ -799,8 +862,9 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Call c)
 #pragma nounroll
     for (int first = row0; first < row1; first += 16) {
         __syncthreads();
-        step_tile<DIM, F32, ONCE, W, 1, true>(again.a, again.pl, at, hk, split, row0, row1, first,
-                                              min(first + 16, row1), lds, ml, votes, wave);
+        step_tile<DIM, F32, ONCE, W, 1, true, FOLD>(again.a, again.pl, at, hk, split, row0, row1,
+                                                    first, min(first + 16, row1), lds, ml, votes,
+                                                    wave);
     }
 }
 
@@ -919,6 +983,22 @@ template <int DIM, bool F32> struct Rows {
     }
     __device__ __forceinline__ bool sees(int key, int sinks) const {
         return key <= p && (key >= lo || key < sinks);
+    }
+    static constexpr int kQuads = DIM / 8;  // of o
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+    }
+    __device__ __forceinline__ f4_t quad(int i) const {
+        const f16x_t &x = o[i / 4];
+        const int k = i % 4 * 4;
+        return f4_t{x[k], x[k + 1], x[k + 2], x[k + 3]};
+    }
+    __device__ __forceinline__ void add(int i, f4_t x, float f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i / 4][i % 4 * 4 + e] = fmaf(x[e], f, o[i / 4][i % 4 * 4 + e]);
     }
     __device__ __forceinline__ void rescale(float f) {
 #pragma unroll
@@ -1042,46 +1122,6 @@ template <int DIM, bool F32> struct Rows {
     }
 };
 
-// Sums that took in many tiles: a faint weight's share would vanish in them (each is off
-// by half a step of the sum, and of 10^5 keys beside a strong one most would be lost).
-// So every kFold tiles, if half as many are left, they are put aside, in memory:
-// registers are few, and the way there is rare.  144 tokens of 89120 keys, float32:
-// off by 5e-7 so, by 3e-5 without.  (Every 32 tiles: 5000 keys 343 us instead of 316.)
-constexpr int kFold = 64;
-template <int DIM, bool F32> struct Total {
-    volatile f4_t o[DIM / 8];
-    float l, m;
-    int top;
-    bool seen;
-    __device__ __forceinline__ void fold(Rows<DIM, F32> &w, int now, bool more) {
-        if (more) back(w, now);
-#pragma unroll
-        for (int d = 0; d < DIM / 32; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                o[4 * d + i / 4] = f4_t{w.o[d][i], w.o[d][i + 1], w.o[d][i + 2], w.o[d][i + 3]};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w.o[d][i + e] = 0.0f;
-            }
-        l = w.l, m = w.m, top = now, seen = w.over != -INFINITY;
-        w.l = 0.0f;
-    }
-    // What was put aside, brought to the maximum and the exponent now and added again.
-    __device__ __forceinline__ void back(Rows<DIM, F32> &w, int now) const {
-        const float f = seen ? factor_of((m - w.m) * w.c) : 1.0f;
-        const float fo = f * __builtin_amdgcn_ldexpf(1.0f, top - now);
-        w.l += l * f;
-#pragma unroll
-        for (int d = 0; d < DIM / 32; ++d) {
-            f4_t x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = o[4 * d + i];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w.o[d][i] = fmaf(x[i / 4][i % 4], fo, w.o[d][i]);
-        }
-    }
-};
-
 // This workgroup's tile of R rows, those with the most keys first; false if it has none.
 template <int R> __device__ __forceinline__ bool pass_place(const Call &c, Place &at) {
     at = find_tile<R>(c.a, c.pl.group, c.base + (int)blockIdx.z);
@@ -1171,7 +1211,7 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
             sc.k[lane] = fabsf(sx) <= FLT_MAX ? sx * k_factor : NAN;
         }
     };
-    Total<DIM, F32> total;
+    Total<W> total;
     int pages = -1;
     if (tiles > 0) {
         load(0, look(0));
@@ -1220,7 +1260,7 @@ __global__ __launch_bounds__((Pass<DIM, F32, RW, KW>::kThreads),
         for (int x = 0; x < R / 16; x += kAll) {
             const int first = row0 + 16 * (x + wave);
             __syncthreads();
-            step_tile<DIM, F32, false, 1, 1, true>(
+            step_tile<DIM, F32, false, 1, 1, true, true>(
                 again.a, again.pl, at, blockIdx.x, 0, row0, row1, min(first, row1),
                 min(first + 16, row1), lds + wave * P::kShare,
                 (float(*)[1][kStepRows])(&ml[0][0][0] + wave * 2 * kStepRows), nullptr, 0);
@@ -1364,6 +1404,7 @@ struct Choice {
     int64_t tiles;
     int splits;
     int least;  // key tiles of a part, at least
+    bool fold;  // a wave may take so many key tiles that their sums are put aside
     size_t part, bytes;  // workspace: bytes of the partial rows, and in all
 };
 
@@ -1395,6 +1436,7 @@ Choice choose(const AttentionArgs &a) {
     ch.waves = dim > 128 ? 2 : 4;
     ch.splits = ch.least = 1;
     ch.part = ch.bytes = 0;
+    ch.fold = true;
     if (ch.rows > 32) return ch;  // (such tiles fill three quarters of the device, or all)
     // the items that are likely to have work: not all tiles do
     const int64_t likely = (rows / 32 > a.batch ? rows / 32 : a.batch) * heads;
@@ -1446,9 +1488,22 @@ Choice choose(const AttentionArgs &a) {
     if (splits > room) splits = room;
     ch.splits = splits < 2 ? 1 : (int)splits;
     if (ch.splits == 1) ch.least = 1;
+    // Without that code one conversation of 448 keys takes 9.3 us, with it 9.6; 32 of 400 to
+    // 8192 with heads of 256 152 and 155.
+    const int64_t per = (most + ch.splits - 1) / ch.splits;
+    ch.fold = ((per > ch.least ? per : ch.least) + ch.waves - 1) / ch.waves >= kFold + kFold / 2;
     ch.part = ch.splits > 1 ? (size_t)ch.splits * (size_t)out * (size_t)dim * 4u : 0;
     ch.bytes = ch.splits > 1 ? ch.part + (size_t)ch.splits * (size_t)out * 8u : 0;
     return ch;
+}
+
+template <int DIM, bool F32, bool ONCE, int W>
+void launch_step(const Call &c, const dim3 &grid, bool fold, hipStream_t stream) {
+    if (fold)
+        hipLaunchKernelGGL((step_kernel<DIM, F32, ONCE, W, true>), grid, dim3(64 * W), 0, stream, c);
+    else
+        hipLaunchKernelGGL((step_kernel<DIM, F32, ONCE, W, false>), grid, dim3(64 * W), 0, stream,
+                           c);
 }
 
 template <int DIM, bool F32>
@@ -1465,12 +1520,11 @@ hipError_t run(const AttentionArgs &a, const Choice &ch, const Plan &pl, hipStre
         else if (ch.rows == 64)
             hipLaunchKernelGGL((pass_kernel<DIM, F32, 2, W>), grid, dim3(128 * W), 0, stream, c);
         else if (!ch.once)
-            hipLaunchKernelGGL((step_kernel<DIM, F32, false, W>), grid, dim3(64 * W), 0, stream, c);
+            launch_step<DIM, F32, false, W>(c, grid, ch.fold, stream);
         else if (ch.waves == W)
-            hipLaunchKernelGGL((step_kernel<DIM, F32, true, W>), grid, dim3(64 * W), 0, stream, c);
+            launch_step<DIM, F32, true, W>(c, grid, ch.fold, stream);
         else
-            hipLaunchKernelGGL((step_kernel<DIM, F32, true, 2 * W>), grid, dim3(128 * W), 0,
-                               stream, c);
+            launch_step<DIM, F32, true, 2 * W>(c, grid, ch.fold, stream);
     }
     const int64_t out = (int64_t)a.n * a.q_heads;
     // Parts of many rows are joined a wave to a row, of few by a workgroup each (whole

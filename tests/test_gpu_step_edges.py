@@ -202,3 +202,47 @@ def test_attention8_large_values_of_little_weight(first, new, rows, half):
         steps = (60 * 8 + 2 * (kv + 18)) * H32 + (2 * H16 if half else 0.0) + 2.0 ** -22
         near(y, np.broadcast_to(want, y.shape),
              np.broadcast_to(want * steps + 2.0 ** -25 * half, y.shape))
+
+
+# ---- attention over 8 bits: sums of many keys ------------------------------------
+LONG = [  # conversations, new tokens of each, query and key/value heads, dim, keys
+    (1, 320, 32, 8, 256, 131072), (1, 320, 32, 8, 128, 131072), (128, 1, 8, 8, 64, 131072),
+    (48, 1, 32, 8, 256, 131072), (48, 3, 8, 8, 128, 131072), (128, 1, 8, 8, 128, 131072),
+    (128, 1, 8, 8, 256, 131072)]
+
+
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("batch,new,hq,hk,dim,keys", LONG)
+def test_attention8_sums_of_unsplit_contexts(batch, new, hq, hk, dim, keys, apart):
+    """Calls that fill the device without cutting the key axis: a wave takes hundreds of
+    tiles.  One strong key of weight 1 and value 1 among others of weight 2^-28.46 and value
+    -1: 32 of them, what one product adds, are 1.45 steps of the sum beside it.
+    apart: one key's value scale far below the others', so that rows have their own
+    exponents."""
+    page, gap = 256, 28.46
+    pages = (keys + page - 1) // page
+    kc = torch.zeros(pages, hk, page, dim, dtype=torch.int8, device=DEV)
+    vc = torch.full_like(kc, -1)
+    kc[0, :, 5, 0], vc[0, :, 5] = 127, 1
+    one = torch.ones(pages, hk, page, device=DEV)
+    vs = one.clone()
+    if apart:
+        vs[1, :, 7] = 2.0 ** -30                       # (a key less of 10^5)
+    q = torch.zeros(batch * new, hq, dim, device=DEV)
+    q[:, :, 0] = gap / np.log2(np.e) / 127
+    c = q4.kv_cache8(kc, vc, one, vs)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).expand(batch, pages).contiguous()
+    call = (hq, q4.F32, batch * new, pages, batch)
+    assert q4.q4_0_select_attention8(c, *call) == 32
+    assert q4.q4_0_attention8_workspace_size(c, *call) == 0
+    start = torch.arange(0, batch * new + 1, new, dtype=torch.int32, device=DEV)
+    y = q4.attention(c, q, start, torch.full((batch,), keys, dtype=torch.int32, device=DEV), table,
+                     scale=1.0).double()
+    weight = np.exp(-127 * float(q[0, 0, 0]))
+    n = torch.arange(keys - new, keys, dtype=torch.float64, device=DEV).repeat(batch)
+    want = ((1 - weight * (n - int(apart))) / (1 + weight * n))[:, None, None]
+    # beside the strong key's, at most 96 tiles of 64 keys: four products (32 keys, two parts)
+    # and a sum, each off by half a step of 1 at most; a weight, 2^-15.5 with the strong key's
+    # at 2^13, is off by half a step of the least numbers, 2^-25; the gap's own rounding
+    tol = (96 * 5 + 24 + 2 * gap) * H32 + weight * keys * (2.0 ** -9.5 + 2 * gap * H32)
+    assert (y - want).abs().max() < tol < weight * keys / 4
