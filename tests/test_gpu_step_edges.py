@@ -246,3 +246,33 @@ def test_attention8_sums_of_unsplit_contexts(batch, new, hq, hk, dim, keys, apar
     # at 2^13, is off by half a step of the least numbers, 2^-25; the gap's own rounding
     tol = (96 * 5 + 24 + 2 * gap) * H32 + weight * keys * (2.0 ** -9.5 + 2 * gap * H32)
     assert (y - want).abs().max() < tol < weight * keys / 4
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("gap", [3.0, 14.0, 18.0])
+def test_attention8_faint_weights_of_a_split_context(gap, half):
+    """One strong key and 40000 of weight e^-gap, one token, the key axis in parts: their
+    sum has to survive, within bounds that a call which loses it misses."""
+    n, dim, page, pages = 40001, 64, 256, 160
+    kc, vc = (torch.zeros(pages, 1, page, dim, dtype=torch.int8, device=DEV) for _ in range(2))
+    ks, vs = (torch.full((pages, 1, page), x, device=DEV) for x in (8.0 / 127, 1.0 / 64))
+    kc[0, 0, 0, 0] = 127
+    vc[:, 0, :, 1] = 64
+    vc[0, 0, 0, 1] = -64
+    q = torch.zeros(1, 2, dim, dtype=torch.float16 if half else torch.float32, device=DEV)
+    q[:, :, 0] = gap
+    c = q4.kv_cache8(kc, vc, ks, vs)
+    dtype = q4.F16 if half else q4.F32
+    assert q4.q4_0_attention8_workspace_size(c, 2, dtype, 1, pages, 1) > 0
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    y = q4.attention(c, q, i32(0, 1), i32(n), table, scale=0.125)
+    score = float(ks[0, 0, 0]) * 127 * 0.125 * gap
+    faint = (n - 1) * np.exp(-score)
+    want = (faint - 1.0) / (faint + 1.0)
+    # beside the strong key's: the tiles of one wave (628 in all, over four waves at least of
+    # eleven parts at least: 15), four products and a sum each; eight waves and 256 parts
+    # joined; a score of `gap` and its weight, two parts
+    tol = (15 * 5 + 8 + 256 + 24 + 4 * gap) * H32 + 2.0 ** -21 + H16 * abs(want) * half
+    assert abs(want - -1.0) > 2 * tol                  # the result without any of them
+    assert (y[0, :, 1].double() - want).abs().max() < tol
+    assert (y[0, :, 2:] == 0).all()
