@@ -276,3 +276,52 @@ def test_attention8_faint_weights_of_a_split_context(gap, half):
     assert abs(want - -1.0) > 2 * tol                  # the result without any of them
     assert (y[0, :, 1].double() - want).abs().max() < tol
     assert (y[0, :, 2:] == 0).all()
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news,kvs,hq,hk", [((1, 3, 5), (700, 90, 333), 8, 2),
+                                            ((150, 1, 90), (150, 40, 300), 32, 16),
+                                            ((900, 260), (900, 300), 32, 16)])
+def test_attention8_captured_calls_take_either_way(news, kvs, hq, hk, dim, half):
+    """A captured call whose cache gets scales far apart between replays, in one
+    conversation: that one's rows as the definition has them, the others' bits as they
+    were; and back again."""
+    page, rng = 32, np.random.default_rng([51, dim])
+    widths = [(kv + page - 1) // page for kv in kvs]
+    kc, vc = (rng.integers(-127, 128, (sum(widths), hk, page, dim)).astype(np.int8) for _ in range(2))
+    ks, vs = ((np.exp(0.3 * rng.standard_normal((sum(widths), hk, page))) / 70).astype(np.float32)
+              for _ in range(2))
+    table = np.zeros((len(kvs), max(widths)), np.int32)
+    for s, w in enumerate(widths):
+        table[s, :w] = sum(widths[:s]) + np.arange(w)
+    start = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    q = rng.standard_normal((start[-1], hq, dim)).astype(np.float16 if half else np.float32)
+    tvs, tq = dev(vs), dev(q)
+    y, ws = torch.empty_like(tq), torch.empty(q4.WORKSPACE_MAX, dtype=torch.uint8, device=DEV)
+    call = (q4.kv_cache8(dev(kc), dev(vc), dev(ks), tvs), tq, dev(start),
+            dev(np.array(kvs, np.int32)), dev(table))
+    usual = q4.attention(*call)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q4.attention(*call, y=y, ws=ws)
+    far = vs.copy()
+    far[table[0, widths[0] // 2], :, 7] *= np.float32(2.0 ** -20)
+    far[table[0, widths[0] - 1], :, (kvs[0] - 1) % page] *= np.float32(2.0 ** (8 if half else 30))
+    for k in range(4):
+        tvs.copy_(dev(far if k % 2 else vs))
+        y.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        n = start[1]
+        assert torch.equal(y[n:], usual[n:])
+        if k % 2 == 0:
+            assert torch.equal(y, usual)
+            continue
+        assert torch.equal(y, q4.attention(*call))
+        for t in {0, 1, n // 2, n - 2, n - 1} & set(range(n)):
+            at = [np.ascontiguousarray(a[:, :1]) for a in (kc, vc, ks, far)]
+            numbers = step.numbers(at[0], at[2]), step.numbers(at[1], at[3])
+            want = block.attend(*numbers, q[t:t + 1, :1], [0, 1], [kvs[0] - n + t + 1], table[:1], 0,
+                                0, dim ** -0.5)
+            near8(y[t:t + 1, :1], *want, kvs[0], dim, half, 33 if max(news) > 64 else 32)
