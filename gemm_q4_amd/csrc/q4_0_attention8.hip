@@ -24,8 +24,7 @@
 // no row of a tile sees are taken as 0 and their codes are finite whatever they are, so
 // what a page holds past its conversation's end never meets the arithmetic.  (One key
 // half way with a scale 2^12 below the others': 64 conversations 191 us instead of 101,
-// prompts 1075 instead of 320; a loop that keeps every row's own exponent at all times
-// would take half as many instructions again.)
+// prompts 1075 instead of 321.)
 //
 // A score is formed less the running maximum, by one fused operation on its product:
 // scores of any size lose nothing, and while the maximum holds its exponential
@@ -33,11 +32,11 @@
 // the factor, the same for all rows); float32 rows have a factor `c` of their own.
 //
 // Measured (32 + 8 heads of 128, binary16 rows but for the first; rates of the bytes or
-// operations that the call cannot do without): one conversation of 448 keys 9.4 us, a
+// operations that the call cannot do without): one conversation of 448 keys 9.2 us, a
 // chain of lengths, page table, keys and the join of the waves; of 131072 keys 52 us, 5.3
 // TB/s (over binary16 91 us); 64 conversations of 470 to 8192 keys, one to four tokens
-// each, 99 us, 5.9 TB/s (185 us over binary16 with a token each); the last 2438 of 5001
-// tokens beside a prompt of 3146 318 us, 730 TFLOP/s.
+// each, 100 us, 5.8 TB/s (185 us over binary16 with a token each); the last 2438 of 5001
+// tokens beside a prompt of 3146 321 us, 722 TFLOP/s.
 #include "q4_0_attention.h"
 #include "q4_0_dma.h"
 
@@ -874,10 +873,13 @@ __global__ __launch_bounds__(64 * W, DIM > 128 ? 1 : 2) void step_kernel(Call c)
 // on its way into LDS: its codes are loaded to registers a tile ahead, written to
 // the other of two stages while this one is worked on, and read there by all RW
 // waves.  Both products are v_mfma_f32_32x32x16_f16 on transposed scores; weights of
-// binary16 rows are rounded once, of float32 rows held in two parts.
+// float32 rows are held in two parts, those of binary16 rows rounded to one, as the
+// result is: prompts of 2438 of 5001 and 3146 tokens are off by 2.9e-4 of their norm,
+// with two parts by 2.1e-4 (the result's own rounding), but those take 403 us instead
+// of 321, and full prompts of both lengths 491 instead of 384.
 //
-// Bound by vector instructions, 360 to 64 keys of 32 rows, of which 32 exponentials take
-// four times as long; they hardly overlap with the matrix cores (busy for 31% of the
+// Bound by vector instructions, 370 to 64 keys of 32 rows, of which 32 exponentials take
+// four times as long; they hardly overlap with the matrix cores (busy for 33% of the
 // cycles) at two waves to a SIMD, where waits for LDS and barriers take the rest;
 // priorities change nothing (316 to 326 us).  What brought them down: codes converted
 // once for all waves (they were half of the instructions when each wave converted its

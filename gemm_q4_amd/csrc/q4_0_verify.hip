@@ -21,8 +21,8 @@
 // Measured: one conversation of four picked drafts over 151936 tokens 8.3 us, a chain of
 // two launches; 12 conversations of up to three drafts over 32003 tokens 14 us, a
 // chain of three; 64 conversations of up to six drafts over 151936 tokens (318 MB that
-// stats has to read) 79 us, of which stats 60: ten operations of 64 bits and five
-// others an element, 71% of its time, where the bytes alone are 44 us.
+// stats has to read) 80 us, of which stats 61: ten operations of 64 bits and five
+// others an element, 70% of its time, where the bytes alone are 44 us.
 #include <float.h>
 
 #include "q4_0_device.h"

@@ -549,7 +549,9 @@ int q4_0_embed(const void *packed, const int32_t *tokens, int64_t n, int64_t out
  * or nothing else than minus infinities, is no distribution: reached, it (or its
  * row of `drafted`) ends the step there with next -1.
  * Weights and their sums are float64, so that the order of summation decides no
- * token; a weight below 2^-980 of its row's largest counts as none.  1 <= n, batch <= Q4_0_MAX_N, 1 <= vocab <= Q4_0_MAX_OUT; sizes whose
+ * token.  A weight is off by 2e-13 of itself at most, so a number that close to the
+ * border between two tokens may take either; one below 2^-980 of its row's largest
+ * counts as none.  1 <= n, batch <= Q4_0_MAX_N, 1 <= vocab <= Q4_0_MAX_OUT; sizes whose
  * workspace would pass Q4_0_WORKSPACE_MAX: Q4_0_EUNSUPPORTED.  */
 int q4_0_verify(const void *logits, int64_t stride, const void *drafted, int64_t drafted_stride,
                 int x_dtype, int64_t vocab, const int32_t *tokens, const int32_t *q_start,
